@@ -358,6 +358,93 @@ int qz_local_search(const float* H, const void* W_hat, int32_t wt, int64_t d_o, 
                     uint8_t* codes, int32_t max_steps, int32_t* moves_host,
                     int32_t* steps_host, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------- microscaled 4-bit weights (MX4) --
+ * A second storage format beside the integer codes: 4-bit floating-point elements with a
+ * power-of-two factor per 32 columns (the OCP microscaling format MXFP4), which the matrix
+ * cores of gfx950 read as it is.  A row of `cols` columns is cut into
+ * G = qz_mx4_blocks(cols) = ceil(cols / 32) blocks of 32 consecutive columns:
+ *   codes   [rows x 16 G] u8: E2M1 codes, two a byte, the even column in the low nibble;
+ *           code = sign << 3 | magnitude code, magnitudes 0, 1/2, 1, 3/2, 2, 3, 4, 6.
+ *           Columns past `cols` in the last block hold zero codes.  16-byte aligned.
+ *   scales  [rows x G] u8: E8M0, E stands for 2^(E - 127); 255 makes the block NaN.
+ * Weights of several experts are the rows of one matrix after another.
+ *
+ * qz_mx4_quantize: round-to-nearest onto this format (the counterpart of qz_rtn).  Per block
+ * with largest magnitude a:
+ *   rule QZ_MX4_FLOOR   E = max(floor(log2 a) - 2 + 127, 0): a lies in [4, 8) 2^(E-127) and
+ *                       what exceeds 6 saturates;
+ *   rule QZ_MX4_LEAST   E or E + 1, whichever has the smaller sum of h_j (w_j - q_j)^2 over the
+ *                       block (64-bit sums; equal: E; E too where the larger factor would
+ *                       round an element to 2^128).  h = colw [cols] fp32 (nullable: ones;
+ *                       nonnegative), for instance diag(H) of qz_build_hessian.
+ * Elements round to the nearest code, ties to the even code; the sign of a zero is kept.  A
+ * block with a NaN or an infinity gets E = 255 and zero codes.  A zero block gets E = 0.
+ *   W       [rows x cols], dtype wt, row stride ldw >= cols elements.
+ *   values  nullable: [rows x cols] dense, dtype wt: what the codes stand for (exact in both
+ *           types), in the same pass.  Must not overlap W.
+ * Asynchronous, no workspace; activations are quantized by the same call.
+ *
+ * qz_mx4_unpack: the same numbers in the form of qz_objective_i32: out [rows x cols] int32 =
+ * 2 x element value, out_scales [rows x G] fp32 = 2^(E - 128) (NaN for 255), zeros [rows x G]
+ * u8 = 0; group size 32 (qz_objective_i32 needs cols % 32 == 0).  Asynchronous.            */
+#define QZ_MX4_FLOOR 0
+#define QZ_MX4_LEAST 1
+int64_t qz_mx4_blocks(int64_t cols);   /* -1 for cols < 1 */
+int qz_mx4_quantize(const void* W, int32_t wt, int64_t rows, int64_t cols, int64_t ldw,
+                    int32_t rule, const float* colw, uint8_t* codes, uint8_t* scales, void* values,
+                    hipStream_t stream);
+int qz_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                  int32_t* out, float* out_scales, uint8_t* zeros, hipStream_t stream);
+
+/* Products with MX4 weights, Y = X W^T + bias (W [d_o x d_i] as codes and scales):
+ *   qz_mx4_linear: X [n x d_i] bf16 (xt = QZ_BF16), row stride ldx >= d_i; weights are widened
+ *     exactly, products and sums in fp32.
+ *   qz_mx4_matmul: X [n x d_i] in MX4 too (from qz_mx4_quantize).
+ *   bias [d_o] fp32, nullable.  Y [n x d_o], dtype yt (QZ_BF16 or QZ_F32), row stride ldy >= d_o
+ *   (elements between the rows are left alone); rounded once.  Must not overlap the inputs.
+ *   Rows of X that are not whole blocks on 16-byte boundaries (d_i % 32, ldx % 8, the
+ *   address) are first copied to the workspace.
+ *   n <= 2^20, d_o <= 2^24, d_i <= 2^24; n = 0 or d_o = 0 does nothing.
+ *   ws: qz_mx4_*_workspace(n, d_o, d_i) bytes, 256-byte aligned (0 bytes: may be null; 0 for
+ *   bad sizes); calls that may overlap need different workspaces.  Asynchronous.          */
+size_t qz_mx4_linear_workspace(int64_t n, int64_t d_o, int64_t d_i);
+int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8_t* codes,
+                  const uint8_t* scales, int64_t d_o, int64_t d_i, const float* bias, void* Y,
+                  int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t qz_mx4_matmul_workspace(int64_t n, int64_t d_o, int64_t d_i);
+int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, const uint8_t* codes,
+                  const uint8_t* scales, int64_t d_o, int64_t d_i, const float* bias, void* Y,
+                  int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* qz_mx4_moe: a routed expert layer on MX4 weights for few tokens (decoding).  Per token x:
+ *   logits = router x (64-bit sums); the top_k experts by descending logit, ties to the lower
+ *   index (a NaN logit counts as -inf); p = softmax over all experts, with QZ_MOE_RENORM
+ *   divided by the sum over the chosen ones;
+ *   y = sum_r p_r W_down[e_r] (silu(g) * u), [g; u] = W_gate_up[e_r] x.
+ *   X [n x d] bf16 (xt = QZ_BF16), row stride ldx >= d; router [n_experts x d] dtype rt.
+ *   gu_codes/gu_scales: [n_experts x 2 f x d], gate rows before up rows; dn_codes/dn_scales:
+ *   [n_experts x d x f].  Y [n x d] bf16.  ids [n x top_k] int32 and weights [n x top_k] fp32
+ *   (nullable): the routing.  Sums in fp32; the hidden vector is kept to 16 bits of mantissa.
+ *   1 <= n_experts <= 256, top_k <= 16, n <= 1024 (more tokens: qz_mx4_linear per expert).
+ *   ws: qz_mx4_moe_workspace(...) bytes, 256-byte aligned; calls that may overlap need
+ *   different workspaces.  Asynchronous.                                                  */
+#define QZ_MOE_RENORM 0x1u
+#define QZ_MOE_MAX_EXPERTS 256
+#define QZ_MOE_MAX_TOP_K 16
+#define QZ_MOE_MAX_TOKENS 1024
+typedef struct {
+  uint32_t struct_size;   /* sizeof(qz_moe) */
+  int32_t n_experts;
+  int32_t top_k;
+  uint32_t flags;         /* QZ_MOE_RENORM */
+} qz_moe;
+size_t qz_mx4_moe_workspace(int64_t n, int64_t d, int64_t f, const qz_moe* params);
+int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int64_t f,
+               const qz_moe* params, const void* router, int32_t rt, const uint8_t* gu_codes,
+               const uint8_t* gu_scales, const uint8_t* dn_codes, const uint8_t* dn_scales,
+               void* Y, int32_t* ids, float* weights, void* ws, size_t ws_bytes,
+               hipStream_t stream);
+
 /* ----------------------------------------------------------------- timing --
  * Per-kernel timing for measurement tools: while enabled, the library records a
  * HIP event pair around each of its kernel launches, on the stream the kernel
@@ -367,7 +454,7 @@ int qz_local_search(const float* H, const void* W_hat, int32_t wt, int64_t d_o, 
  *   QZ_TIMING_KINDS) (host arrays, may be NULL), waits for the recorded events
  *   (SYNC), then, if reset != 0, drops the records.  Returns the number of kinds.
  *   qz_timing_kind_name(k) names kind k ("" when out of range).              */
-#define QZ_TIMING_KINDS 16
+#define QZ_TIMING_KINDS 21
 int qz_timing_enable(int on);
 int qz_timing_read(int64_t* launches, double* total_ms, int max_kinds, int reset);
 const char* qz_timing_kind_name(int kind);

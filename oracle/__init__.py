@@ -28,4 +28,4 @@ IEEE fp32 here, see oracle.grid).
 Functions whose results have no independent pin say "parity unpinned" in their
 docstring.
 """
-from . import grid, pack, hessian, gptq, admm, lattice, objective  # noqa: F401
+from . import grid, pack, hessian, gptq, admm, lattice, mx4, objective  # noqa: F401

@@ -15,7 +15,8 @@ import ctypes as C
 from . import _lib
 from ._lib import (QZ_ADMM_DUAL_NO_RESCALE, QZ_ADMM_REFRESH_FROM_Z, QZ_ADMM_REFRESH_UNCLAMPED,  # noqa: F401
                    QZ_ADMM_WARM_START, QZ_BF16, QZ_F32, QZ_GRID_CALLER, QZ_H_ACCUMULATE,
-                   QZ_H_NO_FINALIZE, QzAdmm, QzGrid)
+                   QZ_H_NO_FINALIZE, QZ_MOE_RENORM, QZ_MX4_FLOOR, QZ_MX4_LEAST, QzAdmm, QzGrid,
+                   QzMoe)
 
 
 class QzError(RuntimeError):
@@ -354,6 +355,194 @@ def qz_unpack(words, cols, bits):
     out = torch.empty((rows, cols), dtype=torch.uint8, device=words.device)
     _check(lib().qz_unpack(_ptr(words), rows, cols, int(bits), _ptr(out), _stream()))
     return out
+
+
+# ------------------------------------------------------------- microscaled 4-bit weights
+def _rows(t, name, dtypes):
+    """A 2-D GPU tensor of one of `dtypes` whose rows are contiguous: (pointer, row stride)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    if t.shape[0] <= 1:   # the stride of a single row is of no meaning
+        return t.data_ptr(), t.shape[1]
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), t.stride(0)
+
+
+def _mx4_pair(codes, scales, rows, cols, name, device):
+    """Checks that codes and scales store matrices of the given total rows and columns."""
+    torch = _torch()
+    blocks = -(-cols // 32)
+    for t, width, what in ((codes, 16 * blocks, "codes"), (scales, blocks, "scales")):
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name} {what} must be uint8")
+        if t.device != device or not t.is_contiguous():
+            raise ValueError(f"{name} {what} must be contiguous and on {device}")
+        if t.numel() != rows * width or t.shape[-1] != width:
+            raise ValueError(f"{name} {what}: expected {rows} rows of {width} bytes")
+
+
+def _on(device, *others):
+    """The raw current stream of `device`, where all `others` (or None) have to live too.  The
+    call itself runs with that device current."""
+    torch = _torch()
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {t.device} and {device} in one call")
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(device, fn, *args):
+    torch = _torch()
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args))
+
+
+def _vector(t, n, name, device):
+    if t is None:
+        return None
+    if t.dtype != _torch().float32:
+        raise TypeError(f"{name} must be fp32")
+    if t.device != device or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values on {device}")
+    return t.data_ptr()
+
+
+def qz_mx4_blocks(cols) -> int:
+    return lib().qz_mx4_blocks(cols)
+
+
+def qz_mx4_quantize(W, rule="floor", colw=None, values=False):
+    """Round a matrix (bf16 or fp32, contiguous rows) to MX4: (codes [rows x 16 G] uint8, scales
+    [rows x G] uint8), and with values=True the numbers they stand for in W's dtype.  rule
+    "floor", or "least" (the better of two factors per block under the column weights colw)."""
+    torch = _torch()
+    ptr, ld = _rows(W, "W", (torch.bfloat16, torch.float32))
+    rows, cols = W.shape
+    if cols < 1:
+        raise ValueError("W has no columns")
+    k = {"floor": _lib.QZ_MX4_FLOOR, "least": _lib.QZ_MX4_LEAST}[rule]
+    dev, blocks = W.device, -(-cols // 32)
+    stream = _on(dev)
+    codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=dev)
+    scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
+    out = torch.empty((rows, cols), dtype=W.dtype, device=dev) if values else None
+    _call(dev, lib().qz_mx4_quantize, ptr, _dtype_code(W), rows, cols, ld, k,
+          _vector(colw, cols, "colw", dev), codes.data_ptr(), scales.data_ptr(),
+          out.data_ptr() if values else None, stream)
+    return (codes, scales, out) if values else (codes, scales)
+
+
+def qz_mx4_unpack(codes, scales, cols):
+    """(codes int32, scales fp32, zeros uint8): the stored matrix in qz_objective's form (group
+    size 32)."""
+    torch = _torch()
+    _dev(codes, "codes")
+    rows, dev = codes.shape[0], codes.device
+    _mx4_pair(codes, scales, rows, cols, "MX4", dev)
+    out = torch.empty((rows, cols), dtype=torch.int32, device=dev)
+    s = torch.empty(scales.shape, dtype=torch.float32, device=dev)
+    z = torch.empty(scales.shape, dtype=torch.uint8, device=dev)
+    _call(dev, lib().qz_mx4_unpack, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
+          s.data_ptr(), z.data_ptr(), _on(dev))
+    return out, s, z
+
+
+def _product_out(out, n, d_o, dtype, device):
+    torch = _torch()
+    if out is None:
+        out = torch.empty((n, d_o), dtype=dtype or torch.bfloat16, device=device)
+    elif tuple(out.shape) != (n, d_o) or (dtype is not None and out.dtype != dtype):
+        raise ValueError(f"out must be [{n} x {d_o}]" + (f" {dtype}" if dtype is not None else ""))
+    ptr, ld = _rows(out, "out", (torch.bfloat16, torch.float32))
+    return out, ptr, max(ld, d_o)
+
+
+def qz_mx4_linear_workspace(n, d_o, d_i) -> int:
+    return lib().qz_mx4_linear_workspace(n, d_o, d_i)
+
+
+def qz_mx4_linear(X, codes, scales, bias=None, out_dtype=None, out=None, ws=None):
+    """Y = X W^T + bias for X bf16 [n x d_i] (contiguous rows) and W [d_o x d_i] in MX4.  Y is
+    out_dtype (bf16 or fp32; default bf16), or `out` is written."""
+    torch = _torch()
+    ptr, ldx = _rows(X, "X", (torch.bfloat16,))
+    (n, d_i), d_o, dev = X.shape, codes.shape[0], X.device
+    _mx4_pair(codes, scales, d_o, d_i, "W", dev)
+    stream = _on(dev, out, ws)
+    out, yp, ldy = _product_out(out, n, d_o, out_dtype, dev)
+    if ws is None:
+        ws = _workspace(lib().qz_mx4_linear_workspace(n, d_o, d_i), dev)
+    _call(dev, lib().qz_mx4_linear, ptr, _lib.QZ_BF16, n, ldx, codes.data_ptr(), scales.data_ptr(),
+          d_o, d_i, _vector(bias, d_o, "bias", dev), yp, _dtype_code(out), ldy, ws.data_ptr(),
+          ws.numel(), stream)
+    return out
+
+
+def qz_mx4_matmul_workspace(n, d_o, d_i) -> int:
+    return lib().qz_mx4_matmul_workspace(n, d_o, d_i)
+
+
+def qz_mx4_matmul(xcodes, xscales, codes, scales, d_i, bias=None, out_dtype=None, out=None, ws=None):
+    """Y = X W^T + bias with X [n x d_i] and W [d_o x d_i] both in MX4."""
+    _dev(xcodes, "X codes")
+    n, d_o, dev = xcodes.shape[0], codes.shape[0], xcodes.device
+    _mx4_pair(xcodes, xscales, n, d_i, "X", dev)
+    _mx4_pair(codes, scales, d_o, d_i, "W", dev)
+    stream = _on(dev, out, ws)
+    out, yp, ldy = _product_out(out, n, d_o, out_dtype, dev)
+    if ws is None:
+        ws = _workspace(lib().qz_mx4_matmul_workspace(n, d_o, d_i), dev)
+    _call(dev, lib().qz_mx4_matmul, xcodes.data_ptr(), xscales.data_ptr(), n, codes.data_ptr(),
+          scales.data_ptr(), d_o, d_i, _vector(bias, d_o, "bias", dev), yp, _dtype_code(out), ldy,
+          ws.data_ptr(), ws.numel(), stream)
+    return out
+
+
+def _moe_params(n_experts, top_k, renorm):
+    return QzMoe(C.sizeof(QzMoe), int(n_experts), int(top_k), _lib.QZ_MOE_RENORM if renorm else 0)
+
+
+def qz_mx4_moe_workspace(n, d, f, n_experts, top_k) -> int:
+    return lib().qz_mx4_moe_workspace(n, d, f, C.byref(_moe_params(n_experts, top_k, False)))
+
+
+def qz_mx4_moe(X, router, gu_codes, gu_scales, dn_codes, dn_scales, top_k, renorm=True,
+               routing=False, ws=None):
+    """The routed expert layer for few tokens: X bf16 [n x d], router [E x d] (bf16 or fp32),
+    gate and up weights [E x 2f x d] and down weights [E x d x f] in MX4.  Returns Y bf16
+    [n x d], and with routing=True also (ids int32, weights fp32) [n x top_k]."""
+    torch = _torch()
+    ptr, ldx = _rows(X, "X", (torch.bfloat16,))
+    (n, d), dev = X.shape, X.device
+    _dev(router, "router")
+    if router.dim() != 2 or router.shape[1] != d or gu_codes.dim() != 3 or gu_codes.shape[1] % 2:
+        raise ValueError("router must be [E x d], the gate and up weights [E x 2f x d]")
+    E, f = router.shape[0], gu_codes.shape[1] // 2
+    if gu_codes.shape[0] != E or tuple(dn_codes.shape[:2]) != (E, d):
+        raise ValueError("the experts' weights must be [E x 2f x d] and [E x d x f]")
+    _mx4_pair(gu_codes, gu_scales, E * 2 * f, d, "gate and up", dev)
+    _mx4_pair(dn_codes, dn_scales, E * d, f, "down", dev)
+    stream = _on(dev, router, ws)
+    p = _moe_params(E, top_k, renorm)
+    if ws is None:
+        ws = _workspace(lib().qz_mx4_moe_workspace(n, d, f, C.byref(p)), dev)
+    k = max(int(top_k), 0)
+    y = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
+    ids = torch.empty((n, k), dtype=torch.int32, device=dev) if routing else None
+    w = torch.empty((n, k), dtype=torch.float32, device=dev) if routing else None
+    _call(dev, lib().qz_mx4_moe, ptr, _lib.QZ_BF16, n, ldx, d, f, C.byref(p), router.data_ptr(),
+          _dtype_code(router), gu_codes.data_ptr(), gu_scales.data_ptr(), dn_codes.data_ptr(),
+          dn_scales.data_ptr(), y.data_ptr(), ids.data_ptr() if routing else None,
+          w.data_ptr() if routing else None, ws.data_ptr(), ws.numel(), stream)
+    return (y, ids, w) if routing else y
 
 
 def qz_timing_enable(on=True):

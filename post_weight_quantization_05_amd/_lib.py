@@ -19,6 +19,8 @@ QZ_ADMM_REFRESH_FROM_Z = 0x4
 QZ_ADMM_DUAL_NO_RESCALE = 0x8
 QZ_ORDER_ACT = 1
 QZ_ORDER_MIN_PIVOT = 2
+QZ_MX4_FLOOR, QZ_MX4_LEAST = 0, 1
+QZ_MOE_RENORM = 0x1
 
 STATUS_NAMES = {0: "QZ_OK", -1: "QZ_EINVAL", -2: "QZ_ENOTPD", -3: "QZ_ENONFINITE", -4: "QZ_EHIP",
                 -5: "QZ_ESOLVER", -6: "QZ_EWORKSPACE"}
@@ -33,7 +35,11 @@ EXPORTS = ("qz_hessian_workspace", "qz_build_hessian", "qz_rtn_workspace", "qz_r
            "qz_objective", "qz_objective_i32", "qz_local_search_workspace", "qz_local_search",
            "qz_packed_words",
            "qz_pack",
-           "qz_unpack", "qz_timing_enable", "qz_timing_read", "qz_timing_kind_name",
+           "qz_unpack",
+           "qz_mx4_blocks", "qz_mx4_quantize", "qz_mx4_unpack", "qz_mx4_linear_workspace",
+           "qz_mx4_linear", "qz_mx4_matmul_workspace", "qz_mx4_matmul", "qz_mx4_moe_workspace",
+           "qz_mx4_moe",
+           "qz_timing_enable", "qz_timing_read", "qz_timing_kind_name",
            "qz_last_error", "qz_abi_version")
 
 
@@ -46,6 +52,11 @@ class QzAdmm(C.Structure):
     _fields_ = [("struct_size", C.c_uint32), ("iters", C.c_int32), ("rho0", C.c_float),
                 ("gamma", C.c_float), ("refresh_every", C.c_int32), ("flags", C.c_uint32),
                 ("t0", C.c_int32)]
+
+
+class QzMoe(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
+                ("flags", C.c_uint32)]
 
 
 P = C.c_void_p
@@ -83,6 +94,16 @@ _SIGS = {
     "qz_packed_words": (I64, [I64, I32]),
     "qz_pack": (C.c_int, [P, I64, I64, I32, P, P]),
     "qz_unpack": (C.c_int, [P, I64, I64, I32, P, P]),
+    "qz_mx4_blocks": (I64, [I64]),
+    "qz_mx4_quantize": (C.c_int, [P, I32, I64, I64, I64, I32, P, P, P, P, P]),
+    "qz_mx4_unpack": (C.c_int, [P, P, I64, I64, P, P, P, P]),
+    "qz_mx4_linear_workspace": (SZ, [I64, I64, I64]),
+    "qz_mx4_linear": (C.c_int, [P, I32, I64, I64, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),
+    "qz_mx4_matmul_workspace": (SZ, [I64, I64, I64]),
+    "qz_mx4_matmul": (C.c_int, [P, P, I64, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),
+    "qz_mx4_moe_workspace": (SZ, [I64, I64, I64, C.POINTER(QzMoe)]),
+    "qz_mx4_moe": (C.c_int, [P, I32, I64, I64, I64, I64, C.POINTER(QzMoe), P, I32, P, P, P, P, P, P,
+                             P, P, SZ, P]),
     "qz_timing_enable": (C.c_int, [C.c_int]),
     "qz_timing_read": (C.c_int, [C.POINTER(C.c_int64), C.POINTER(C.c_double), C.c_int, C.c_int]),
     "qz_timing_kind_name": (C.c_char_p, [C.c_int]),

@@ -59,6 +59,9 @@ enum KernelKind : int {
   K_LS_PROPOSE,
   K_LS_ACCEPT,
   K_ORDER,
+  K_MX4_QUANTIZE,
+  K_MX4_PRODUCT,
+  K_MX4_MOE,
   K_KIND_COUNT
 };
 // Records an event pair around the enclosed launches when timing is enabled.
@@ -255,6 +258,37 @@ int launch_inverse_f32(const float* x, int64_t n, float* y, hipStream_t s);
 int launch_range_of_grid(const float* scales, const uint8_t* zeros, int64_t n, int bits,
                          float* lo0, float* hi0, hipStream_t s);
 int launch_copy_bytes(const void* src, int64_t n, void* dst, hipStream_t s);
+
+// microscaled 4-bit storage (k_mx4.hip, k_mx4_gemm.hip, k_mx4_moe.hip)
+int launch_mx4_quantize(const void* W, int wt, int64_t rows, int64_t cols, int64_t ldw, int rule,
+                        const float* colw, uint8_t* codes, uint8_t* scales, void* values,
+                        hipStream_t s);
+int launch_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                      int32_t* out, float* out_scales, uint8_t* zeros, hipStream_t s);
+// out [n x ldo] = X [n x d_i] (bf16), zero in columns d_i .. ldo
+int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint16_t* out,
+                   int64_t ldo, hipStream_t s);
+struct Mx4Product {   // Y = X W^T + bias
+  int64_t n, d_o, G;                            // G: blocks of a row
+  const uint16_t* X; int64_t ldx;               // bf16 [n x 32 G], rows 16-byte aligned, or null:
+  const uint8_t* xcodes; const uint8_t* xscales;   // X in MX4
+  const uint8_t* codes; const uint8_t* scales;  // W
+  const float* bias;                            // [d_o] or null
+  void* Y; int yt; int64_t ldy;
+};
+int launch_mx4_product(const Mx4Product& p, hipStream_t s);
+struct MoeArgs {
+  int64_t n, d, f, Gd, Gf;                      // Gd, Gf: blocks of rows of d and f columns
+  int E, k, renorm;
+  const uint16_t* X; int64_t ldx;               // bf16 [n x 32 Gd], rows 16-byte aligned
+  const void* router;
+  const uint8_t *gu_codes, *gu_scales, *dn_codes, *dn_scales;
+  uint16_t* Y; int32_t* ids; float* weights;    // ids, weights nullable
+  double* logits;                               // [n x E]
+  int32_t* sel; double* top;                    // [n x k] chosen expert and its logit
+  uint16_t *h_hi, *h_lo; int64_t ldh;           // [n k x 32 Gf]
+};
+int launch_moe(const MoeArgs& a, int router_type, hipStream_t s);
 
 // eigendecomposition of Sigma H Sigma (k_eig.hip): workspace bytes (asks the solver library
 // for its scratch size once per size), and the decomposition in the caller's workspace

@@ -1,0 +1,421 @@
+"""GPU: the microscaled 4-bit operators against the oracle's definitions in 64 bits.
+
+Quantisation is compared bit for bit.  Products are compared exactly where every partial sum
+is a small multiple of a power of two (then fp32 sums have no rounding, whatever their order),
+and within a derived bound on ordinary values:
+
+  fp32 sums: the matrix cores add 32 (bf16) or 128 (MX4) products into one accumulator at a
+  time, so a sum of K products passes through at most K / 32 roundings of the accumulator, 32
+  inside a step, and the joins of the wavefronts' partial sums (below 32); each rounding is at
+  most 2^-23 (truncation) of a partial sum, and those are at most S = sum |x w|:
+      |error| <= (K / 32 + 64) 2^-23 S,
+  plus half a step of the output type, 2^-8 |y| in bf16 and 2^-24 |y| in fp32."""
+import numpy as np
+import pytest
+
+from gpu_util import qz, to_dev, to_host
+from oracle import mx4, objective
+
+pytestmark = pytest.mark.gpu
+
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def _t():
+    import torch
+    return torch
+
+
+def _dtype(name):
+    return {"bf16": _t().bfloat16, "f32": _t().float32}[name]
+
+
+def _bf16(a):
+    """Values rounded to bf16, as float64, and the device tensor."""
+    t = _t().from_numpy(np.ascontiguousarray(a, np.float32)).to(_t().bfloat16)
+    return t.double().numpy(), t.cuda()
+
+
+def _host(t):
+    return t.double().cpu().numpy() if t.is_floating_point() else to_host(t)
+
+
+def _random_codes(rng, rows, cols, e_lo=126, e_hi=129):
+    """Codes (zero past cols) and factors."""
+    g = -(-cols // 32)
+    c = rng.integers(0, 16, (rows, 32 * g)).astype(np.uint8)
+    c[:, cols:] = 0
+    return c[:, 0::2] | (c[:, 1::2] << 4), rng.integers(e_lo, e_hi, (rows, g)).astype(np.uint8)
+
+
+def _sum_bound(K, S, out, y):
+    return (K / 32 + 64) * 2.0 ** -23 * S + HALF[out] * np.abs(y)
+
+
+# ------------------------------------------------------------------------------ quantisation
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 31), (2, 32), (5, 33), (70, 200), (33, 1056),
+                                       (64, 4096), (300, 520), (1, 25600)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rule,weighted", [("floor", False), ("least", False), ("least", True)])
+def test_quantize_bit_exact(rows, cols, dtype, rule, weighted):
+    q = qz()
+    rng = np.random.default_rng([rows, cols])
+    w = rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)))
+    w[rng.random((rows, cols)) < 0.1] = 0.0
+    near = rng.random((rows, cols)) < 0.3     # many values on the grid, on ties and at 6 .. 8
+    w = np.where(near, np.round(w * 8) / 8 * 2, w)
+    x = _t().from_numpy(w.astype(np.float32)).to(_dtype(dtype))
+    h = np.exp(rng.standard_normal(cols)).astype(np.float32) if weighted else None
+    c, s, v = q.qz_mx4_quantize(x.cuda(), rule=rule, colw=None if h is None else to_dev(h), values=True)
+    c_ref, s_ref = mx4.quantize(x.float().numpy(), rule, h)
+    np.testing.assert_array_equal(to_host(s), s_ref)
+    np.testing.assert_array_equal(to_host(c), c_ref)
+    assert v.dtype == x.dtype
+    np.testing.assert_array_equal(_host(v), mx4.values(c_ref, s_ref, cols))
+    c2, s2 = q.qz_mx4_quantize(x.cuda(), rule=rule, colw=None if h is None else to_dev(h))
+    assert _t().equal(c, c2) and _t().equal(s, s2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rule", ["floor", "least"])
+def test_quantize_special_values(dtype, rule):
+    q = qz()
+    top = float(_t().finfo(_dtype(dtype)).max)
+    rows = [[0.0] * 40, [-0.0] * 40, [2.0 ** -126] * 40, [2.0 ** -130, -(2.0 ** -128)] * 20,
+            [2.0 ** -133] + [0.0] * 39, [top, -top] * 20, [1.0] * 32 + [float("nan")] + [2.0] * 7,
+            [float("inf")] + [1.0] * 39, [-float("inf"), float("nan")] * 20, [1e-30, 1e30] * 20,
+            [7.0, 0.5, -3.0, -0.0] * 10, [5.0, -5.0, 2.5, 1.75, 0.75, 0.25, 3.5, 1.25] * 5]
+    x = _t().tensor(rows, dtype=_t().float32).to(_dtype(dtype))
+    c, s, v = q.qz_mx4_quantize(x.cuda(), rule=rule, values=True)
+    c_ref, s_ref = mx4.quantize(x.float().numpy(), rule)
+    np.testing.assert_array_equal(to_host(s), s_ref)
+    np.testing.assert_array_equal(to_host(c), c_ref)
+    np.testing.assert_array_equal(_host(v), mx4.values(c_ref, s_ref, 40))
+
+
+def test_quantize_strided_and_unaligned_rows():
+    q, torch = qz(), _t()
+    base = torch.randn((37, 300), device="cuda")
+    for x in (base[:, 5:205], base[:, 4:132], base[::2, 1:97], base[3:4, 7:39],
+              base.to(torch.bfloat16)[:, 3:131], base.to(torch.bfloat16)[:, 8:200]):
+        c, s, v = q.qz_mx4_quantize(x, rule="least", values=True)
+        c_ref, s_ref = mx4.quantize(x.float().cpu().numpy(), "least")
+        np.testing.assert_array_equal(to_host(c), c_ref)
+        np.testing.assert_array_equal(to_host(s), s_ref)
+        np.testing.assert_array_equal(_host(v), mx4.values(c_ref, s_ref, x.shape[1]))
+
+
+@pytest.mark.parametrize("cols", [32, 33, 96])
+def test_unpack(cols):
+    q = qz()
+    rng = np.random.default_rng(cols)
+    codes, scales = _random_codes(rng, 17, cols, 0, 256)
+    scales[0, 0], scales[1, 0], scales[2, 0], scales[3, 0] = 0, 1, 2, 255
+    c, s, z = q.qz_mx4_unpack(to_dev(codes), to_dev(scales), cols)
+    np.testing.assert_array_equal(to_host(c), 2 * mx4.elements(codes, cols))
+    want = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(np.int64) - 128))
+    np.testing.assert_array_equal(_host(s), want)
+    assert not to_host(z).any()
+
+
+# ---------------------------------------------------------------------------------- products
+NS = [1, 2, 5, 15, 16, 17, 31, 33, 64, 65, 128, 129, 200, 257, 300]
+SHAPES = [(32, 16), (1, 1), (31, 7), (33, 15), (64, 17), (96, 100), (200, 33), (512, 64),
+          (640, 130), (1024, 257), (1056, 40), (2080, 520)]
+
+
+def _cases():
+    """Every n with some shape and every shape with some n, and the corners of both."""
+    out = [(n, *SHAPES[i % len(SHAPES)]) for i, n in enumerate(NS)]
+    out += [(NS[(5 * i + 3) % len(NS)], *s) for i, s in enumerate(SHAPES)]
+    return sorted(set(out + [(300, 2080, 520), (1, 2080, 520), (257, 1, 1), (130, 96, 1030)]))
+
+
+@pytest.mark.parametrize("n,d_i,d_o", _cases())
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_linear_exact(n, d_i, d_o, out):
+    """Integers -8 .. 8 times multiples of 1/4 up to 12 (factors 1/2 .. 2): sums are multiples
+    of 1/4 below 2^18, exact in fp32; bf16 output is the one rounding of that."""
+    q = qz()
+    rng = np.random.default_rng([n, d_i, d_o])
+    x = rng.integers(-8, 9, (n, d_i)).astype(np.float64)
+    codes, scales = _random_codes(rng, d_o, d_i)
+    bias = rng.integers(-50, 50, d_o).astype(np.float32) if (n + d_o) % 2 else None
+    y = x @ mx4.values(codes, scales, d_i).T + (0 if bias is None else bias)
+    got = q.qz_mx4_linear(_bf16(x)[1], to_dev(codes), to_dev(scales),
+                          bias=None if bias is None else to_dev(bias), out_dtype=_dtype(out))
+    assert got.dtype == _dtype(out)
+    want = _t().from_numpy(y).float().to(_dtype(out)).double().numpy()
+    np.testing.assert_array_equal(_host(got), want)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", _cases())
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_exact(n, d_i, d_o, out):
+    """Both factors 1/2 .. 2: products are multiples of 1/16 up to 144, sums below 2^19."""
+    q = qz()
+    rng = np.random.default_rng([n, d_i, d_o, 4])
+    xc, xs = _random_codes(rng, n, d_i)
+    codes, scales = _random_codes(rng, d_o, d_i)
+    bias = rng.integers(-50, 50, d_o).astype(np.float32) if (n + d_o) % 2 else None
+    y = mx4.values(xc, xs, d_i) @ mx4.values(codes, scales, d_i).T + (0 if bias is None else bias)
+    got = q.qz_mx4_matmul(to_dev(xc), to_dev(xs), to_dev(codes), to_dev(scales), d_i,
+                          bias=None if bias is None else to_dev(bias), out_dtype=_dtype(out))
+    want = _t().from_numpy(y).float().to(_dtype(out)).double().numpy()
+    np.testing.assert_array_equal(_host(got), want)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", [(1, 4096, 512), (13, 5120, 300), (100, 1408, 256), (515, 2048, 384)])
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_products_of_ordinary_values(n, d_i, d_o, four, out):
+    q = qz()
+    rng = np.random.default_rng([n, d_i])
+    x, xd = _bf16(rng.standard_t(4, (n, d_i)))
+    w = (rng.standard_normal((d_o, d_i)) * 0.015).astype(np.float32)
+    codes, scales = mx4.quantize(w)
+    wv = mx4.values(codes, scales, d_i)
+    if four:
+        xc, xs = q.qz_mx4_quantize(xd)
+        got = q.qz_mx4_matmul(xc, xs, to_dev(codes), to_dev(scales), d_i, out_dtype=_dtype(out))
+        x = mx4.values(*mx4.quantize(x), d_i)
+    else:
+        got = q.qz_mx4_linear(xd, to_dev(codes), to_dev(scales), out_dtype=_dtype(out))
+    y = x @ wv.T
+    assert (np.abs(_host(got) - y) <= _sum_bound(d_i, np.abs(x) @ np.abs(wv).T, out, y)).all()
+
+
+def test_far_factors():
+    """The ends of the factor's range: 2^-127 (subnormal weights) against 2^100 inputs, and
+    products that cancel exactly."""
+    q = qz()
+    rng = np.random.default_rng(5)
+    codes, _ = _random_codes(rng, 40, 96)
+    scales = np.zeros((40, 3), np.uint8)
+    scales[20:] = 1
+    x, xd = _bf16(np.ldexp(rng.integers(-8, 9, (20, 96)).astype(np.float64), 100))
+    want = x @ mx4.values(codes, scales, 96).T
+    got = q.qz_mx4_linear(xd, to_dev(codes), to_dev(scales), out_dtype=_t().float32)
+    np.testing.assert_array_equal(_host(got), want)
+    xc, _ = _random_codes(rng, 20, 96)
+    xs = np.full((20, 3), 227, np.uint8)
+    want = mx4.values(xc, xs, 96) @ mx4.values(codes, scales, 96).T
+    got = q.qz_mx4_matmul(to_dev(xc), to_dev(xs), to_dev(codes), to_dev(scales), 96, out_dtype=_t().float32)
+    np.testing.assert_array_equal(_host(got), want)
+
+
+@pytest.mark.parametrize("n", [1, 16, 40, 130, 300])
+@pytest.mark.parametrize("d_i", [256, 1056])
+def test_nan_stays_in_its_row(n, d_i):
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(n)
+    x = rng.integers(-8, 9, (n, d_i)).astype(np.float64)
+    codes, scales = _random_codes(rng, 70, d_i)
+    scales[33, -1] = 255
+    bad = n // 2
+    x[bad, 3] = np.nan
+    got = _host(q.qz_mx4_linear(_bf16(x)[1], to_dev(codes), to_dev(scales), out_dtype=torch.float32))
+    assert np.isnan(got[bad]).all() and np.isnan(got[:, 33]).all()
+    keep_t, keep_r = np.arange(n) != bad, np.arange(70) != 33
+    want = x[keep_t] @ mx4.values(codes, scales, d_i)[keep_r].T
+    np.testing.assert_array_equal(got[keep_t][:, keep_r], want)
+    xc, xs = _random_codes(rng, n, d_i)
+    xs[bad, 0] = 255
+    got = _host(q.qz_mx4_matmul(to_dev(xc), to_dev(xs), to_dev(codes), to_dev(scales), d_i,
+                                out_dtype=torch.float32))
+    assert np.isnan(got[bad]).all() and np.isnan(got[:, 33]).all()
+    want = mx4.values(xc, xs, d_i)[keep_t] @ mx4.values(codes, scales, d_i)[keep_r].T
+    np.testing.assert_array_equal(got[keep_t][:, keep_r], want)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", [(1, 128, 50), (16, 200, 33), (70, 96, 129), (300, 512, 300)])
+def test_strided_inputs_and_outputs(n, d_i, d_o):
+    """Rows inside wider buffers, at odd offsets: nothing between the rows is touched."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng([n, d_o])
+    x = rng.integers(-8, 9, (n, d_i)).astype(np.float64)
+    codes, scales = _random_codes(rng, d_o, d_i)
+    want = x @ mx4.values(codes, scales, d_i).T
+    xc, xs = _random_codes(rng, n, d_i)
+    want4 = mx4.values(xc, xs, d_i) @ mx4.values(codes, scales, d_i).T
+    for off, dtype in ((0, torch.float32), (1, torch.bfloat16), (8, torch.bfloat16), (3, torch.float32)):
+        wide = torch.full((n, d_i + 19), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, off:off + d_i] = _bf16(x)[1]
+        for four in (False, True):
+            y = torch.full((n + 2, d_o + 11), 7.0, dtype=dtype, device="cuda")
+            part = y[1:n + 1, off:off + d_o]
+            if four:
+                q.qz_mx4_matmul(to_dev(xc), to_dev(xs), to_dev(codes), to_dev(scales), d_i, out=part)
+            else:
+                q.qz_mx4_linear(wide[:, off:off + d_i], to_dev(codes), to_dev(scales), out=part)
+            ref = torch.full_like(y, 7.0)
+            ref[1:n + 1, off:off + d_o] = torch.from_numpy(want4 if four else want).to(dtype).cuda()
+            assert torch.equal(y, ref), (off, dtype, four)
+
+
+def test_empty_products():
+    q, torch = qz(), _t()
+    codes, scales = _random_codes(np.random.default_rng(0), 8, 64)
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    assert q.qz_mx4_linear(x, to_dev(codes), to_dev(scales)).shape == (0, 8)
+    c, s = q.qz_mx4_quantize(x)
+    assert c.shape == (0, 32) and q.qz_mx4_matmul(c, s, to_dev(codes), to_dev(scales), 64).shape == (0, 8)
+    x = torch.ones((3, 64), dtype=torch.bfloat16, device="cuda")
+    assert q.qz_mx4_linear(x, to_dev(codes)[:0], to_dev(scales)[:0]).shape == (3, 0)
+
+
+# --------------------------------------------------------------------------- the expert layer
+def _moe_bound(x, router, gu, dn, k, renorm):
+    """(y, |error| allowed).  Per pair: dg, du from the fp32 sums; |silu'| <= 1.1; the exponential,
+    quotient and product of h: 16 steps of 2^-24; the split of h: 2^-16; the weight: 2^-20; then
+    the down sum (value and remainder: twice the products) and the join of the experts."""
+    f, d = gu.shape[1] // 2, x.shape[1]
+    ids, p = mx4.route(x, router, k, renorm)
+    y, err = np.zeros((len(x), dn.shape[1])), np.zeros((len(x), dn.shape[1]))
+    eps_d, eps_f = (d / 32 + 64) * 2.0 ** -23, (2 * f / 32 + 64 + 32) * 2.0 ** -23
+    for t in range(len(x)):
+        for r, e in enumerate(ids[t]):
+            a = gu[e] @ x[t]
+            da = eps_d * (np.abs(gu[e]) @ np.abs(x[t]))
+            g, u = a[:f], a[f:]
+            s = g / (1 + np.exp(-g))
+            h = s * u
+            dh = 1.1 * da[:f] * (np.abs(u) + da[f:]) + np.abs(s) * da[f:] + np.abs(h) * (2.0 ** -20 + 2.0 ** -16)
+            y[t] += p[t, r] * (dn[e] @ h)
+            err[t] += p[t, r] * (np.abs(dn[e]) @ (dh + (eps_f + 2.0 ** -20) * np.abs(h)))
+    return y, ids, p, err + 2.0 ** -8 * np.abs(y)
+
+
+MOE = [  # n, d, f, experts, top_k, renorm, router type
+    (1, 64, 32, 4, 1, True, "bf16"), (1, 256, 96, 8, 2, False, "bf16"), (3, 100, 33, 5, 5, True, "f32"),
+    (7, 512, 128, 16, 4, True, "bf16"), (16, 128, 64, 128, 8, True, "bf16"), (17, 33, 1, 3, 2, False, "f32"),
+    (40, 256, 160, 64, 6, False, "bf16"), (64, 96, 64, 4, 3, True, "f32"), (65, 64, 40, 256, 16, True, "bf16"),
+    (130, 64, 32, 2, 1, False, "bf16"), (1, 1, 1, 1, 1, True, "f32"), (5, 1056, 544, 7, 2, True, "bf16")]
+
+
+def _moe_inputs(case):
+    n, d, f, E, k, renorm, rt = case
+    rng = np.random.default_rng([n, d, f, E])
+    x, xd = _bf16(rng.standard_normal((n, d)))
+    router = (rng.standard_normal((E, d)) / np.sqrt(d)).astype(np.float32)
+    rd = _t().from_numpy(router).to(_dtype(rt))
+    gu = mx4.quantize(rng.standard_normal((E * 2 * f, d)).astype(np.float32) / np.sqrt(d))
+    dn = mx4.quantize(rng.standard_normal((E * d, f)).astype(np.float32) / np.sqrt(f))
+    stored = [a.reshape(E, b, -1) for a, b in zip((*gu, *dn), (2 * f, 2 * f, d, d))]
+    return x, xd, rd.double().numpy(), rd.cuda(), stored, [to_dev(a) for a in stored]
+
+
+@pytest.mark.parametrize("case", MOE)
+def test_moe(case):
+    q = qz()
+    n, d, f, E, k, renorm, _ = case
+    x, xd, router, rd, st, dev = _moe_inputs(case)
+    want, ids, p, bound = _moe_bound(x, router, mx4.values(st[0], st[1], d), mx4.values(st[2], st[3], f), k, renorm)
+    y, got_ids, w = q.qz_mx4_moe(xd, rd, *dev, k, renorm=renorm, routing=True)
+    np.testing.assert_array_equal(to_host(got_ids), ids)
+    # exp of a rounded difference below 2^5, the sum and the quotient: 2^-20 in all
+    assert (np.abs(_host(w) - p) <= 2.0 ** -20 * p).all()
+    assert (np.abs(_host(y) - want) <= bound).all(), np.max(np.abs(_host(y) - want) / bound)
+    assert _t().equal(y, q.qz_mx4_moe(xd, rd, *dev, k, renorm=renorm))     # and again, to the bit
+
+
+def test_moe_ties_and_strides():
+    """Equal router rows: the lower index.  Rows of x inside a wider buffer, odd offset."""
+    q, torch = qz(), _t()
+    case = (9, 64, 32, 12, 3, True, "bf16")
+    x, xd, router, rd, st, dev = _moe_inputs(case)
+    rd[5:9] = rd[4]
+    rd[10] = rd[1]
+    ids, p = mx4.route(x, rd.double().cpu().numpy(), 3, True)
+    wide = torch.full((9, 80), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 7:71] = xd
+    y, got, w = q.qz_mx4_moe(wide[:, 7:71], rd, *dev, 3, routing=True)
+    np.testing.assert_array_equal(to_host(got), ids)
+    assert torch.equal(y, q.qz_mx4_moe(xd, rd, *dev, 3))
+
+
+def test_moe_nan_rows():
+    """A token with a NaN (all its logits are NaN) takes the first experts and gives NaN; the
+    others are as without it.  A NaN router row is chosen last."""
+    q, torch = qz(), _t()
+    case = (6, 64, 32, 8, 2, True, "bf16")
+    x, xd, router, rd, st, dev = _moe_inputs(case)
+    clean = q.qz_mx4_moe(xd, rd, *dev, 2)
+    bad = xd.clone()
+    bad[2, 5] = float("nan")
+    y, ids, w = q.qz_mx4_moe(bad, rd, *dev, 2, routing=True)
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[2]).all() and list(to_host(ids)[2]) == [0, 1]
+    r2 = rd.clone()
+    r2[3] = float("nan")
+    y, ids, w = q.qz_mx4_moe(xd, r2, *dev, 8, routing=True)
+    assert (to_host(ids)[:, 7] == 3).all() and (to_host(w)[:, 7] == 0).all()
+    assert not torch.isnan(y).any()
+
+
+# --------------------------------------------------------------------- streams, graphs, a run
+def test_streams_and_graph_replays():
+    """The operators on a side stream and in a graph, replayed between eager work on new data."""
+    q, torch = qz(), _t()
+    case = (4, 200, 96, 8, 2, True, "bf16")     # rows that are copied to the workspace first
+    x, xd, router, rd, st, dev = _moe_inputs(case)
+    codes, scales = q.qz_mx4_quantize(torch.randn((300, 200), device="cuda"))
+
+    def chain(inp):
+        c, s = q.qz_mx4_quantize(inp)
+        return (q.qz_mx4_linear(inp, codes, scales), q.qz_mx4_matmul(c, s, codes, scales, 200),
+                q.qz_mx4_moe(inp, rd, *dev, 2))
+
+    eager = chain(xd)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = chain(xd)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(eager, other))
+    static = xd.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = chain(static)
+    for seed in range(4):
+        fresh = torch.randn((4, 200), generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16).cuda()
+        static.copy_(fresh)
+        g.replay()
+        want = chain(fresh)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)), seed
+
+
+def test_calibrate_quantise_and_use():
+    """The operators as they are used together: Hessian, factors chosen under diag(H), the layer
+    objective of the stored weights, and the layer run on its inputs."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(3)
+    x, xd = _bf16(rng.standard_t(4, (512, 256)) * np.where(rng.random(256) < 0.05, 20.0, 1.0))
+    w = (rng.standard_normal((96, 256)) * 0.015).astype(np.float32)
+    h = q.qz_build_hessian(xd, damp=0.01)
+    f = {}
+    for rule, colw in (("floor", None), ("least", h["diag"])):
+        codes, scales, values = q.qz_mx4_quantize(to_dev(w), rule=rule, colw=colw, values=True)
+        c, s, z = q.qz_mx4_unpack(codes, scales, 256)
+        f[rule] = q.qz_objective(h["H"], to_dev(w), c, s, z, 32)
+        want = objective.objective(_host(h["H"]), w, _host(values))
+        assert abs(f[rule] - want) <= 1e-4 * want
+        y = q.qz_mx4_linear(xd, codes, scales, out_dtype=torch.float32)
+        v = _host(values)
+        assert (np.abs(_host(y) - x @ v.T) <= _sum_bound(256, np.abs(x) @ np.abs(v).T, "f32", x @ v.T)).all()
+    weighted = {r: (_host(h["diag"]) * (mx4.values(*mx4.quantize(w, r, c), 256) - w) ** 2).sum()
+                for r, c in (("floor", None), ("least", to_host(h["diag"])))}
+    assert weighted["least"] < weighted["floor"]
+
+
+def test_timing_kinds_are_reported():
+    q, torch = qz(), _t()
+    q.qz_timing_read(reset=True)
+    q.qz_timing_enable(True)
+    c, s = q.qz_mx4_quantize(torch.randn((64, 64), device="cuda"))
+    q.qz_mx4_matmul(c, s, c, s, 64)
+    q.qz_timing_enable(False)
+    t = q.qz_timing_read(reset=True)
+    assert t["mx4_quantize"][0] == 1 and t["mx4_product"][0] == 1

@@ -1,0 +1,186 @@
+"""CPU: the microscaled 4-bit oracle against hand-derived values, and the refusals of the
+library's MX4 entry points (host-side checks: no GPU is touched)."""
+import ctypes as C
+import os
+
+import numpy as np
+import pytest
+
+from oracle import mx4
+
+
+@pytest.mark.parametrize("a,code", [
+    (0.0, 0), (0.25, 0), (0.2500001, 1), (0.5, 1), (0.75, 2), (0.7499999, 1), (1.0, 2), (1.25, 2),
+    (1.2500001, 3), (1.75, 4), (2.5, 4), (2.5000002, 5), (3.5, 6), (3.4999998, 5), (5.0, 6),
+    (5.0000005, 7), (6.0, 7), (7.99, 7), (100.0, 7)])
+def test_rounding_to_elements(a, code):
+    assert mx4.nearest_code(np.array([a]))[0] == code
+
+
+def test_a_block_by_hand():
+    # amax 7 lies in [4, 8) x 2^0: E = 127 and 7 saturates to 6 (error 1); with E = 128 the
+    # grid is 0 1 2 3 4 6 8 12: 7 is a tie between 6 (code 5) and 8 (code 6, even): error 1,
+    # 0.5 goes to the even code 0 (error .25 squared) and 3 stays, so "least" keeps 127
+    w = np.zeros((1, 32), np.float32)
+    w[0, :4] = [7.0, 0.5, -3.0, -0.0]
+    codes, scales = mx4.quantize(w)
+    assert scales[0, 0] == 127
+    assert list(codes[0, :2]) == [0x17, 0x8D] and not codes[0, 2:].any()
+    assert mx4.quantize(w, "least")[1][0, 0] == 127
+    # all elements 7.5: saturation costs 1.5 each, the doubled grid rounds to 8: 0.5 each
+    w[:] = 7.5
+    codes, scales = mx4.quantize(w, "least")
+    assert scales[0, 0] == 128 and (codes == 0x66).all()
+    assert (mx4.values(codes, scales, 32) == 8.0).all()
+
+
+def test_column_weights_decide():
+    # 7.5 gains from the doubled factor, 0.5 (which becomes 0 there) loses
+    w = np.zeros((1, 32), np.float32)
+    w[0, 0], w[0, 1] = 7.5, 0.5
+    one = np.ones(32)
+    assert mx4.quantize(w, "least", one)[1][0, 0] == 128
+    heavy = one.copy()
+    heavy[1] = 100.0
+    assert mx4.quantize(w, "least", heavy)[1][0, 0] == 127
+
+
+def test_edges_of_the_exponent():
+    tiny = np.float32(2.0 ** -149)
+    w = np.zeros((4, 32), np.float32)
+    w[1, 5] = tiny
+    w[2, 5] = np.finfo(np.float32).max
+    w[3, 5] = np.inf
+    codes, scales = mx4.quantize(w)
+    assert list(scales[:, 0]) == [0, 0, 252, 255]
+    assert not codes[0].any() and not codes[1].any() and not codes[3].any()
+    assert mx4.values(codes, scales, 32)[2, 5] == 6 * 2.0 ** 125
+    assert np.isnan(mx4.values(codes, scales, 32)[3]).all()
+
+
+def test_padding_and_storage_order():
+    w = np.zeros((2, 33), np.float32)
+    w[0, 1], w[1, 32] = 1.0, -4.0
+    codes, scales = mx4.quantize(w)
+    assert codes.shape == (2, 32) and scales.shape == (2, 2)
+    assert codes[0, 0] == 0x60 and scales[0, 0] == 125      # 1 = 4 x 2^-2, odd column: high nibble
+    assert codes[1, 16] == 0x0E and scales[1, 1] == 127
+    np.testing.assert_array_equal(mx4.values(codes, scales, 33), w)
+
+
+def test_routing_ties_go_to_the_lower_index():
+    x = np.array([[1.0, 2.0]])
+    router = np.array([[0.0, 1.0], [2.0, 0.0], [0.0, 1.0], [1.0, 0.0]])   # logits 2 2 2 1
+    ids, w = mx4.route(x, router, 2, True)
+    assert list(ids[0]) == [0, 1] and list(w[0]) == [0.5, 0.5]
+    ids, w = mx4.route(x, router, 4, False)
+    assert list(ids[0]) == [0, 1, 2, 3] and abs(w.sum() - 1) < 1e-15
+
+
+# ------------------------------------------------------------------------ refusals (C ABI)
+@pytest.fixture(scope="module")
+def lib():
+    from post_weight_quantization_05_amd import _lib, build
+    if not os.path.exists(_lib.LIB_PATH):
+        build.build()
+    return _lib.load()
+
+
+A = 1 << 20      # an address that is aligned for everything; never dereferenced
+
+
+def test_quantize_refusals(lib):
+    from post_weight_quantization_05_amd import _lib
+    good = dict(W=A, wt=0, rows=4, cols=40, ldw=40, rule=0, colw=None, codes=A, scales=A, values=None,
+                stream=None)
+
+    def call(**kw):
+        return lib.qz_mx4_quantize(*{**good, **kw}.values())
+
+    for kw in (dict(wt=2), dict(rows=-1), dict(cols=0), dict(ldw=39), dict(rule=2), dict(colw=A),
+               dict(W=None), dict(codes=None), dict(scales=None), dict(codes=A + 8), dict(W=A + 1),
+               dict(values=A + 1), dict(rule=1, colw=A + 2)):
+        assert call(**kw) == _lib.QZ_EINVAL, kw
+        assert lib.qz_last_error()
+    assert call(rows=0, W=None, codes=None) == _lib.QZ_OK
+    assert lib.qz_mx4_blocks(33) == 2 and lib.qz_mx4_blocks(32) == 1 and lib.qz_mx4_blocks(0) == -1
+    assert lib.qz_mx4_unpack(A, A, 4, 0, A, A, A, None) == _lib.QZ_EINVAL
+    assert lib.qz_mx4_unpack(A + 4, A, 4, 32, A, A, A, None) == _lib.QZ_EINVAL
+    assert lib.qz_mx4_unpack(A, A, 4, 32, A, None, A, None) == _lib.QZ_EINVAL
+    assert lib.qz_mx4_unpack(None, None, 0, 32, None, None, None, None) == _lib.QZ_OK
+
+
+def test_linear_refusals(lib):
+    from post_weight_quantization_05_amd import _lib
+    need = lib.qz_mx4_linear_workspace(3, 20, 40)
+    assert need >= 3 * 64 * 2 and lib.qz_mx4_linear_workspace(-1, 20, 40) == 0
+    assert lib.qz_mx4_linear_workspace(3, 20, 0) == 0
+    good = dict(X=A, xt=0, n=3, ldx=40, codes=A, scales=A, d_o=20, d_i=40, bias=None, Y=A, yt=1,
+                ldy=20, ws=A, ws_bytes=need, stream=None)
+
+    def call(**kw):
+        return lib.qz_mx4_linear(*{**good, **kw}.values())
+
+    for kw in (dict(xt=1), dict(n=-1), dict(n=(1 << 20) + 1), dict(ldx=39), dict(codes=None),
+               dict(codes=A + 4), dict(scales=None), dict(d_o=-1), dict(d_i=0), dict(bias=A + 1),
+               dict(Y=None), dict(Y=A + 2), dict(yt=5), dict(ldy=19), dict(X=None), dict(X=A + 1)):
+        assert call(**kw) == _lib.QZ_EINVAL, kw
+    for kw in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=A + 16)):
+        assert call(**kw) == _lib.QZ_EWORKSPACE, kw
+    assert call(n=0, X=None, Y=None) == _lib.QZ_OK
+    assert call(d_o=0, ldy=0, codes=None) == _lib.QZ_OK
+
+
+def test_matmul_refusals(lib):
+    from post_weight_quantization_05_amd import _lib
+    need = lib.qz_mx4_matmul_workspace(3, 20, 40)
+    good = dict(xc=A, xs=A, n=3, codes=A, scales=A, d_o=20, d_i=40, bias=None, Y=A, yt=0, ldy=20, ws=A,
+                ws_bytes=need, stream=None)
+
+    def call(**kw):
+        return lib.qz_mx4_matmul(*{**good, **kw}.values())
+
+    for kw in (dict(xc=None), dict(xs=None), dict(xc=A + 8), dict(n=-1), dict(codes=A + 2),
+               dict(d_i=0), dict(ldy=19), dict(Y=A + 1), dict(yt=-1)):
+        assert call(**kw) == _lib.QZ_EINVAL, kw
+    assert call(n=0, xc=None, Y=None) == _lib.QZ_OK
+
+
+def test_moe_refusals(lib):
+    from post_weight_quantization_05_amd import _lib
+    def params(E=8, k=2, flags=0, size=C.sizeof(_lib.QzMoe)):
+        return _lib.QzMoe(size, E, k, flags)
+
+    need = lib.qz_mx4_moe_workspace(3, 64, 40, C.byref(params()))
+    assert need > 0
+    assert lib.qz_mx4_moe_workspace(1025, 64, 40, C.byref(params())) == 0
+    assert lib.qz_mx4_moe_workspace(3, 64, 40, C.byref(params(k=9))) == 0
+    good = dict(X=A, xt=0, n=3, ldx=64, d=64, f=40, p=C.byref(params()), router=A, rt=0, gc=A, gs=A,
+                dc=A, ds=A, Y=A, ids=None, weights=None, ws=A, ws_bytes=need, stream=None)
+
+    def call(**kw):
+        return lib.qz_mx4_moe(*{**good, **kw}.values())
+
+    for kw in (dict(xt=1), dict(rt=4), dict(n=-1), dict(n=1025), dict(ldx=63), dict(d=0), dict(f=0),
+               dict(p=None), dict(X=None), dict(router=None), dict(Y=None), dict(gc=None),
+               dict(gs=None), dict(dc=A + 8), dict(ds=None), dict(Y=A + 1), dict(ids=A + 2),
+               dict(weights=A + 1), dict(router=A + 1)):
+        assert call(**kw) == _lib.QZ_EINVAL, kw
+    for kw in (dict(E=0), dict(E=257), dict(k=0), dict(k=17, E=64), dict(k=9), dict(flags=2), dict(size=4)):
+        assert call(p=C.byref(params(**kw))) == _lib.QZ_EINVAL, kw
+    for kw in (dict(ws=None), dict(ws_bytes=need - 1), dict(ws=A + 8)):
+        assert call(**kw) == _lib.QZ_EWORKSPACE, kw
+    assert call(n=0, X=None, Y=None) == _lib.QZ_OK
+
+
+def test_the_binding_refuses_what_it_cannot_pass_on():
+    import torch
+    import post_weight_quantization_05_amd as q
+    x = torch.zeros((2, 32), dtype=torch.bfloat16)
+    c, s = torch.zeros((4, 16), dtype=torch.uint8), torch.zeros((4, 1), dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        q.qz_mx4_quantize(x)                 # not on a GPU
+    with pytest.raises(ValueError):
+        q.qz_mx4_linear(x, c, s)
+    with pytest.raises(ValueError):
+        q.qz_mx4_matmul(c, s, c, s, 32)
