@@ -404,7 +404,7 @@ int qz_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int
  *   (elements between the rows are left alone); rounded once.  Must not overlap the inputs.
  *   Rows of X that are not whole blocks on 16-byte boundaries (d_i % 32, ldx % 8, the
  *   address) are first copied to the workspace.
- *   n <= 2^20, d_o <= 2^24, d_i <= 2^24; n = 0 or d_o = 0 does nothing.
+ *   n <= 2^20, d_o <= 2^24, d_i <= 2^20; n = 0 or d_o = 0 does nothing.
  *   ws: qz_mx4_*_workspace(n, d_o, d_i) bytes, 256-byte aligned (0 bytes: may be null; 0 for
  *   bad sizes); calls that may overlap need different workspaces.  Asynchronous.          */
 size_t qz_mx4_linear_workspace(int64_t n, int64_t d_o, int64_t d_i);

@@ -12,7 +12,7 @@ namespace {
 // Launches index rows and tokens with 16-row grid rows and 32-bit grid dimensions.
 constexpr int64_t kMaxRows = int64_t(1) << 24;
 constexpr int64_t kMaxTokens = int64_t(1) << 20;
-constexpr int64_t kMaxCols = int64_t(1) << 24;
+constexpr int64_t kMaxCols = int64_t(1) << 20;   // byte offsets of a 256-row tile fit 32 bits
 
 bool float_type(int t) { return t == QZ_BF16 || t == QZ_F32; }
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -36,13 +36,19 @@ int check_codes(const char* who, const uint8_t* codes, const uint8_t* scales) {
 // Rows of X that the kernels read as they are: whole blocks on 16-byte boundaries.  Other
 // rows are copied to the workspace first.
 bool direct_x(const void* X, int64_t d_i, int64_t ldx) {
-  return d_i % kMxBlock == 0 && ldx % 8 == 0 && aligned(X, 16);
+  return d_i % kMxBlock == 0 && ldx % 8 == 0 && ldx <= 2 * kMaxCols && aligned(X, 16);
 }
 
 size_t linear_ws(int64_t n, int64_t d_i) {
   Carver c(nullptr);
   c.take<uint16_t>(static_cast<size_t>(n) * mx_blocks(d_i) * kMxBlock);
   return c.used;
+}
+
+// What the kernels may assume of the output and of the factors.
+void set_alignment(Mx4Product* p) {
+  p->y_vec = p->ldy % 4 == 0 && aligned(p->Y, 4 * type_size(p->yt));
+  p->factors_aligned = aligned(p->scales, 4) && aligned(p->xscales, 4);
 }
 
 struct MoeWs {
@@ -124,7 +130,7 @@ static int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i,
   const std::string w(who);
   if (!float_type(yt)) return fail(QZ_EINVAL, w + ": bad output dtype");
   if (n < 0 || n > kMaxTokens || d_o < 0 || d_o > kMaxRows || d_i < 1 || d_i > kMaxCols)
-    return fail(QZ_EINVAL, w + ": need 0 <= n <= 2^20, 0 <= d_o <= 2^24, 1 <= d_i <= 2^24");
+    return fail(QZ_EINVAL, w + ": need 0 <= n <= 2^20, 0 <= d_o <= 2^24, 1 <= d_i <= 2^20");
   if (ldy < d_o) return fail(QZ_EINVAL, w + ": ldy must be at least d_o");
   if (n == 0 || d_o == 0) return QZ_OK;
   if (!Y) return fail(QZ_EINVAL, w + ": null pointer");
@@ -169,6 +175,7 @@ int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8
   p.Y = Y;
   p.yt = yt;
   p.ldy = ldy;
+  set_alignment(&p);
   return launch_mx4_product(p, stream);
 }
 
@@ -200,6 +207,7 @@ int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, cons
   p.Y = Y;
   p.yt = yt;
   p.ldy = ldy;
+  set_alignment(&p);
   return launch_mx4_product(p, stream);
 }
 
@@ -217,7 +225,7 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
   if (!float_type(rt)) return fail(QZ_EINVAL, "mx4_moe: bad router dtype");
   QZ_TRY(check_moe(params));
   if (!moe_sizes(n, d, f))
-    return fail(QZ_EINVAL, "mx4_moe: need 0 <= n <= 1024, 1 <= d <= 2^24, 1 <= f <= 2^20");
+    return fail(QZ_EINVAL, "mx4_moe: need 0 <= n <= 1024, 1 <= d <= 2^20, 1 <= f <= 2^20");
   if (ldx < d) return fail(QZ_EINVAL, "mx4_moe: ldx must be at least d");
   if (n == 0) return QZ_OK;
   if (!X || !router || !Y) return fail(QZ_EINVAL, "mx4_moe: null pointer");

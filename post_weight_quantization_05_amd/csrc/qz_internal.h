@@ -275,6 +275,9 @@ struct Mx4Product {   // Y = X W^T + bias
   const uint8_t* codes; const uint8_t* scales;  // W
   const float* bias;                            // [d_o] or null
   void* Y; int yt; int64_t ldy;
+  int y_vec;                                    // four consecutive outputs are 4-element aligned
+  int factors_aligned;                          // both arrays of factors start on 4-byte boundaries
+  float* partial;                               // split sums [splits][n][d_o], or null
 };
 int launch_mx4_product(const Mx4Product& p, hipStream_t s);
 struct MoeArgs {
