@@ -184,10 +184,10 @@ struct TileShape {
   static constexpr int kFRows = BM + (X4 ? BN : 0);                     // rows of factors
   static constexpr int kFactors = kFRows * 16;
   static constexpr int kLds = G::kRing * kStage + 2 * kFactors;
-  static constexpr int kWCopies = BM * G::kWRow / 1024 / (WM * WN);     // per wavefront and stage
-  static constexpr int kXCopies = BN * G::kXRow / 1024 / (WM * WN);
-  static_assert(BM * G::kWRow % (1024 * WM * WN) == 0 && BN * G::kXRow % (1024 * WM * WN) == 0,
-                "every wavefront issues the same number of copies");
+  static constexpr int kWPieces = BM * G::kWRow / 1024, kXPieces = BN * G::kXRow / 1024;
+  static constexpr int kPieces = kWPieces + kXPieces;                   // copies of a stage
+  static constexpr int kCopies = kPieces / (WM * WN);                   // of a wavefront; the first
+  static constexpr int kExtra = kPieces % (WM * WN);                    // kExtra have one more
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -228,26 +228,28 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
   const int nst = all - st0 < stages_per_split ? all - st0 : stages_per_split;   // >= 1
   const int full = static_cast<int>(Gb / kBlocks);   // stages before the ragged one
 
-  // Copy roles: copy j of a wavefront is 1024 bytes of LDS, 1024 / row bytes whole rows.  Rows
-  // past the matrix read its last row again; their results are not stored.
-  uint32_t woff[T::kWCopies], xoff[T::kXCopies];
-  int wchunk, xchunk;
+  // Copy roles: wavefront w makes the copies w, w + kWaves, ... of a stage, 1024 bytes of LDS
+  // each, whole rows.  Rows past the matrix read its last row again; their results are not
+  // stored.
+  constexpr int kMine = T::kCopies + (T::kExtra ? 1 : 0);
+  uint32_t off[kMine];
+  constexpr int wl = Geo::kWRow / 16, xl = Geo::kXRow / 16;
+  const int wchunk = (lane % wl) ^ swz<Geo::kWRow>(lane / wl);
+  const int xchunk = (lane % xl) ^ swz<Geo::kXRow>(lane / xl);
   {
-    constexpr int wl = Geo::kWRow / 16, xl = Geo::kXRow / 16;
-    wchunk = (lane % wl) ^ swz<Geo::kWRow>(lane / wl);
-    xchunk = (lane % xl) ^ swz<Geo::kXRow>(lane / xl);
     const int64_t xp = X4 ? Gb * 16 : p.ldx * 2;
 #pragma unroll
-    for (int j = 0; j < T::kWCopies; ++j) {
-      const int row = (wave * T::kWCopies + j) * (64 / wl) + lane / wl;
-      const int64_t r = r0 + row < p.d_o ? row : p.d_o - 1 - r0;
-      woff[j] = static_cast<uint32_t>(r * Gb * 16 + 16 * wchunk);
-    }
-#pragma unroll
-    for (int j = 0; j < T::kXCopies; ++j) {
-      const int row = (wave * T::kXCopies + j) * (64 / xl) + lane / xl;
-      const int64_t t = t0 + row < p.n ? row : p.n - 1 - t0;
-      xoff[j] = static_cast<uint32_t>(t * xp + 16 * xchunk);
+    for (int j = 0; j < kMine; ++j) {
+      const int piece = wave + j * kWaves;
+      if (piece < T::kWPieces) {
+        const int row = piece * (64 / wl) + lane / wl;
+        const int64_t r = r0 + row < p.d_o ? row : p.d_o - 1 - r0;
+        off[j] = static_cast<uint32_t>(r * Gb * 16 + 16 * wchunk);
+      } else {
+        const int row = (piece - T::kWPieces) * (64 / xl) + lane / xl;
+        const int64_t t = t0 + row < p.n ? row : p.n - 1 - t0;
+        off[j] = static_cast<uint32_t>(t * xp + 16 * xchunk);
+      }
     }
   }
   const uint8_t* const wbase = p.codes + r0 * Gb * 16;
@@ -307,18 +309,13 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
     lds_u8* const dst = lds + (st % kRing) * T::kStage;
     const bool whole = st0 + st < full;
 #pragma unroll
-    for (int j = 0; j < T::kWCopies; ++j) {
-      lds_u8* const at = dst + (wave * T::kWCopies + j) * 1024;
-      if (whole || b0 + wchunk < Gb)
-        copy_lds<16>(at, wbase + b0 * 16, woff[j]);
-      else
-        *(__attribute__((address_space(3))) i32x4*)(at + 16 * lane) = i32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int j = 0; j < T::kXCopies; ++j) {
-      lds_u8* const at = dst + T::BM * Geo::kWRow + (wave * T::kXCopies + j) * 1024;
-      if (whole || b0 + (X4 ? xchunk : xchunk / 4) < Gb)
-        copy_lds<16>(at, xbase + b0 * (X4 ? 16 : 64), xoff[j]);
+    for (int j = 0; j < kMine; ++j) {
+      const int piece = wave + j * kWaves;
+      if (piece >= T::kPieces) break;
+      lds_u8* const at = dst + piece * 1024;
+      const bool w = piece < T::kWPieces;
+      if (whole || b0 + (w ? wchunk : X4 ? xchunk : xchunk / 4) < Gb)
+        copy_lds<16>(at, w ? wbase + b0 * 16 : xbase + b0 * (X4 ? 16 : 64), off[j]);
       else
         *(__attribute__((address_space(3))) i32x4*)(at + 16 * lane) = i32x4{0, 0, 0, 0};
     }
@@ -332,16 +329,16 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-  constexpr int kCopies = T::kWCopies + T::kXCopies;
   // Stage st + 1 has landed: everything but the copies of the kRing - 2 stages after it, which
-  // may be in flight where those stages are whole (each wavefront then has exactly kCopies of
-  // each; a fetch of factors only makes the wait longer).
+  // may be in flight where those stages are whole (a wavefront then has issued exactly its
+  // number of copies for each; a fetch of factors only makes the wait longer).
   auto landed = [&](int st) {
-    const bool more = st + kRing - 1 < nst && st0 + st + kRing - 1 < full;
-    if (more)
-      wait_and_join<(kRing - 2) * kCopies>();
-    else
+    if (st + kRing - 1 >= nst || st0 + st + kRing - 1 >= full)
       wait_and_join<0>();
+    else if (wave < T::kExtra)
+      wait_and_join<(kRing - 2) * (T::kCopies + 1)>();
+    else
+      wait_and_join<(kRing - 2) * T::kCopies>();
   };
 
 #pragma unroll
