@@ -405,9 +405,10 @@ int qz_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int
  *   Rows of X that are not whole blocks on 16-byte boundaries (d_i % 32, ldx % 8, the
  *   address) are first copied to the workspace.
  *   n <= 2^20, d_o <= 2^24, d_i <= 2^20; n = 0 or d_o = 0 does nothing.
- *   ws: qz_mx4_*_workspace(n, d_o, d_i) bytes, 256-byte aligned (0 bytes: may be null; 0 for
- *   bad sizes); calls that may overlap need different workspaces.  Asynchronous.          */
-size_t qz_mx4_linear_workspace(int64_t n, int64_t d_o, int64_t d_i);
+ *   ws: as many bytes as the query says for the same sizes, and for qz_mx4_linear the same X and
+ *   ldx (X = null: enough for any), 256-byte aligned; 0 bytes: may be null (0 for bad sizes too);
+ *   calls that may overlap need different workspaces.  Asynchronous.                       */
+size_t qz_mx4_linear_workspace(const void* X, int64_t n, int64_t ldx, int64_t d_o, int64_t d_i);
 int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8_t* codes,
                   const uint8_t* scales, int64_t d_o, int64_t d_i, const float* bias, void* Y,
                   int32_t yt, int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);

@@ -358,61 +358,69 @@ def qz_unpack(words, cols, bits):
 
 
 # ------------------------------------------------------------- microscaled 4-bit weights
-def _rows(t, name, dtypes):
-    """A 2-D GPU tensor of one of `dtypes` whose rows are contiguous: (pointer, row stride)."""
+# A call on a small matrix takes the GPU a few microseconds, so these functions ask torch for as
+# little as they can: device indices instead of device objects, and the raw stream handle.
+def _matrix(t, name):
+    """Row stride of a 2-D GPU tensor with contiguous rows that do not overlap."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be a matrix with contiguous rows")
-    if t.shape[0] <= 1:   # the stride of a single row is of no meaning
-        return t.data_ptr(), t.shape[1]
-    if t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), t.stride(0)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if rows <= 1:      # the stride of a single row is of no meaning
+        ld = cols
+    if (step != 1 and cols > 1) or ld < cols:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return ld
 
 
-def _mx4_pair(codes, scales, rows, cols, name, device):
-    """Checks that codes and scales store matrices of the given total rows and columns."""
-    torch = _torch()
-    blocks = -(-cols // 32)
-    for t, width, what in ((codes, 16 * blocks, "codes"), (scales, blocks, "scales")):
-        if t.dtype != torch.uint8:
-            raise TypeError(f"{name} {what} must be uint8")
-        if t.device != device or not t.is_contiguous():
-            raise ValueError(f"{name} {what} must be contiguous and on {device}")
-        if t.numel() != rows * width or t.shape[-1] != width:
-            raise ValueError(f"{name} {what}: expected {rows} rows of {width} bytes")
+def _mx4_pair(codes, scales, rows, cols, name, index):
+    """Checks that codes and scales store `rows` rows of `cols` columns, on GPU `index`."""
+    blocks = (cols + 31) >> 5
+    u8 = _torch().uint8
+    if codes.dtype != u8 or scales.dtype != u8:
+        raise TypeError(f"{name}: codes and scales must be uint8")
+    if codes.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{name}: codes and scales must be on GPU {index}")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous")
+    if codes.shape[-1] != 16 * blocks or scales.shape[-1] != blocks \
+            or codes.numel() != 16 * blocks * rows or scales.numel() != blocks * rows:
+        raise ValueError(f"{name}: expected {rows} rows of {16 * blocks} code bytes and {blocks} factors")
 
 
-def _on(device, *others):
-    """The raw current stream of `device`, where all `others` (or None) have to live too.  The
-    call itself runs with that device current."""
-    torch = _torch()
-    for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {t.device} and {device} in one call")
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _call(device, fn, *args):
-    torch = _torch()
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args))
-    else:
-        with torch.cuda.device(device):
-            _check(fn(*args))
-
-
-def _vector(t, n, name, device):
+def _vector(t, n, name, index):
     if t is None:
         return None
-    if t.dtype != _torch().float32:
+    if t.dtype is not _torch().float32:
         raise TypeError(f"{name} must be fp32")
-    if t.device != device or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous values on {device}")
+    if t.get_device() != index or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values on GPU {index}")
     return t.data_ptr()
+
+
+def _scratch(ws, need, device):
+    """(pointer, size) of a workspace of `need` bytes: the caller's, a new one, or none."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = _workspace(need, device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the inputs' GPU")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def _run(index, fn, *args):
+    """fn(*args, stream) on the current stream of GPU `index`, with that GPU current."""
+    cuda = _torch()._C
+    if cuda._cuda_getDevice() == index:
+        st = fn(*args, cuda._cuda_getCurrentRawStream(index))
+    else:
+        with _torch().cuda.device(index):
+            st = fn(*args, cuda._cuda_getCurrentRawStream(index))
+    if st != 0:
+        _check(st)
 
 
 def qz_mx4_blocks(cols) -> int:
@@ -424,19 +432,21 @@ def qz_mx4_quantize(W, rule="floor", colw=None, values=False):
     [rows x G] uint8), and with values=True the numbers they stand for in W's dtype.  rule
     "floor", or "least" (the better of two factors per block under the column weights colw)."""
     torch = _torch()
-    ptr, ld = _rows(W, "W", (torch.bfloat16, torch.float32))
+    ld = _matrix(W, "W")
+    wt = _dtype_code(W)
     rows, cols = W.shape
     if cols < 1:
         raise ValueError("W has no columns")
-    k = {"floor": _lib.QZ_MX4_FLOOR, "least": _lib.QZ_MX4_LEAST}[rule]
-    dev, blocks = W.device, -(-cols // 32)
-    stream = _on(dev)
+    if rule not in ("floor", "least"):
+        raise ValueError(f"rule must be 'floor' or 'least', not {rule!r}")
+    dev, blocks = W.device, (cols + 31) >> 5
     codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=dev)
     scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
     out = torch.empty((rows, cols), dtype=W.dtype, device=dev) if values else None
-    _call(dev, lib().qz_mx4_quantize, ptr, _dtype_code(W), rows, cols, ld, k,
-          _vector(colw, cols, "colw", dev), codes.data_ptr(), scales.data_ptr(),
-          out.data_ptr() if values else None, stream)
+    _run(dev.index, lib().qz_mx4_quantize, W.data_ptr(), wt, rows, cols, ld,
+         _lib.QZ_MX4_LEAST if rule == "least" else _lib.QZ_MX4_FLOOR,
+         _vector(colw, cols, "colw", dev.index), codes.data_ptr(), scales.data_ptr(),
+         out.data_ptr() if values else None)
     return (codes, scales, out) if values else (codes, scales)
 
 
@@ -446,43 +456,47 @@ def qz_mx4_unpack(codes, scales, cols):
     torch = _torch()
     _dev(codes, "codes")
     rows, dev = codes.shape[0], codes.device
-    _mx4_pair(codes, scales, rows, cols, "MX4", dev)
+    _mx4_pair(codes, scales, rows, cols, "matrix", dev.index)
     out = torch.empty((rows, cols), dtype=torch.int32, device=dev)
     s = torch.empty(scales.shape, dtype=torch.float32, device=dev)
     z = torch.empty(scales.shape, dtype=torch.uint8, device=dev)
-    _call(dev, lib().qz_mx4_unpack, codes.data_ptr(), scales.data_ptr(), rows, cols, out.data_ptr(),
-          s.data_ptr(), z.data_ptr(), _on(dev))
+    _run(dev.index, lib().qz_mx4_unpack, codes.data_ptr(), scales.data_ptr(), rows, cols,
+         out.data_ptr(), s.data_ptr(), z.data_ptr())
     return out, s, z
 
 
 def _product_out(out, n, d_o, dtype, device):
+    """(out, its row stride, its dtype code) for a product's result."""
     torch = _torch()
     if out is None:
         out = torch.empty((n, d_o), dtype=dtype or torch.bfloat16, device=device)
-    elif tuple(out.shape) != (n, d_o) or (dtype is not None and out.dtype != dtype):
+        return out, d_o, _dtype_code(out)
+    if tuple(out.shape) != (n, d_o) or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must be [{n} x {d_o}]" + (f" {dtype}" if dtype is not None else ""))
-    ptr, ld = _rows(out, "out", (torch.bfloat16, torch.float32))
-    return out, ptr, max(ld, d_o)
+    if out.device != device:
+        raise ValueError(f"out must be on {device}")
+    return out, _matrix(out, "out"), _dtype_code(out)
 
 
 def qz_mx4_linear_workspace(n, d_o, d_i) -> int:
-    return lib().qz_mx4_linear_workspace(n, d_o, d_i)
+    """Bytes that suffice for any address and row stride of X."""
+    return lib().qz_mx4_linear_workspace(None, n, 0, d_o, d_i)
 
 
 def qz_mx4_linear(X, codes, scales, bias=None, out_dtype=None, out=None, ws=None):
     """Y = X W^T + bias for X bf16 [n x d_i] (contiguous rows) and W [d_o x d_i] in MX4.  Y is
     out_dtype (bf16 or fp32; default bf16), or `out` is written."""
-    torch = _torch()
-    ptr, ldx = _rows(X, "X", (torch.bfloat16,))
-    (n, d_i), d_o, dev = X.shape, codes.shape[0], X.device
-    _mx4_pair(codes, scales, d_o, d_i, "W", dev)
-    stream = _on(dev, out, ws)
-    out, yp, ldy = _product_out(out, n, d_o, out_dtype, dev)
-    if ws is None:
-        ws = _workspace(lib().qz_mx4_linear_workspace(n, d_o, d_i), dev)
-    _call(dev, lib().qz_mx4_linear, ptr, _lib.QZ_BF16, n, ldx, codes.data_ptr(), scales.data_ptr(),
-          d_o, d_i, _vector(bias, d_o, "bias", dev), yp, _dtype_code(out), ldy, ws.data_ptr(),
-          ws.numel(), stream)
+    L = lib()
+    ldx = _matrix(X, "X")
+    if _dtype_code(X) != _lib.QZ_BF16:
+        raise TypeError("X must be bf16")
+    (n, d_i), d_o, dev, x = X.shape, codes.shape[0], X.device, X.data_ptr()
+    index = dev.index
+    _mx4_pair(codes, scales, d_o, d_i, "W", index)
+    out, ldy, yt = _product_out(out, n, d_o, out_dtype, dev)
+    wp, wn, ws = _scratch(ws, L.qz_mx4_linear_workspace(x, n, ldx, d_o, d_i), dev)
+    _run(index, L.qz_mx4_linear, x, _lib.QZ_BF16, n, ldx, codes.data_ptr(), scales.data_ptr(), d_o,
+         d_i, _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy, wp, wn)
     return out
 
 
@@ -492,17 +506,17 @@ def qz_mx4_matmul_workspace(n, d_o, d_i) -> int:
 
 def qz_mx4_matmul(xcodes, xscales, codes, scales, d_i, bias=None, out_dtype=None, out=None, ws=None):
     """Y = X W^T + bias with X [n x d_i] and W [d_o x d_i] both in MX4."""
+    L = lib()
     _dev(xcodes, "X codes")
     n, d_o, dev = xcodes.shape[0], codes.shape[0], xcodes.device
-    _mx4_pair(xcodes, xscales, n, d_i, "X", dev)
-    _mx4_pair(codes, scales, d_o, d_i, "W", dev)
-    stream = _on(dev, out, ws)
-    out, yp, ldy = _product_out(out, n, d_o, out_dtype, dev)
-    if ws is None:
-        ws = _workspace(lib().qz_mx4_matmul_workspace(n, d_o, d_i), dev)
-    _call(dev, lib().qz_mx4_matmul, xcodes.data_ptr(), xscales.data_ptr(), n, codes.data_ptr(),
-          scales.data_ptr(), d_o, d_i, _vector(bias, d_o, "bias", dev), yp, _dtype_code(out), ldy,
-          ws.data_ptr(), ws.numel(), stream)
+    index = dev.index
+    _mx4_pair(xcodes, xscales, n, d_i, "X", index)
+    _mx4_pair(codes, scales, d_o, d_i, "W", index)
+    out, ldy, yt = _product_out(out, n, d_o, out_dtype, dev)
+    wp, wn, ws = _scratch(ws, L.qz_mx4_matmul_workspace(n, d_o, d_i), dev)
+    _run(index, L.qz_mx4_matmul, xcodes.data_ptr(), xscales.data_ptr(), n, codes.data_ptr(),
+         scales.data_ptr(), d_o, d_i, _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy,
+         wp, wn)
     return out
 
 
@@ -519,29 +533,33 @@ def qz_mx4_moe(X, router, gu_codes, gu_scales, dn_codes, dn_scales, top_k, renor
     """The routed expert layer for few tokens: X bf16 [n x d], router [E x d] (bf16 or fp32),
     gate and up weights [E x 2f x d] and down weights [E x d x f] in MX4.  Returns Y bf16
     [n x d], and with routing=True also (ids int32, weights fp32) [n x top_k]."""
-    torch = _torch()
-    ptr, ldx = _rows(X, "X", (torch.bfloat16,))
-    (n, d), dev = X.shape, X.device
-    _dev(router, "router")
+    torch, L = _torch(), lib()
+    ldx = _matrix(X, "X")
+    if _dtype_code(X) != _lib.QZ_BF16:
+        raise TypeError("X must be bf16")
+    (n, d), dev, k = X.shape, X.device, int(top_k)
+    index = dev.index
     if router.dim() != 2 or router.shape[1] != d or gu_codes.dim() != 3 or gu_codes.shape[1] % 2:
         raise ValueError("router must be [E x d], the gate and up weights [E x 2f x d]")
+    if router.get_device() != index or not router.is_contiguous():
+        raise ValueError("router must be contiguous and on the inputs' GPU")
     E, f = router.shape[0], gu_codes.shape[1] // 2
-    if gu_codes.shape[0] != E or tuple(dn_codes.shape[:2]) != (E, d):
+    if gu_codes.shape[0] != E or dn_codes.dim() != 3 or dn_codes.shape[0] != E or dn_codes.shape[1] != d:
         raise ValueError("the experts' weights must be [E x 2f x d] and [E x d x f]")
-    _mx4_pair(gu_codes, gu_scales, E * 2 * f, d, "gate and up", dev)
-    _mx4_pair(dn_codes, dn_scales, E * d, f, "down", dev)
-    stream = _on(dev, router, ws)
-    p = _moe_params(E, top_k, renorm)
-    if ws is None:
-        ws = _workspace(lib().qz_mx4_moe_workspace(n, d, f, C.byref(p)), dev)
-    k = max(int(top_k), 0)
+    _mx4_pair(gu_codes, gu_scales, E * 2 * f, d, "gate and up weights", index)
+    _mx4_pair(dn_codes, dn_scales, E * d, f, "down weights", index)
+    p = C.byref(_moe_params(E, k, renorm))
+    wp, wn, ws = _scratch(ws, L.qz_mx4_moe_workspace(n, d, f, p), dev)
     y = torch.empty((n, d), dtype=torch.bfloat16, device=dev)
-    ids = torch.empty((n, k), dtype=torch.int32, device=dev) if routing else None
-    w = torch.empty((n, k), dtype=torch.float32, device=dev) if routing else None
-    _call(dev, lib().qz_mx4_moe, ptr, _lib.QZ_BF16, n, ldx, d, f, C.byref(p), router.data_ptr(),
-          _dtype_code(router), gu_codes.data_ptr(), gu_scales.data_ptr(), dn_codes.data_ptr(),
-          dn_scales.data_ptr(), y.data_ptr(), ids.data_ptr() if routing else None,
-          w.data_ptr() if routing else None, ws.data_ptr(), ws.numel(), stream)
+    if routing and k > 0:
+        ids = torch.empty((n, k), dtype=torch.int32, device=dev)
+        w = torch.empty((n, k), dtype=torch.float32, device=dev)
+        ip, kp = ids.data_ptr(), w.data_ptr()
+    else:
+        ip = kp = None
+    _run(index, L.qz_mx4_moe, X.data_ptr(), _lib.QZ_BF16, n, ldx, d, f, p, router.data_ptr(),
+         _dtype_code(router), gu_codes.data_ptr(), gu_scales.data_ptr(), dn_codes.data_ptr(),
+         dn_scales.data_ptr(), y.data_ptr(), ip, kp, wp, wn)
     return (y, ids, w) if routing else y
 
 

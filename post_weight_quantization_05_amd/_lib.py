@@ -97,7 +97,7 @@ _SIGS = {
     "qz_mx4_blocks": (I64, [I64]),
     "qz_mx4_quantize": (C.c_int, [P, I32, I64, I64, I64, I32, P, P, P, P, P]),
     "qz_mx4_unpack": (C.c_int, [P, P, I64, I64, P, P, P, P]),
-    "qz_mx4_linear_workspace": (SZ, [I64, I64, I64]),
+    "qz_mx4_linear_workspace": (SZ, [P, I64, I64, I64, I64]),
     "qz_mx4_linear": (C.c_int, [P, I32, I64, I64, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),
     "qz_mx4_matmul_workspace": (SZ, [I64, I64, I64]),
     "qz_mx4_matmul": (C.c_int, [P, P, I64, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),

@@ -39,10 +39,25 @@ bool direct_x(const void* X, int64_t d_i, int64_t ldx) {
   return d_i % kMxBlock == 0 && ldx % 8 == 0 && ldx <= 2 * kMaxCols && aligned(X, 16);
 }
 
-size_t linear_ws(int64_t n, int64_t d_i) {
-  Carver c(nullptr);
-  c.take<uint16_t>(static_cast<size_t>(n) * mx_blocks(d_i) * kMxBlock);
-  return c.used;
+// X's rows copied to whole blocks, and the sums of a split product.
+struct ProductWs {
+  uint16_t* xpad;
+  float* partial;
+  size_t bytes;
+};
+ProductWs product_ws(void* base, bool x4, bool pad, int64_t n, int64_t d_o, int64_t d_i) {
+  Carver c(base);
+  ProductWs w;
+  w.xpad = c.take<uint16_t>(pad ? static_cast<size_t>(n) * mx_blocks(d_i) * kMxBlock : 0);
+  const int64_t splits = n > 0 && d_o > 0 ? mx4_product_splits(x4, n, d_o, mx_blocks(d_i)) : 1;
+  w.partial = c.take<float>(splits > 1 ? static_cast<size_t>(splits) * n * d_o : 0);
+  w.bytes = c.used;
+  if (splits <= 1) w.partial = nullptr;
+  return w;
+}
+
+bool product_sizes(int64_t n, int64_t d_o, int64_t d_i) {
+  return n >= 0 && n <= kMaxTokens && d_o >= 0 && d_o <= kMaxRows && d_i >= 1 && d_i <= kMaxCols;
 }
 
 // What the kernels may assume of the output and of the factors.
@@ -129,7 +144,7 @@ static int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i,
                          int32_t yt, int64_t ldy) {
   const std::string w(who);
   if (!float_type(yt)) return fail(QZ_EINVAL, w + ": bad output dtype");
-  if (n < 0 || n > kMaxTokens || d_o < 0 || d_o > kMaxRows || d_i < 1 || d_i > kMaxCols)
+  if (!product_sizes(n, d_o, d_i))
     return fail(QZ_EINVAL, w + ": need 0 <= n <= 2^20, 0 <= d_o <= 2^24, 1 <= d_i <= 2^20");
   if (ldy < d_o) return fail(QZ_EINVAL, w + ": ldy must be at least d_o");
   if (n == 0 || d_o == 0) return QZ_OK;
@@ -140,9 +155,9 @@ static int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i,
   return QZ_OK;
 }
 
-size_t qz_mx4_linear_workspace(int64_t n, int64_t d_o, int64_t d_i) {
-  if (n < 0 || n > kMaxTokens || d_o < 0 || d_o > kMaxRows || d_i < 1 || d_i > kMaxCols) return 0;
-  return linear_ws(n, d_i);
+size_t qz_mx4_linear_workspace(const void* X, int64_t n, int64_t ldx, int64_t d_o, int64_t d_i) {
+  if (!product_sizes(n, d_o, d_i)) return 0;
+  return product_ws(nullptr, false, !X || !direct_x(X, d_i, ldx), n, d_o, d_i).bytes;
 }
 
 int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8_t* codes,
@@ -154,7 +169,9 @@ int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8
   if (n == 0 || d_o == 0) return QZ_OK;
   if (!X) return fail(QZ_EINVAL, "mx4_linear: null pointer");
   if (!aligned(X, 2)) return fail(QZ_EINVAL, "mx4_linear: arrays must be aligned to their elements");
-  QZ_TRY(check_ws("mx4_linear", ws, ws_bytes, linear_ws(n, d_i)));
+  const bool pad = !direct_x(X, d_i, ldx);
+  const ProductWs w = product_ws(ws, false, pad, n, d_o, d_i);
+  QZ_TRY(check_ws("mx4_linear", ws, ws_bytes, w.bytes));
   set_error("");
   ScopedTimer tm(K_MX4_PRODUCT, stream);
   Mx4Product p{};
@@ -163,11 +180,11 @@ int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8
   p.G = mx_blocks(d_i);
   p.X = static_cast<const uint16_t*>(X);
   p.ldx = ldx;
-  if (!direct_x(X, d_i, ldx)) {
+  p.partial = w.partial;
+  if (pad) {
     p.ldx = p.G * kMxBlock;
-    p.X = static_cast<const uint16_t*>(ws);
-    QZ_TRY(launch_mx4_pad(static_cast<const uint16_t*>(X), n, d_i, ldx, static_cast<uint16_t*>(ws),
-                          p.ldx, stream));
+    p.X = w.xpad;
+    QZ_TRY(launch_mx4_pad(static_cast<const uint16_t*>(X), n, d_i, ldx, w.xpad, p.ldx, stream));
   }
   p.codes = codes;
   p.scales = scales;
@@ -180,10 +197,8 @@ int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8
 }
 
 size_t qz_mx4_matmul_workspace(int64_t n, int64_t d_o, int64_t d_i) {
-  (void)n;
-  (void)d_o;
-  (void)d_i;
-  return 0;
+  if (!product_sizes(n, d_o, d_i)) return 0;
+  return product_ws(nullptr, true, false, n, d_o, d_i).bytes;
 }
 
 int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, const uint8_t* codes,
@@ -192,7 +207,8 @@ int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, cons
   QZ_TRY(check_product("mx4_matmul", n, d_o, d_i, codes, scales, bias, Y, yt, ldy));
   if (n == 0 || d_o == 0) return QZ_OK;
   QZ_TRY(check_codes("mx4_matmul", xcodes, xscales));
-  QZ_TRY(check_ws("mx4_matmul", ws, ws_bytes, qz_mx4_matmul_workspace(n, d_o, d_i)));
+  const ProductWs w = product_ws(ws, true, false, n, d_o, d_i);
+  QZ_TRY(check_ws("mx4_matmul", ws, ws_bytes, w.bytes));
   set_error("");
   ScopedTimer tm(K_MX4_PRODUCT, stream);
   Mx4Product p{};
@@ -201,6 +217,7 @@ int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, cons
   p.G = mx_blocks(d_i);
   p.xcodes = xcodes;
   p.xscales = xscales;
+  p.partial = w.partial;
   p.codes = codes;
   p.scales = scales;
   p.bias = bias;

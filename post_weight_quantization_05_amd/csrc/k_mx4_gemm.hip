@@ -123,9 +123,9 @@ __device__ __forceinline__ void store4(const Mx4Product& p, int split, int64_t t
 // as both operands agree on it.
 //
 // LDS rows hold kBlocks 16-byte chunks (codes) or 8 (bf16 X of two blocks).  Chunk c of row r
-// lies at chunk c ^ swz(r), with swz stepping once per 128 bytes of rows, so the eight lanes
-// that an LDS read serves at a time touch eight different bank groups.  The copies keep LDS
-// linear and permute their global sources instead.
+// lies at chunk c ^ swz(r), with swz stepping once per 256 bytes of rows, so that 16 rows at the
+// same column touch all 64 banks (stepping once per 128 bytes cost half of the LDS cycles in
+// conflicts).  The copies keep LDS linear and permute their global sources instead.
 //
 // Factors come 16 blocks of a row at a time, by 4-byte copies where rows of factors are
 // 4-byte aligned (G % 4 == 0 and the base), through registers otherwise.
@@ -142,7 +142,7 @@ struct TileGeom<false> {   // 64 columns a stage: 32 bytes of codes, 128 bytes o
 
 template <int RB>
 __device__ __forceinline__ int swz(int row) {
-  return (row / (128 / RB)) & (RB / 16 - 1);
+  return (row / (256 / RB)) & (RB / 16 - 1);
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
@@ -234,8 +234,10 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
   constexpr int kMine = T::kCopies + (T::kExtra ? 1 : 0);
   uint32_t off[kMine];
   constexpr int wl = Geo::kWRow / 16, xl = Geo::kXRow / 16;
-  const int wchunk = (lane % wl) ^ swz<Geo::kWRow>(lane / wl);
-  const int xchunk = (lane % xl) ^ swz<Geo::kXRow>(lane / xl);
+  const int wchunk = (lane % wl) ^ swz<Geo::kWRow>(lane / wl);   // swz repeats after 16 rows
+  auto xchunk = [&](int piece) {   // a copy of bf16 X is only 8 rows
+    return (lane % xl) ^ swz<Geo::kXRow>((piece - T::kWPieces) * (64 / xl) + lane / xl);
+  };
   {
     const int64_t xp = X4 ? Gb * 16 : p.ldx * 2;
 #pragma unroll
@@ -248,7 +250,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
       } else {
         const int row = (piece - T::kWPieces) * (64 / xl) + lane / xl;
         const int64_t t = t0 + row < p.n ? row : p.n - 1 - t0;
-        off[j] = static_cast<uint32_t>(t * xp + 16 * xchunk);
+        off[j] = static_cast<uint32_t>(t * xp + 16 * xchunk(piece));
       }
     }
   }
@@ -314,7 +316,7 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
       if (piece >= T::kPieces) break;
       lds_u8* const at = dst + piece * 1024;
       const bool w = piece < T::kWPieces;
-      if (whole || b0 + (w ? wchunk : X4 ? xchunk : xchunk / 4) < Gb)
+      if (whole || b0 + (w ? wchunk : X4 ? xchunk(piece) : xchunk(piece) / 4) < Gb)
         copy_lds<16>(at, w ? wbase + b0 * 16 : xbase + b0 * (X4 ? 16 : 64), off[j]);
       else
         *(__attribute__((address_space(3))) i32x4*)(at + 16 * lane) = i32x4{0, 0, 0, 0};
@@ -475,6 +477,8 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
                      0, s, X, n, d_i, ldx, out, ldo);
   return check_launch("mx4_pad");
 }
+
+int mx4_product_splits(bool, int64_t, int64_t, int64_t) { return 1; }
 
 int launch_mx4_product(const Mx4Product& p, hipStream_t s) {
   if (p.n > 64 && p.d_o >= 64)

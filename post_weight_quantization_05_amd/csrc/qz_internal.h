@@ -279,6 +279,8 @@ struct Mx4Product {   // Y = X W^T + bias
   int factors_aligned;                          // both arrays of factors start on 4-byte boundaries
   float* partial;                               // split sums [splits][n][d_o], or null
 };
+// parts of the contraction whose sums go through p.partial (1: none, partial unused)
+int mx4_product_splits(bool x4, int64_t n, int64_t d_o, int64_t G);
 int launch_mx4_product(const Mx4Product& p, hipStream_t s);
 struct MoeArgs {
   int64_t n, d, f, Gd, Gf;                      // Gd, Gf: blocks of rows of d and f columns
