@@ -1,5 +1,7 @@
 // Microscaled 4-bit (MX4) quantisation: round-to-nearest of a matrix on E2M1 elements with
 // one power-of-two factor per 32 columns of a row.
+#include <type_traits>
+
 #include "mx4.h"
 
 namespace qz {
@@ -52,23 +54,26 @@ __device__ __forceinline__ void widen8(uint32_t q, float factor, float (&x)[8]) 
 
 // Squared error of eight elements in 64 bits.  w - q is exact in fp32 (q is 0 or within a factor
 // of two of w, or w saturates at less than twice the top), so only the sums round.
+template <bool WEIGHTED>
 __device__ __forceinline__ double error8(const float (&v)[8], const float (&x)[8],
-                                         const float* h) {
+                                         const float (&h)[8]) {
   double s = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const double d = v[i] - x[i];
-    s = h ? fma(d * d, static_cast<double>(h[i]), s) : fma(d, d, s);
+    s = WEIGHTED ? fma(d * d, static_cast<double>(h[i]), s) : fma(d, d, s);
   }
   return s;
 }
 
 // Four lanes per block, eight columns each: every load and store of a wavefront is contiguous
 // (bf16: 16 bytes a lane), and the block's maximum and sums are two moves inside the quad.  The
-// work is one pass over W, bound by HBM.  VEC: rows of W (and of `values`) start on 16-byte
+// work is one pass over W, bound by HBM.  VEC: rows of W and of `values`, and colw, start on 16-byte
 // boundaries and are whole chunks of eight; other rows go element by element.  Idx: 32-bit where
 // the chunks' index fits, since its division is the longest computation of the FLOOR rule.
-template <int WT, bool LEAST, bool VEC, class Idx>
+enum Rule { kFloor, kLeast, kLeastWeighted };
+
+template <int WT, Rule RULE, bool VEC, class Idx>
 __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(
     const void* __restrict__ W, int64_t rows, int64_t cols, int64_t ldw,
     const float* __restrict__ colw, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales,
@@ -118,17 +123,27 @@ __global__ __launch_bounds__(kThreads) void mx4_quantize_kernel(
     const uint32_t ex = quad_max(top) >> 23;
     uint32_t e = ex > 2 ? ex - 2 : 0;
     uint32_t q = round8(v, mx_factor(e));
-    if constexpr (LEAST) {
+    if constexpr (RULE != kFloor) {
       float h[8], x[8], y[8];
-      if (colw) {
+      if constexpr (RULE == kLeastWeighted) {
+        if constexpr (VEC) {
+          const f32x4* p = reinterpret_cast<const f32x4*>(colw + (left > 0 ? c0 : 0));
+          const f32x4 a = p[0], b = p[1];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = i < left ? colw[c0 + i] : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            h[i] = a[i];
+            h[4 + i] = b[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[i] = i < left ? colw[c0 + i] : 0.f;
+        }
       }
       const uint32_t q1 = round8(v, mx_factor(e + 1));
       widen8(q, mx_factor(e), x);
       widen8(q1, mx_factor(e + 1), y);
-      const double d0 = quad_sum(error8(v, x, colw ? h : nullptr));
-      const double d1 = quad_sum(error8(v, y, colw ? h : nullptr));
+      const double d0 = quad_sum(error8<RULE == kLeastWeighted>(v, x, h));
+      const double d1 = quad_sum(error8<RULE == kLeastWeighted>(v, y, h));
       if (d1 < d0) {   // the same in the four lanes: both sums add the same pairs
         q = q1;
         e += 1;
@@ -206,12 +221,12 @@ int grid_for(int64_t items) {
 
 namespace {
 
-template <int WT, bool LEAST>
+template <int WT, Rule RULE>
 int quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, const float* colw,
              uint8_t* codes, uint8_t* scales, void* values, hipStream_t s) {
   const size_t size = WT == QZ_BF16 ? 2 : 4;
   auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-  const bool vec = cols % 8 == 0 && ldw * size % 16 == 0 && on16(W) && on16(values);
+  const bool vec = cols % 8 == 0 && ldw * size % 16 == 0 && on16(W) && on16(values) && on16(colw);
   const int64_t items = rows * mx_blocks(cols) * 4;
   const dim3 g(grid_for(items));
   // the grid's stride may carry the 32-bit index past the end once
@@ -220,9 +235,9 @@ int quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, const float
     hipLaunchKernelGGL(kernel, g, dim3(kThreads), 0, s, W, rows, cols, ldw, colw, codes, scales, values);
     return check_launch("mx4_quantize");
   };
-  if (!narrow) return go(mx4_quantize_kernel<WT, LEAST, false, uint64_t>);
-  return vec ? go(mx4_quantize_kernel<WT, LEAST, true, uint32_t>)
-             : go(mx4_quantize_kernel<WT, LEAST, false, uint32_t>);
+  if (!narrow) return go(mx4_quantize_kernel<WT, RULE, false, uint64_t>);
+  return vec ? go(mx4_quantize_kernel<WT, RULE, true, uint32_t>)
+             : go(mx4_quantize_kernel<WT, RULE, false, uint32_t>);
 }
 
 }  // namespace
@@ -230,9 +245,15 @@ int quantize(const void* W, int64_t rows, int64_t cols, int64_t ldw, const float
 int launch_mx4_quantize(const void* W, int wt, int64_t rows, int64_t cols, int64_t ldw, int rule,
                         const float* colw, uint8_t* codes, uint8_t* scales, void* values,
                         hipStream_t s) {
-  const auto f = wt == QZ_BF16 ? (rule == QZ_MX4_LEAST ? quantize<QZ_BF16, true> : quantize<QZ_BF16, false>)
-                               : (rule == QZ_MX4_LEAST ? quantize<QZ_F32, true> : quantize<QZ_F32, false>);
-  return f(W, rows, cols, ldw, colw, codes, scales, values, s);
+  auto by_rule = [&](auto type) {
+    constexpr int WT = decltype(type)::value;
+    const auto f = rule != QZ_MX4_LEAST ? quantize<WT, kFloor>
+                   : colw               ? quantize<WT, kLeastWeighted>
+                                        : quantize<WT, kLeast>;
+    return f(W, rows, cols, ldw, colw, codes, scales, values, s);
+  };
+  return wt == QZ_BF16 ? by_rule(std::integral_constant<int, QZ_BF16>{})
+                       : by_rule(std::integral_constant<int, QZ_F32>{});
 }
 
 int launch_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
