@@ -229,29 +229,37 @@ int launch_skinny(const Mx4Product& p, int waves, hipStream_t s) {
 // ---------------------------------------------------------------------------- large products
 // Workgroup tile of BM rows of W by BN rows of X (tokens), BM = 32 MT WM, BN = 32 NT WN, in
 // WM x WN wavefronts of 32 MT x 32 NT each.  Codes (and bf16 X) stream into LDS by
-// global_load_lds, `kBlocks` blocks of every row a stage, `kRing` stages deep; weights are
-// widened in registers on the way from LDS to the matrix cores.  In a stage lane l holds row
-// (or token) l % 32 of a 32-row tile and, of each pair of blocks, block l / 32, so a lane's
-// operand is one 16-byte read with one factor; the order of the contraction is free as long
-// as both operands agree on it.
+// global_load_lds; weights are widened in registers between LDS and the matrix cores.  Of a pair
+// of blocks, lane l holds row (or token) l % 32 of a 32-row tile and block l / 32 of the pair, so
+// an operand is one 16-byte read with one factor; the order of the contraction is free as long as
+// both operands agree on it.
 //
-// LDS rows hold kBlocks 16-byte chunks (codes) or 8 (bf16 X of two blocks).  Chunk c of row r
-// lies at chunk c ^ swz(r), with swz stepping once per 256 bytes of rows, so that 16 rows at the
-// same column touch all 64 banks (stepping once per 128 bytes cost half of the LDS cycles in
-// conflicts).  The copies keep LDS linear and permute their global sources instead.
-//
-// Factors come 16 blocks of a row at a time, by 4-byte copies where rows of factors are
-// 4-byte aligned (G % 4 == 0 and the base), through registers otherwise.
+// What sets the shapes: a compute unit takes about one row segment (up to a 128-byte line) from
+// L2 in 3.5 clocks, whatever its length (measured on the copies alone: 14 B/clk in 64-byte pieces,
+// 23 with mostly 128-byte ones), and 32 x 32 products of 64 columns take 32 clocks of a SIMD.  So:
+//   X in MX4: stages of 256 columns, 128 bytes of a row on both sides, two of them in LDS;
+//   X in bf16: stages of 64 columns of X (128 bytes a row), three in LDS, and W in pairs of
+//   stages (64 bytes a row), two pairs in LDS, half the rows of a pair copied with each stage;
+//   factors: 64 of a row at a time (a fetch costs a request a row, like a stage).
+// LDS rows are swizzled in 16-byte chunks: chunk c of row r lies at chunk c ^ swz(r), stepping
+// once per 256 bytes of rows, so that 16 rows at the same column touch all 64 banks (stepping
+// once per 128 bytes cost half of the LDS cycles in conflicts).  The copies keep LDS linear and
+// permute their global sources instead.
 template <bool X4>
 struct TileGeom;
 template <>
-struct TileGeom<true> {    // 128 columns a stage: 64 bytes of codes a row on both sides
-  static constexpr int kBlocks = 4, kRing = 4, kWRow = 64, kXRow = 64;
+struct TileGeom<true> {
+  static constexpr int kBlocks = 8, kRing = 2;      // of a stage; stages in LDS
+  static constexpr int kWRow = 128, kXRow = 128;    // bytes of an LDS row
+  static constexpr int kWParts = 1;                 // stages that share a W buffer
 };
 template <>
-struct TileGeom<false> {   // 64 columns a stage: 32 bytes of codes, 128 bytes of X a row
-  static constexpr int kBlocks = 2, kRing = 3, kWRow = 32, kXRow = 128;
+struct TileGeom<false> {
+  static constexpr int kBlocks = 2, kRing = 3;
+  static constexpr int kWRow = 64, kXRow = 128;
+  static constexpr int kWParts = 2;
 };
+constexpr int kFetch = 64;   // factors of a row in LDS
 
 template <int RB>
 __device__ __forceinline__ int swz(int row) {
@@ -291,17 +299,24 @@ __device__ __forceinline__ void wait_and_join() {
 template <bool X4, int WM, int WN, int MT, int NT>
 struct TileShape {
   using G = TileGeom<X4>;
-  static constexpr int kThreads = WM * WN * 64;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
-  static constexpr int kStage = BM * G::kWRow + BN * G::kXRow;          // bytes of a stage
-  static constexpr int kFRows = BM + (X4 ? BN : 0);                     // rows of factors
-  static constexpr int kFactors = kFRows * 16;
-  static constexpr int kLds = G::kRing * kStage + 2 * kFactors;
-  static constexpr int kWPieces = BM * G::kWRow / 1024, kXPieces = BN * G::kXRow / 1024;
-  static constexpr int kPieces = kWPieces + kXPieces;                   // copies of a stage
-  static constexpr int kCopies = kPieces / (WM * WN);                   // of a wavefront; the first
-  static constexpr int kExtra = kPieces % (WM * WN);                    // kExtra have one more
-  static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+  static constexpr int kWBytes = BM * G::kWRow, kXBytes = BN * G::kXRow;   // of a buffer
+  static constexpr int kWBuffers = G::kWParts == 1 ? G::kRing : 2;
+  static constexpr int kFRows = BM + (X4 ? BN : 0);                        // rows of factors
+  static constexpr int kLds = kWBuffers * kWBytes + G::kRing * kXBytes + kFRows * kFetch;
+  // copies (1024 bytes of LDS each) of a stage: a part of a W buffer and an X buffer
+  static constexpr int kWPieces = kWBytes / 1024 / G::kWParts, kXPieces = kXBytes / 1024;
+  static constexpr int kPieces = kWPieces + kXPieces;
+  static constexpr int kCopies = kPieces / kWaves;   // of a wavefront; the first kExtra have one more
+  static constexpr int kExtra = kPieces % kWaves;
+  static constexpr int kXLeast = kCopies - (kWPieces + kWaves - 1) / kWaves;   // of X, at least
+  static_assert(G::kRing == 2 || (G::kRing == 3 && kXLeast >= 0), "the waits of a stage");
+  // the results of 32 tokens of a wavefront, on their way to whole lines of Y
+  static constexpr int kOutPitch = 32 * MT * 4 + 16;
+  static constexpr int kOut = kWaves * 32 * kOutPitch;
+  static constexpr int kShared = kLds > kOut ? kLds : kOut;
+  static_assert(kShared <= 160 * 1024, "LDS of a compute unit");
 };
 
 template <bool X4, int WM, int WN, int MT, int NT>
@@ -309,11 +324,12 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
                                                                 int tiles_x, int stages_per_split) {
   using T = TileShape<X4, WM, WN, MT, NT>;
   using Geo = TileGeom<X4>;
-  constexpr int kWaves = WM * WN, kRing = Geo::kRing, kBlocks = Geo::kBlocks;
-  constexpr int kPer = 16 / kBlocks;   // stages that one fetch of factors serves
+  constexpr int kRing = Geo::kRing, kBlocks = Geo::kBlocks, kParts = Geo::kWParts;
+  constexpr int kPer = kFetch / kBlocks;   // stages that one fetch of factors serves
   extern __shared__ __align__(1024) uint8_t smem[];
-  lds_u8* const lds = (lds_u8*)smem;
-  lds_u8* const fac = lds + kRing * T::kStage;
+  lds_u8* const lds_w = (lds_u8*)smem;
+  lds_u8* const lds_x = lds_w + T::kWBuffers * T::kWBytes;
+  lds_u8* const lds_f = lds_x + kRing * T::kXBytes;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -332,107 +348,114 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
   const int in_group = kGroup * tiles_x;
   const int g0 = pid / in_group * kGroup;
   const int gh = tiles_w - g0 < kGroup ? tiles_w - g0 : kGroup;
-  const int64_t r0 = static_cast<int64_t>(g0 + pid % in_group % gh) * T::BM;
-  const int64_t t0 = static_cast<int64_t>(pid % in_group / gh) * T::BN;
+  // (the divisions leave the uniform tile in vector registers, and with it every address)
+  const int64_t r0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(g0 + pid % in_group % gh)) * T::BM;
+  const int64_t t0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(pid % in_group / gh)) * T::BN;
+  // last rows inside the matrices, counted in the tile: rows past them read these again
+  const int last_r = static_cast<int>(p.d_o - 1 - r0 < T::BM ? p.d_o - 1 - r0 : T::BM);
+  const int last_t = static_cast<int>(p.n - 1 - t0 < T::BN ? p.n - 1 - t0 : T::BN);
 
-  const int64_t Gb = p.G;
-  const int all = static_cast<int>(ceil_div(Gb, kBlocks));
+  const int Gb = static_cast<int>(p.G);
+  const int all = (Gb + kBlocks - 1) / kBlocks;
   const int st0 = split * stages_per_split;
   const int nst = all - st0 < stages_per_split ? all - st0 : stages_per_split;   // >= 1
-  const int full = static_cast<int>(Gb / kBlocks);   // stages before the ragged one
+  const int whole = Gb / kBlocks - st0;     // stages of this split before the ragged one
+  const int first = st0 * kBlocks;          // its first block
 
-  // Copy roles: wavefront w makes the copies w, w + kWaves, ... of a stage, 1024 bytes of LDS
-  // each, whole rows.  Rows past the matrix read its last row again; their results are not
-  // stored.
-  constexpr int kMine = T::kCopies + (T::kExtra ? 1 : 0);
-  uint32_t off[kMine];
-  constexpr int wl = Geo::kWRow / 16, xl = Geo::kXRow / 16;
-  const int wchunk = (lane % wl) ^ swz<Geo::kWRow>(lane / wl);   // swz repeats after 16 rows
-  auto xchunk = [&](int piece) {   // a copy of bf16 X is only 8 rows
-    return (lane % xl) ^ swz<Geo::kXRow>((piece - T::kWPieces) * (64 / xl) + lane / xl);
+  const uint32_t w_pitch = static_cast<uint32_t>(Gb) * 16;
+  const uint32_t x_pitch = X4 ? w_pitch : static_cast<uint32_t>(p.ldx) * 2;
+  const uint8_t* const wbase = p.codes + r0 * w_pitch + static_cast<int64_t>(first) * 16;
+  const uint8_t* const xbase = X4 ? p.xcodes + t0 * w_pitch + static_cast<int64_t>(first) * 16
+                                  : reinterpret_cast<const uint8_t*>(p.X + t0 * p.ldx) + static_cast<int64_t>(first) * 64;
+
+  // Stage st (of this split) into its buffers: wavefront w makes the copies w, w + waves, ...
+  // of whole LDS rows.  The lanes' offsets are formed anew each time: kept in registers they
+  // would push the accumulators out.
+  auto zero16 = [&](lds_u8* at) {
+    *(__attribute__((address_space(3))) i32x4*)(at + 16 * lane) = i32x4{0, 0, 0, 0};
   };
-  {
-    const int64_t xp = X4 ? Gb * 16 : p.ldx * 2;
+  auto copy_w = [&](int st, int piece, int ln, bool full) {
+    constexpr int per = Geo::kWRow / 16;
+    const int wp = piece + (st % kParts) * T::kWPieces;
+    const int r = wp * (64 / per) + ln / per, chunk = (ln % per) ^ swz<Geo::kWRow>(r);
+    const int b = st / kParts * (kParts * kBlocks);     // first block of the buffer
+    lds_u8* const at = lds_w + (st / kParts % T::kWBuffers) * T::kWBytes + wp * 1024;
+    if (full || first + b + chunk < Gb)
+      copy_lds<16>(at, wbase + static_cast<int64_t>(b) * 16,
+                   static_cast<uint32_t>(r < last_r ? r : last_r) * w_pitch + 16 * chunk);
+    else
+      zero16(at);
+  };
+  auto copy_x = [&](int st, int piece, int ln, bool full) {
+    constexpr int per = Geo::kXRow / 16;
+    const int r = piece * (64 / per) + ln / per, chunk = (ln % per) ^ swz<Geo::kXRow>(r);
+    lds_u8* const at = lds_x + (st % kRing) * T::kXBytes + piece * 1024;
+    if (full || first + st * kBlocks + (X4 ? chunk : chunk / 4) < Gb)
+      copy_lds<16>(at, xbase + static_cast<int64_t>(st) * (kBlocks * (X4 ? 16 : 64)),
+                   static_cast<uint32_t>(r < last_t ? r : last_t) * x_pitch + 16 * chunk);
+    else
+      zero16(at);
+  };
+  auto copies = [&](int st, bool full) {
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int piece = wave + j * kWaves;
-      if (piece < T::kWPieces) {
-        const int row = piece * (64 / wl) + lane / wl;
-        const int64_t r = r0 + row < p.d_o ? row : p.d_o - 1 - r0;
-        off[j] = static_cast<uint32_t>(r * Gb * 16 + 16 * wchunk);
-      } else {
-        const int row = (piece - T::kWPieces) * (64 / xl) + lane / xl;
-        const int64_t t = t0 + row < p.n ? row : p.n - 1 - t0;
-        off[j] = static_cast<uint32_t>(t * xp + 16 * xchunk(piece));
+    for (int j = 0; j < T::kCopies + (T::kExtra ? 1 : 0); ++j) {
+      const int piece = wave + j * T::kWaves;
+      if ((j + 1) * T::kWaves <= T::kWPieces) {
+        copy_w(st, piece, ln, full);
+      } else if (j * T::kWaves >= T::kWPieces) {
+        if (piece < T::kPieces && st < nst) copy_x(st, piece - T::kWPieces, ln, full);
+      } else if (piece < T::kWPieces) {
+        copy_w(st, piece, ln, full);
+      } else if (piece < T::kPieces && st < nst) {
+        copy_x(st, piece - T::kWPieces, ln, full);
       }
     }
-  }
-  const uint8_t* const wbase = p.codes + r0 * Gb * 16;
-  const uint8_t* const xbase = X4 ? p.xcodes + t0 * Gb * 16
-                                  : reinterpret_cast<const uint8_t*>(p.X) + t0 * p.ldx * 2;
-  const bool dword_factors = Gb % 4 == 0 && p.factors_aligned;
+  };
+  const int issues = static_cast<int>(round_up(nst, kParts));   // the last one may be W's alone
+  auto issue = [&](int st) {
+    if (st / kParts * kParts + kParts <= whole)
+      copies(st, true);
+    else
+      copies(st, false);
+  };
 
-  // Factors of 16 blocks from block b0 on, to buffer `buf`: row i at 16 i.
-  auto fetch_factors = [&](int64_t b0, int buf) {
-    lds_u8* const dst = fac + buf * T::kFactors;
-    if (dword_factors) {
-#pragma unroll
-      for (int j = 0; j < (T::kFRows / 16 + kWaves - 1) / kWaves; ++j) {
-        const int piece = wave + j * kWaves;      // 16 rows of four words
-        if (piece * 16 >= T::kFRows) break;
-        const int row = piece * 16 + lane / 4;
-        const int64_t b = b0 + 4 * (lane % 4);
-        lds_u8* const at = dst + piece * 256;
+  // kFetch factors of every row from block b0 on (counted from `first`).  Word k of row r lies at
+  // word k ^ (r % 16) of its 64 bytes, off the banks of its neighbours.
+  const bool word_factors = Gb % 4 == 0 && p.factors_aligned;
+  auto fetch_factors = [&](int b0) {
+    if (word_factors) {
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      for (int piece = wave; piece < T::kFRows / 4; piece += T::kWaves) {   // four rows each
+        const int row = piece * 4 + ln / 16;
+        const int b = first + b0 + 4 * ((ln % 16) ^ (row % 16));
+        lds_u8* const at = lds_f + piece * 256;
         if (b < Gb) {
-          if (!X4 || piece * 16 < T::BM) {
-            const int64_t r = r0 + row < p.d_o ? row : p.d_o - 1 - r0;
-            copy_lds<4>(at, p.scales + r0 * Gb, static_cast<uint32_t>(r * Gb + b));
-          } else {
-            const int64_t t = t0 + row - T::BM < p.n ? row - T::BM : p.n - 1 - t0;
-            copy_lds<4>(at, p.xscales + t0 * Gb, static_cast<uint32_t>(t * Gb + b));
-          }
-        } else {
-          *(__attribute__((address_space(3))) uint32_t*)(at + 4 * lane) = 0x7f7f7f7fu;
+          if (!X4 || piece < T::BM / 4)
+            copy_lds<4>(at, p.scales + r0 * Gb, static_cast<uint32_t>((row < last_r ? row : last_r) * Gb + b));
+          else
+            copy_lds<4>(at, p.xscales + t0 * Gb,
+                        static_cast<uint32_t>((row - T::BM < last_t ? row - T::BM : last_t) * Gb + b));
         }
+        else
+          *(__attribute__((address_space(3))) uint32_t*)(at + 4 * lane) = 0x7f7f7f7fu;
       }
     } else {
-      for (int row = tid; row < T::kFRows; row += T::kThreads) {
-        const uint8_t* src;
-        if (!X4 || row < T::BM)
-          src = p.scales + (r0 + row < p.d_o ? r0 + row : p.d_o - 1) * Gb;
-        else
-          src = p.xscales + (t0 + row - T::BM < p.n ? t0 + row - T::BM : p.n - 1) * Gb;
-        uint32_t w[4];
+      for (int i = tid; i < T::kFRows * 16; i += T::kThreads) {
+        const int row = i / 16, k = i % 16;
+        const bool w = !X4 || row < T::BM;
+        const int r = w ? (row < last_r ? row : last_r) : (row - T::BM < last_t ? row - T::BM : last_t);
+        const uint8_t* src = (w ? p.scales + r0 * Gb : p.xscales + t0 * Gb) + static_cast<int64_t>(r) * Gb;
+        uint32_t v = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int64_t b = b0 + 4 * i + k;
-            w[i] |= (b < Gb ? static_cast<uint32_t>(src[b]) : kMxOne) << (8 * k);
-          }
+        for (int c = 0; c < 4; ++c) {
+          const int b = first + b0 + 4 * k + c;
+          v |= (b < Gb ? static_cast<uint32_t>(src[b]) : kMxOne) << (8 * c);
         }
-        *(__attribute__((address_space(3))) i32x4*)(dst + 16 * row) =
-            i32x4{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3])};
+        *(__attribute__((address_space(3))) uint32_t*)(lds_f + row * kFetch + 4 * (k ^ (row % 16))) = v;
       }
-    }
-  };
-
-  auto issue = [&](int st) {   // stage st (counted from st0) into its ring slot
-    const int64_t b0 = static_cast<int64_t>(st0 + st) * kBlocks;
-    if (st % kPer == 0) fetch_factors(b0, (st / kPer) & 1);
-    lds_u8* const dst = lds + (st % kRing) * T::kStage;
-    const bool whole = st0 + st < full;
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      const int piece = wave + j * kWaves;
-      if (piece >= T::kPieces) break;
-      lds_u8* const at = dst + piece * 1024;
-      const bool w = piece < T::kWPieces;
-      if (whole || b0 + (w ? wchunk : X4 ? xchunk(piece) : xchunk(piece) / 4) < Gb)
-        copy_lds<16>(at, w ? wbase + b0 * 16 : xbase + b0 * (X4 ? 16 : 64), off[j]);
-      else
-        *(__attribute__((address_space(3))) i32x4*)(at + 16 * lane) = i32x4{0, 0, 0, 0};
     }
   };
 
@@ -444,109 +467,236 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.f;
 
-  // Stage st + 1 has landed: everything but the copies of the kRing - 2 stages after it, which
-  // may be in flight where those stages are whole (a wavefront then has issued exactly its
-  // number of copies for each; a fetch of factors only makes the wait longer).
-  auto landed = [&](int st) {
-    if (st + kRing - 1 >= nst || st0 + st + kRing - 1 >= full)
+  // Stage st + 1 has landed for every wavefront, and every wavefront is done with the LDS reads
+  // of stage st.  With two buffers that is everything.  With three, the batch issued last (stage
+  // st + 2) may be in flight where it is whole, so that the wavefront has issued its full number
+  // of copies; but where st + 1 begins a W buffer, that batch holds the second half of it, ahead
+  // of the copies of X.  (A fetch of factors only makes the wait longer.)
+  auto join = [&](int st) {
+    if (kRing == 2 || st + 2 >= nst || st + 2 + kParts > whole)
       wait_and_join<0>();
+    else if (st % kParts == kParts - 1)
+      wait_and_join<T::kXLeast>();
     else if (wave < T::kExtra)
-      wait_and_join<(kRing - 2) * (T::kCopies + 1)>();
+      wait_and_join<T::kCopies + 1>();
     else
-      wait_and_join<(kRing - 2) * T::kCopies>();
+      wait_and_join<T::kCopies>();
   };
 
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i)
-    if (i < nst) issue(i);
-  landed(-1);
-
   const int row = lane & 31, half = lane >> 5;
-  for (int st = 0; st < nst; ++st) {
-    if (st + kRing - 1 < nst) issue(st + kRing - 1);
-    lds_u8* const ws = lds + (st % kRing) * T::kStage + (wm * 32 * MT + row) * Geo::kWRow;
-    lds_u8* const xs = lds + (st % kRing) * T::kStage + T::BM * Geo::kWRow +
-                       (wn * 32 * NT + row) * Geo::kXRow;
-    lds_u8* const fw = fac + ((st / kPer) & 1) * T::kFactors + (wm * 32 * MT + row) * 16 +
-                       (st % kPer) * kBlocks;
-    auto rd16 = [](lds_u8* q) {
-      return *(__attribute__((address_space(3))) i32x4*)q;
+  lds_u8* const my_w = lds_w + (wm * 32 * MT + row) * Geo::kWRow;
+  lds_u8* const my_x = lds_x + (wn * 32 * NT + row) * Geo::kXRow;
+  lds_u8* const my_fw = lds_f + (wm * 32 * MT + row) * kFetch;
+  lds_u8* const my_fx = lds_f + (T::BM + wn * 32 * NT + row) * kFetch;
+  auto rd16 = [](lds_u8* q) { return *(__attribute__((address_space(3))) i32x4*)q; };
+  auto rd4 = [](lds_u8* q) { return *(__attribute__((address_space(3))) uint32_t*)q; };
+
+  // A stage is worked through in steps; the operands of a step are read from LDS into the
+  // second of two register sets while the matrix cores work on the first, and a stage's last
+  // step runs beside the reads of the next stage's first one, behind the join.
+#define QZ_FENCE __builtin_amdgcn_sched_barrier(0)
+  // Products may be moved past branches (they have no side effects), down to the end of the
+  // stage and with all its operands alive: this keeps those before it where they are.
+  auto pin = [&] {
+#pragma unroll
+    for (int a = 0; a < MT; ++a)
+#pragma unroll
+      for (int b = 0; b < NT; ++b) asm volatile("" : "+v"(acc[a][b]));
+  };
+  fetch_factors(0);
+#pragma unroll
+  for (int i = 0; i < kRing; ++i)
+    if (i < issues) issue(i);
+  wait_and_join<0>();
+
+  // The factors of stage st are in registers everywhere when a fetch replaces them: the last
+  // stage of a fetch meets the others once more, and the fetch has the rest of it to land.
+  auto refetch = [&](int st) {
+    if ((st + 1) % kPer == 0 && st + 1 < nst) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4));   // lgkmcnt = 0
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      fetch_factors((st + 1) * kBlocks);
+    }
+  };
+
+  if constexpr (X4) {
+    i32x4 w0[MT], x0[NT], w1[MT], x1[NT];
+    uint32_t ew[MT], ex[NT], nw[MT], nx[NT];
+    auto load = [&](int st, int s, i32x4 (&w)[MT], i32x4 (&x)[NT]) {
+      const int c = 16 * ((4 * half + s) ^ swz<128>(row));
+#pragma unroll
+      for (int a = 0; a < MT; ++a) w[a] = rd16(my_w + (st % kRing) * T::kWBytes + a * 32 * 128 + c);
+#pragma unroll
+      for (int b = 0; b < NT; ++b) x[b] = rd16(my_x + (st % kRing) * T::kXBytes + b * 32 * 128 + c);
     };
-    if constexpr (X4) {
-      lds_u8* const fx = fw + (T::BM + wn * 32 * NT - wm * 32 * MT) * 16;
-      int ew[MT], ex[NT];
+    auto load_factors = [&](int st) {
+      const int k = 4 * ((2 * (st % kPer) + half) ^ (row % 16));
+#pragma unroll
+      for (int a = 0; a < MT; ++a) nw[a] = rd4(my_fw + a * 32 * kFetch + k);
+#pragma unroll
+      for (int b = 0; b < NT; ++b) nx[b] = rd4(my_fx + b * 32 * kFetch + k);
+    };
+    auto multiply = [&](auto s, const i32x4 (&w)[MT], const i32x4 (&x)[NT]) {
 #pragma unroll
       for (int a = 0; a < MT; ++a)
-        ew[a] = static_cast<int>(*(__attribute__((address_space(3))) uint32_t*)(fw + a * 512) >> (8 * half));
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-        ex[b] = static_cast<int>(*(__attribute__((address_space(3))) uint32_t*)(fx + b * 512) >> (8 * half));
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        i32x8 wv[MT], xv[NT];
-        const int cw = 16 * ((2 * s + half) ^ swz<Geo::kWRow>(row));
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          const i32x4 c = rd16(ws + a * 32 * Geo::kWRow + cw);
-          wv[a] = i32x8{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
-        }
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
-          const i32x4 c = rd16(xs + b * 32 * Geo::kXRow + cw);
-          xv[b] = i32x8{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
+          const i32x8 wv = {w[a][0], w[a][1], w[a][2], w[a][3], 0, 0, 0, 0};
+          const i32x8 xv = {x[b][0], x[b][1], x[b][2], x[b][3], 0, 0, 0, 0};
+          acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              wv, xv, acc[a][b], 4, 4, decltype(s)::value, static_cast<int>(ew[a]),
+              decltype(s)::value, static_cast<int>(ex[b]));
         }
+    };
+    using std::integral_constant;
+    load(0, 0, w0, x0);
+    load_factors(0);
+    for (int st = 0; st < nst; ++st) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+      for (int a = 0; a < MT; ++a) ew[a] = nw[a];
 #pragma unroll
-          for (int b = 0; b < NT; ++b) {
-            if (s == 0)
-              acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[a], xv[b], acc[a][b], 4, 4,
-                                                                         0, ew[a], 0, ex[b]);
-            else
-              acc[a][b] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv[a], xv[b], acc[a][b], 4, 4,
-                                                                         2, ew[a], 2, ex[b]);
-          }
+      for (int b = 0; b < NT; ++b) ex[b] = nx[b];
+      refetch(st);
+      load(st, 1, w1, x1);
+      QZ_FENCE;
+      multiply(integral_constant<int, 0>{}, w0, x0);
+      QZ_FENCE;
+      load(st, 2, w0, x0);
+      QZ_FENCE;
+      multiply(integral_constant<int, 1>{}, w1, x1);
+      QZ_FENCE;
+      load(st, 3, w1, x1);
+      QZ_FENCE;
+      multiply(integral_constant<int, 2>{}, w0, x0);
+      QZ_FENCE;
+      pin();
+      if (st + 1 < nst) {
+        join(st);
+        if (st + kRing < issues) issue(st + kRing);
+        load(st + 1, 0, w0, x0);
+        load_factors(st + 1);
       }
-    } else {
-      const int cw = 16 * (half ^ swz<Geo::kWRow>(row));
-      i32x4 c[MT];
-      float f[MT];
+      QZ_FENCE;
+      multiply(integral_constant<int, 3>{}, w1, x1);
+      QZ_FENCE;
+      pin();
+    }
+  } else {
+    i32x4 c[MT], cn[MT], x0[NT], x1[NT];
+    uint32_t f[MT], fn[MT];   // factors of the four blocks of a pair of stages
+    auto load_w = [&](int st) {
+      const int at = (st / 2 % 2) * T::kWBytes + 16 * ((2 * (st % 2) + half) ^ swz<64>(row));
+      const int k = 4 * ((st % kPer / 2) ^ (row % 16));
 #pragma unroll
       for (int a = 0; a < MT; ++a) {
-        c[a] = rd16(ws + a * 32 * Geo::kWRow + cw);
-        f[a] = mx_factor(fw[a * 512 + half]);
+        cn[a] = rd16(my_w + a * 32 * 64 + at);
+        fn[a] = rd4(my_fw + a * 32 * kFetch + k);
       }
+    };
+    auto load_x = [&](int st, int j, i32x4 (&x)[NT]) {
+      const int at = (st % kRing) * T::kXBytes + 16 * ((4 * half + j) ^ swz<128>(row));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        bf16x8 xv[NT];
+      for (int b = 0; b < NT; ++b) x[b] = rd16(my_x + b * 32 * 128 + at);
+    };
+    auto multiply = [&](int j, const i32x4 (&x)[NT]) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a) {
+        const bf16x8 wv = mx_word_bf16(static_cast<uint32_t>(c[a][j]), __uint_as_float(f[a]));
 #pragma unroll
         for (int b = 0; b < NT; ++b)
-          xv[b] = __builtin_bit_cast(bf16x8, rd16(xs + b * 32 * Geo::kXRow + 16 * ((4 * half + j) ^ swz<Geo::kXRow>(row))));
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          const bf16x8 wv = mx_word_bf16(static_cast<uint32_t>(c[a][j]), f[a]);
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, xv[b], acc[a][b], 0, 0, 0);
-        }
+          acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wv, __builtin_bit_cast(bf16x8, x[b]),
+                                                              acc[a][b], 0, 0, 0);
       }
+    };
+    load_w(0);
+    load_x(0, 0, x0);
+    for (int st = 0; st < nst; ++st) {
+#pragma unroll
+      for (int a = 0; a < MT; ++a) {
+        c[a] = cn[a];
+        f[a] = (fn[a] >> (8 * (2 * (st % 2) + half)) & 255u) << 23;
+      }
+      refetch(st);
+      load_x(st, 1, x1);
+      QZ_FENCE;
+      multiply(0, x0);
+      QZ_FENCE;
+      load_x(st, 2, x0);
+      QZ_FENCE;
+      multiply(1, x1);
+      QZ_FENCE;
+      load_x(st, 3, x1);
+      QZ_FENCE;
+      multiply(2, x0);
+      QZ_FENCE;
+      pin();
+      if (st + 1 < nst) {
+        join(st);
+        if (st + kRing < issues) issue(st + kRing);
+        load_w(st + 1);
+        load_x(st + 1, 0, x0);
+      }
+      QZ_FENCE;
+      multiply(3, x1);
+      QZ_FENCE;
+      pin();
     }
-    if (st + 1 < nst) landed(st);
   }
+#undef QZ_FENCE
 
-  // Register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of a tile, token l % 32.
+  // Register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of a tile, token l % 32.  32 tokens
+  // at a time go through LDS of the wavefront's own, so that Y is written in whole lines.
+  const int osize = p.partial || p.yt == QZ_F32 ? 4 : 2;
+  uint8_t* const ybase = p.partial ? reinterpret_cast<uint8_t*>(p.partial + split * p.n * p.d_o)
+                                   : static_cast<uint8_t*>(p.Y);
+  const int64_t ld = p.partial ? p.d_o : p.ldy;
+  const bool lines = ld * osize % 16 == 0 && reinterpret_cast<uintptr_t>(ybase) % 16 == 0;
+  lds_u8* const out = (lds_u8*)smem + wave * 32 * T::kOutPitch;
+  const int64_t wr0 = r0 + wm * 32 * MT;
+  __syncthreads();
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    const int64_t t = t0 + (wn * NT + b) * 32 + row;
-    if (t >= p.n) continue;
 #pragma unroll
     for (int a = 0; a < MT; ++a)
 #pragma unroll
       for (int r4 = 0; r4 < 4; ++r4) {
-        const int64_t r = r0 + (wm * MT + a) * 32 + 8 * r4 + 4 * half;
+        const int rr = a * 32 + 8 * r4 + 4 * half;
         f32x4 v = {acc[a][b][4 * r4], acc[a][b][4 * r4 + 1], acc[a][b][4 * r4 + 2], acc[a][b][4 * r4 + 3]};
-        store4(p, split, t, r, v);
+        if (p.bias && !p.partial) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (wr0 + rr + i < p.d_o) v[i] += p.bias[wr0 + rr + i];
+        }
+        if (osize == 4) {
+          *(__attribute__((address_space(3))) f32x4*)(out + row * T::kOutPitch + 4 * rr) = v;
+        } else {
+          const uint32_t lo = f32_to_bf16(v[0]) | (static_cast<uint32_t>(f32_to_bf16(v[1])) << 16);
+          const uint32_t hi = f32_to_bf16(v[2]) | (static_cast<uint32_t>(f32_to_bf16(v[3])) << 16);
+          *(__attribute__((address_space(3))) uint64_t*)(out + row * T::kOutPitch + 2 * rr) = static_cast<uint64_t>(hi) << 32 | lo;
+        }
       }
+    const int64_t tb = t0 + (wn * NT + b) * 32;
+    const int per_row = 32 * MT * osize / 16;           // pieces of 16 bytes
+    for (int i = lane; i < 32 * per_row; i += 64) {
+      const int t = i / per_row, k = i % per_row, e0 = k * 16 / osize;
+      if (tb + t >= p.n || wr0 + e0 >= p.d_o) continue;
+      const i32x4 v = rd16(out + t * T::kOutPitch + 16 * k);
+      uint8_t* const dst = ybase + ((tb + t) * ld + wr0 + e0) * osize;
+      if (lines && wr0 + e0 + 16 / osize <= p.d_o) {
+        *reinterpret_cast<i32x4*>(dst) = v;
+      } else if (osize == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (wr0 + e0 + j < p.d_o) reinterpret_cast<int*>(dst)[j] = v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (wr0 + e0 + j < p.d_o)
+            reinterpret_cast<uint16_t*>(dst)[j] = static_cast<uint16_t>(static_cast<uint32_t>(v[j / 2]) >> (16 * (j % 2)));
+      }
+    }
   }
 }
 
@@ -559,14 +709,14 @@ int launch_tile(const Mx4Product& p, int splits, hipStream_t s) {
   QZ_HIP(hipGetDevice(&dev));
   if (dev > 63 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
     QZ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, T::kLds));
+                               hipFuncAttributeMaxDynamicSharedMemorySize, T::kShared));
     if (dev <= 63) allowed.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
   }
   const int tw = static_cast<int>(ceil_div(p.d_o, T::BM)), tx = static_cast<int>(ceil_div(p.n, T::BN));
   const int all = static_cast<int>(ceil_div(p.G, TileGeom<X4>::kBlocks));
-  const int per = static_cast<int>(ceil_div(all, splits));
+  const int per = static_cast<int>(round_up(ceil_div(all, splits), TileGeom<X4>::kWParts));
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tw) * tx, static_cast<unsigned>(ceil_div(all, per))),
-                     dim3(T::kThreads), T::kLds, s, p, tw, tx, per);
+                     dim3(T::kThreads), T::kShared, s, p, tw, tx, per);
   return check_launch("mx4_tile");
 }
 
