@@ -1,5 +1,6 @@
 // Products with MX4 weights: Y = X W^T + b, W [d_o x d_i] in MX4, X in bf16 or MX4.
 #include <atomic>
+#include <cmath>
 
 #include "mx4.h"
 
@@ -7,17 +8,9 @@ namespace qz {
 
 namespace {
 
-// Four results of token t, rows r .. r + 3: the output with its bias, or the partial sums of a
-// split (fp32 [split][n][d_o]).
-__device__ __forceinline__ void store4(const Mx4Product& p, int split, int64_t t, int64_t r, f32x4 v) {
+// Four results of token t, rows r .. r + 3, with their bias.
+__device__ __forceinline__ void store4(const Mx4Product& p, int64_t t, int64_t r, f32x4 v) {
   if (r >= p.d_o) return;
-  if (p.partial) {
-    float* o = p.partial + (split * p.n + t) * p.d_o + r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (r + i < p.d_o) o[i] = v[i];
-    return;
-  }
   const bool whole = r + 4 <= p.d_o;
   if (p.bias) {
 #pragma unroll
@@ -215,7 +208,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
     f32x4 v = part[0][i][lane];
     for (int w = 1; w < waves; ++w) v += part[w][i][lane];
     const int64_t t = t0 + 16 * (i % NT) + m;
-    if (t < p.n) store4(p, 0, t, r0 + 16 * (i / NT) + 4 * q, v);
+    if (t < p.n) store4(p, t, r0 + 16 * (i / NT) + 4 * q, v);
   }
 }
 
@@ -320,7 +313,7 @@ struct TileShape {
 };
 
 template <bool X4, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product p, int tiles_w,
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx4_tile_kernel(const Mx4Product p, int tiles_w,
                                                                 int tiles_x, int stages_per_split) {
   using T = TileShape<X4, WM, WN, MT, NT>;
   using Geo = TileGeom<X4>;
@@ -700,6 +693,36 @@ __global__ __launch_bounds__(WM * WN * 64) void mx4_tile_kernel(const Mx4Product
   }
 }
 
+// Rows of X copied to rows of whole blocks, zero beyond d_i.
+__global__ __launch_bounds__(256) void mx4_pad_kernel(const uint16_t* __restrict__ X, int64_t n,
+                                                      int64_t d_i, int64_t ldx,
+                                                      uint16_t* __restrict__ out, int64_t ldo) {
+  for (int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x; t < n * ldo;
+       t += (int64_t)gridDim.x * 256) {
+    const int64_t r = t / ldo, c = t % ldo;
+    out[t] = c < d_i ? X[r * ldx + c] : static_cast<uint16_t>(0);
+  }
+}
+
+// Y = the splits' sums in their order, with the bias.  Four results a thread.
+__global__ __launch_bounds__(256) void mx4_join_kernel(const Mx4Product p, int splits) {
+  const int64_t per_row = (p.d_o + 3) / 4, total = p.n * per_row;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t t = i / per_row, r = i % per_row * 4;
+    const float* src = p.partial + t * p.d_o + r;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (p.d_o % 4 == 0) {
+      for (int k = 0; k < splits; ++k) v += *reinterpret_cast<const f32x4*>(src + k * p.n * p.d_o);
+    } else {
+      for (int k = 0; k < splits; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (r + j < p.d_o) v[j] += src[k * p.n * p.d_o + j];
+    }
+    store4(p, t, r, v);
+  }
+}
+
 template <bool X4, int WM, int WN, int MT, int NT>
 int launch_tile(const Mx4Product& p, int splits, hipStream_t s) {
   using T = TileShape<X4, WM, WN, MT, NT>;
@@ -715,20 +738,17 @@ int launch_tile(const Mx4Product& p, int splits, hipStream_t s) {
   const int tw = static_cast<int>(ceil_div(p.d_o, T::BM)), tx = static_cast<int>(ceil_div(p.n, T::BN));
   const int all = static_cast<int>(ceil_div(p.G, TileGeom<X4>::kBlocks));
   const int per = static_cast<int>(round_up(ceil_div(all, splits), TileGeom<X4>::kWParts));
-  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tw) * tx, static_cast<unsigned>(ceil_div(all, per))),
-                     dim3(T::kThreads), T::kShared, s, p, tw, tx, per);
-  return check_launch("mx4_tile");
-}
-
-// Rows of X copied to rows of whole blocks, zero beyond d_i.
-__global__ __launch_bounds__(256) void mx4_pad_kernel(const uint16_t* __restrict__ X, int64_t n,
-                                                      int64_t d_i, int64_t ldx,
-                                                      uint16_t* __restrict__ out, int64_t ldo) {
-  for (int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x; t < n * ldo;
-       t += (int64_t)gridDim.x * 256) {
-    const int64_t r = t / ldo, c = t % ldo;
-    out[t] = c < d_i ? X[r * ldx + c] : static_cast<uint16_t>(0);
-  }
+  const int parts = static_cast<int>(ceil_div(all, per));
+  Mx4Product q = p;
+  if (parts == 1) q.partial = nullptr;
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tw) * tx, parts), dim3(T::kThreads),
+                     T::kShared, s, q, tw, tx, per);
+  QZ_TRY(check_launch("mx4_tile"));
+  if (parts == 1) return QZ_OK;
+  const int64_t blocks = ceil_div(p.n * ceil_div(p.d_o, 4), 256);
+  hipLaunchKernelGGL(mx4_join_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)),
+                     dim3(256), 0, s, q, parts);
+  return check_launch("mx4_join");
 }
 
 }  // namespace
@@ -741,17 +761,96 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
   return check_launch("mx4_pad");
 }
 
-int mx4_product_splits(bool, int64_t, int64_t, int64_t) { return 1; }
-
+// ------------------------------------------------------------------------- choice of a kernel
+// Times of the alternatives, in microseconds, from their sizes.  A tile kernel's stage takes
+// `alone` when its workgroup has a compute unit to itself (latency and the barriers), and `share`
+// for each of the up to two resident ones when those are busy; then a launch, and for a split
+// contraction the pass that joins the sums.  Fitted to 400 measurements (20 to 2048 tokens, seven
+// layers of 512 to 12288 columns, 1 to 16 splits; 9% root mean square) and choosing within 8% of
+// the best one measured there in all but two, where it is 12% off.  For few tokens a workgroup's
+// time is the row segments it reads, 1.8 ns each (checked at 1 to 64 tokens: 2.4 ns at one token,
+// where HBM counts, 1.7 to 1.9 from 13 on).
+// Both sides, measured: 64 tokens 4096 -> 4096 bf16, few-token kernel 13.3 and best tile 16.4; 64
+// tokens 4096 -> 12288, 33 and 21.9 (128 x 32, four splits); 2048 tokens 4096 -> 4096, tiles of
+// 256 x 256 104, of 256 x 128 72; 128 tokens 12288 -> 4096, unsplit 97 or more, 16 splits 31.
 namespace {
+
+struct Choice {
+  enum Kind { kFew11, kFew12, kFew22, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
+  int splits;
+};
+struct TileTime {
+  int bm, bn, resident;
+  double alone, share;
+};
+constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 of MX4
+    {{256, 256, 1, 1.746, 1.746}, {256, 128, 1, 1.021, 1.021}, {128, 128, 2, 1.027, 0.513},
+     {128, 64, 2, 0.592, 0.369}, {64, 64, 2, 0.477, 0.239}, {128, 32, 2, 0.427, 0.256}},
+    {{256, 256, 1, 2.072, 2.072}, {256, 128, 1, 1.419, 1.419}, {128, 128, 2, 1.272, 0.636},
+     {128, 64, 2, 0.760, 0.495}, {64, 64, 2, 0.527, 0.264}, {128, 32, 2, 0.616, 0.308}}};
+
+Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
+  if (n <= 16) return {Choice::kFew11, 1};   // one tile of tokens: nothing to share
+  Choice best{Choice::kFew11, 1};
+  double best_t = 1e30;
+  const auto consider = [&](Choice::Kind kind, int splits, double t) {
+    if (t < best_t) {
+      best_t = t;
+      best = {kind, splits};
+    }
+  };
+  const int few[3][2] = {{1, 1}, {1, 2}, {2, 2}};
+  for (int i = 0; i < 3; ++i) {
+    const int rt = few[i][0], nt = few[i][1];
+    const double groups = static_cast<double>(ceil_div(d_o, 16 * rt)) * ceil_div(n, 16 * nt);
+    const int tokens = static_cast<int>(n < 16 * nt ? n : 16 * nt);
+    const double segments = 48 * rt + tokens * (x4 ? 3 : 8);
+    consider(static_cast<Choice::Kind>(Choice::kFew11 + i), 1,
+             3.0 + 1.8e-3 * std::ceil(groups / 256) * std::ceil(G / 8.0) * segments);
+  }
+  const int blocks = x4 ? 8 : 2, even = x4 ? 1 : 2;
+  const int64_t all = ceil_div(G, blocks);
+  for (int i = 0; i < 6; ++i) {
+    const TileTime& c = kTiles[x4][i];
+    const double tiles = static_cast<double>(ceil_div(d_o, c.bm)) * ceil_div(n, c.bn);
+    for (const int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      const int64_t per = round_up(ceil_div(all, want), even), splits = ceil_div(all, per);
+      if (splits != want || (want > 1 && (per < 2 || want * n * d_o > (int64_t{1} << 26)))) continue;
+      const double groups = std::ceil(tiles * splits / 256);
+      const double full = std::floor(groups / c.resident), rest = groups - full * c.resident;
+      double t = full * std::fmax(c.alone, c.resident * c.share);
+      if (rest > 0) t += std::fmax(c.alone, rest * c.share);
+      t = 4.0 + per * t;
+      if (splits > 1) t += 4.0 + 1.3e-6 * splits * n * d_o;   // written and read, fp32
+      consider(static_cast<Choice::Kind>(Choice::k256x256 + i), static_cast<int>(splits), t);
+    }
+  }
+  return best;
+}
 
 template <bool X4>
 int launch_product(const Mx4Product& p, hipStream_t s) {
-  if (p.n > 64) return launch_tile<X4, 2, 4, 4, 2>(p, 1, s);
-  return launch_skinny<X4, 1, 1>(p, 8, s);
+  const Choice c = choose(X4, p.n, p.d_o, p.G);
+  switch (c.kind) {
+    // eight wavefronts along d_i; four where three or more workgroups share a compute unit
+    case Choice::kFew11: return launch_skinny<X4, 1, 1>(p, p.d_o > 512 * 16 ? 4 : 8, s);
+    case Choice::kFew12: return launch_skinny<X4, 1, 2>(p, 4, s);
+    case Choice::kFew22: return launch_skinny<X4, 2, 2>(p, 4, s);
+    case Choice::k256x256: return launch_tile<X4, 2, 4, 4, 2>(p, c.splits, s);
+    case Choice::k256x128: return launch_tile<X4, 4, 2, 2, 2>(p, c.splits, s);
+    case Choice::k128x128: return launch_tile<X4, 2, 2, 2, 2>(p, c.splits, s);
+    case Choice::k128x64: return launch_tile<X4, 2, 2, 2, 1>(p, c.splits, s);
+    case Choice::k64x64: return launch_tile<X4, 2, 2, 1, 1>(p, c.splits, s);
+    case Choice::k128x32: return launch_tile<X4, 4, 1, 1, 1>(p, c.splits, s);
+  }
+  return fail(QZ_EHIP, "mx4_product: no kernel");
 }
 
 }  // namespace
+
+int mx4_product_splits(bool x4, int64_t n, int64_t d_o, int64_t G) {
+  return choose(x4, n, d_o, G).splits;
+}
 
 int launch_mx4_product(const Mx4Product& p, hipStream_t s) {
   return p.X ? launch_product<false>(p, s) : launch_product<true>(p, s);
