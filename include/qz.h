@@ -426,13 +426,13 @@ int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, cons
  *   gu_codes/gu_scales: [n_experts x 2 f x d], gate rows before up rows; dn_codes/dn_scales:
  *   [n_experts x d x f].  Y [n x d] bf16.  ids [n x top_k] int32 and weights [n x top_k] fp32
  *   (nullable): the routing.  Sums in fp32; the hidden vector is kept to 16 bits of mantissa.
- *   1 <= n_experts <= 256, top_k <= 16, n <= 1024 (more tokens: qz_mx4_linear per expert).
+ *   1 <= n_experts <= 256, top_k <= 16, n <= 256 (more tokens: qz_mx4_linear per expert).
  *   ws: qz_mx4_moe_workspace(...) bytes, 256-byte aligned; calls that may overlap need
  *   different workspaces.  Asynchronous.                                                  */
 #define QZ_MOE_RENORM 0x1u
 #define QZ_MOE_MAX_EXPERTS 256
 #define QZ_MOE_MAX_TOP_K 16
-#define QZ_MOE_MAX_TOKENS 1024
+#define QZ_MOE_MAX_TOKENS 256
 typedef struct {
   uint32_t struct_size;   /* sizeof(qz_moe) */
   int32_t n_experts;

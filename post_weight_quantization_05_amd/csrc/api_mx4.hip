@@ -68,7 +68,8 @@ void set_alignment(Mx4Product* p) {
 
 struct MoeWs {
   double *logits, *top;
-  int32_t* sel;
+  int32_t *sel, *slot_expert, *slot_count, *slot_pairs;
+  float* y_pairs;
   uint16_t *h_hi, *h_lo, *xpad;
   size_t bytes;
 };
@@ -79,6 +80,11 @@ MoeWs moe_ws(void* base, int64_t n, int64_t d, int64_t f, const qz_moe* p) {
   w.logits = c.take<double>(static_cast<size_t>(n) * p->n_experts);
   w.top = c.take<double>(pairs);
   w.sel = c.take<int32_t>(pairs);
+  const size_t slots = static_cast<size_t>(moe_slots(n, p->n_experts, p->top_k));
+  w.slot_expert = c.take<int32_t>(slots);
+  w.slot_count = c.take<int32_t>(slots);
+  w.slot_pairs = c.take<int32_t>(slots * n);
+  w.y_pairs = c.take<float>(pairs * round_up(d, 4));
   w.h_hi = c.take<uint16_t>(pairs * mx_blocks(f) * kMxBlock);
   w.h_lo = c.take<uint16_t>(pairs * mx_blocks(f) * kMxBlock);
   w.xpad = c.take<uint16_t>(static_cast<size_t>(n) * mx_blocks(d) * kMxBlock);
@@ -242,7 +248,7 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
   if (!float_type(rt)) return fail(QZ_EINVAL, "mx4_moe: bad router dtype");
   QZ_TRY(check_moe(params));
   if (!moe_sizes(n, d, f))
-    return fail(QZ_EINVAL, "mx4_moe: need 0 <= n <= 1024, 1 <= d <= 2^20, 1 <= f <= 2^20");
+    return fail(QZ_EINVAL, "mx4_moe: need 0 <= n <= 256, 1 <= d <= 2^20, 1 <= f <= 2^20");
   if (ldx < d) return fail(QZ_EINVAL, "mx4_moe: ldx must be at least d");
   if (n == 0) return QZ_OK;
   if (!X || !router || !Y) return fail(QZ_EINVAL, "mx4_moe: null pointer");
@@ -285,6 +291,11 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
   a.h_hi = w.h_hi;
   a.h_lo = w.h_lo;
   a.ldh = a.Gf * kMxBlock;
+  a.slot_expert = w.slot_expert;
+  a.slot_count = w.slot_count;
+  a.slot_pairs = w.slot_pairs;
+  a.y_pairs = w.y_pairs;
+  a.ldy = round_up(d, 4);
   return launch_moe(a, rt, stream);
 }
 

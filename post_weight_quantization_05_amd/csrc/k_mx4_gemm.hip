@@ -2,7 +2,7 @@
 #include <atomic>
 #include <cmath>
 
-#include "mx4.h"
+#include "mx4_few.h"
 
 namespace qz {
 
@@ -42,162 +42,39 @@ __device__ __forceinline__ void store4(const Mx4Product& p, int64_t t, int64_t r
 }
 
 // ------------------------------------------------------------------------------ few tokens
-// Workgroup of 16 RT rows of W by 16 NT tokens; its wavefronts take turns along d_i, a unit of 256
-// columns at a time: whole 128-byte lines of codes, straight from global memory to the matrix
-// cores, since every code is used once.  Of each 128 columns lane l loads row l % 16, block
-// l / 16: 16 bytes of codes.  Sums in fp32; the wavefronts' sums are added in their order.
-//
-// bf16 X: a load of 16 bytes a lane covers 64 contiguous bytes of each row, so product j of the
-// four takes the columns 32 j + 8 (l / 16) + 0..7 of X, and the codes have to follow: a 4 x 4
-// transpose of words between the four lanes of a row (two pairs of lane swaps) turns word i of
-// block l / 16 into word l / 16 of block i.  (With X read in the shape of whole blocks instead,
-// each of the four loads touches the same two lines of every row, and a compute unit looks up a
-// line in about four clocks: at 13 tokens that cost more than the codes did.)
-//
-// The next unit's loads are issued before the current one's products.
-struct __attribute__((packed)) Bytes8 {
-  uint32_t lo, hi;
-};
-
-// Eight factors of a row from block b0 on, at any alignment (1 past the row's end).
-__device__ __forceinline__ uint2 eight_factors(const uint8_t* row, int b0, int G, bool whole) {
-  if (whole) {
-    const Bytes8 v = *reinterpret_cast<const Bytes8*>(row + b0);
-    return make_uint2(v.lo, v.hi);
-  }
-  uint32_t lo = 0, hi = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo |= (b0 + i < G ? static_cast<uint32_t>(row[b0 + i]) : kMxOne) << (8 * i);
-    hi |= (b0 + 4 + i < G ? static_cast<uint32_t>(row[b0 + 4 + i]) : kMxOne) << (8 * i);
-  }
-  return make_uint2(lo, hi);
-}
-
-// Word i of lane group g (16 lanes each) <-> word g of lane group i.
-__device__ __forceinline__ void transpose_words(uint32_t (&w)[4]) {
-  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  w[0] = c[0];
-  w[1] = c[1];
-  w[2] = d[0];
-  w[3] = d[1];
-}
-
-template <bool X4, int RT, int NT>
-struct SkinnyUnit {
-  uint4 c[2][RT];
-  uint2 e[RT];
-  uint4 x[2][NT][X4 ? 1 : 4];
-  uint2 f[NT];
-};
-
+// Workgroup of 16 RT rows of W by 16 NT tokens; its wavefronts take turns along d_i (mx4_few.h).
+// Sums in fp32; the wavefronts' sums are added in their order.
 constexpr int kSkinnyWaves = 8;
 
 template <bool X4, int RT, int NT>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4Product p) {
+  constexpr Few X = X4 ? Few::kMx4 : Few::kBf16;
   __shared__ f32x4 part[kSkinnyWaves][RT * NT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
   const int64_t r0 = blockIdx.x * (int64_t)(16 * RT), t0 = blockIdx.y * (int64_t)(16 * NT);
   const int G = static_cast<int>(p.G);
-  const uint8_t* wc[RT];
-  const uint8_t* ws[RT];
-  const uint8_t* xc[NT];
-  const uint8_t* xs[NT];
-  bool have[NT];   // lanes without a token read nothing
+  FewRows<X, RT, NT> rows;
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
     const int64_t r = r0 + 16 * a + m < p.d_o ? r0 + 16 * a + m : p.d_o - 1;
-    wc[a] = p.codes + r * G * 16 + 16 * q;
-    ws[a] = p.scales + r * G;
+    rows.wc[a] = p.codes + r * G * 16 + 16 * q;
+    rows.ws[a] = p.scales + r * G;
   }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    have[b] = t0 + 16 * b + m < p.n;
-    const int64_t t = have[b] ? t0 + 16 * b + m : p.n - 1;
-    xc[b] = (X4 ? p.xcodes + t * G * 16 : reinterpret_cast<const uint8_t*>(p.X + t * p.ldx)) + 16 * q;
-    xs[b] = X4 ? p.xscales + t * G : nullptr;
+    rows.have[b] = t0 + 16 * b + m < p.n;   // lanes without a token read nothing
+    const int64_t t = rows.have[b] ? t0 + 16 * b + m : p.n - 1;
+    rows.xc[b] = (X4 ? p.xcodes + t * G * 16 : reinterpret_cast<const uint8_t*>(p.X + t * p.ldx)) + 16 * q;
+    rows.xs[b] = X4 ? p.xscales + t * G : nullptr;
   }
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  using Unit = SkinnyUnit<X4, RT, NT>;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto load = [&](int b0, Unit& v) {
-    const bool whole = b0 + 8 <= G;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int blk = b0 + 4 * u;
-#pragma unroll
-      for (int a = 0; a < RT; ++a) {
-        v.c[u][a] = zero;
-        if (whole || blk + q < G) v.c[u][a] = *reinterpret_cast<const uint4*>(wc[a] + blk * 16);
-      }
-#pragma unroll
-      for (int b = 0; b < NT; ++b)
-#pragma unroll
-        for (int j = 0; j < (X4 ? 1 : 4); ++j) {
-          v.x[u][b][j] = zero;
-          if (have[b] && (whole || blk + (X4 ? q : j) < G))
-            v.x[u][b][j] = *reinterpret_cast<const uint4*>(xc[b] + blk * (X4 ? 16 : 64) + 64 * j);
-        }
-    }
-#pragma unroll
-    for (int a = 0; a < RT; ++a) v.e[a] = eight_factors(ws[a], b0, G, whole);
-    if constexpr (X4) {
-#pragma unroll
-      for (int b = 0; b < NT; ++b) v.f[b] = eight_factors(xs[b], b0, G, whole);
-    }
-  };
-  auto multiply = [&](const Unit& v) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
-      for (int a = 0; a < RT; ++a) {
-        const uint32_t e = u ? v.e[a].y : v.e[a].x;
-        if constexpr (X4) {
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                mx_operand(v.c[u][a]), mx_operand(v.x[u][b][0]), acc[a][b], 4, 4, 0,
-                static_cast<int>(e >> (8 * q)), 0, static_cast<int>((u ? v.f[b].y : v.f[b].x) >> (8 * q)));
-        } else {
-          uint32_t w[4] = {v.c[u][a].x, v.c[u][a].y, v.c[u][a].z, v.c[u][a].w};
-          transpose_words(w);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bf16x8 wv = mx_word_bf16(w[j], mx_factor((e >> (8 * j)) & 255u));
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-              acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  wv, __builtin_bit_cast(bf16x8, v.x[u][b][j]), acc[a][b], 0, 0, 0);
-          }
-        }
-      }
-    }
-  };
-  {
-    Unit u0, u1;
-    const int step = waves * 8;
-    int b0 = wave * 8;
-    if (b0 < G) load(b0, u0);
-    while (b0 < G) {
-      if (b0 + step < G) load(b0 + step, u1);
-      multiply(u0);
-      b0 += step;
-      if (b0 >= G) break;
-      if (b0 + step < G) load(b0 + step, u0);
-      multiply(u1);
-      b0 += step;
-    }
-  }
+  few_products(rows, G, wave, waves, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

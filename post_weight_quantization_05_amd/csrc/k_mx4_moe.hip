@@ -1,238 +1,352 @@
-// A routed expert layer on MX4 weights for a few tokens, in three launches:
+// A routed expert layer on MX4 weights for a few tokens, in four launches:
 //
 //   1. logits[t][e] = <x_t, router_e>, summed in 64 bits (products of bf16 values are exact
 //      there), so the choice of experts does not hang on the order of a sum.
 //   2. per chosen (token t, rank r) with expert e: h = silu(g) u, [g; u] = W_gate_up[e] x_t.
-//      Every workgroup finds the tokens of its expert from the logits by itself.
-//   3. y_t = sum_r w_tr W_down[e_tr] h_tr, all experts of 16 output rows in one workgroup, so
-//      nothing is added through memory and the order of the sums is fixed.
+//      Every workgroup finds its expert and that expert's tokens from the logits by itself.
+//   3. the rows of W_down[e] h, per pair, fp32.
+//   4. y_t = sum_r w_tr (W_down[e_tr] h_tr), in the order of r.
 //
-// h is kept as two bf16 numbers (value and remainder, 16 bits of mantissa together): the
-// matrix cores take bf16, and rounding h once to bf16 would be as large an error as the
-// final rounding of y.
-#include "mx4.h"
+// Weights are read once per 16 tokens of an expert, 16 rows by 16 tokens on the matrix cores
+// (mx4_few.h); what bounds the layer is reading them from HBM.  h is kept as two bf16 numbers
+// (value and remainder, 16 bits of mantissa together): the matrix cores take bf16, and rounding h
+// once to bf16 would be as large an error as the final rounding of y.
+#include "mx4_few.h"
 
 namespace qz {
 
 namespace {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = kWaves * 64;
-constexpr int kTokens = 64;    // tokens of one workgroup of the down product
+constexpr int kWaves = 8;      // of the logits' and the expert products' workgroups, at most
+constexpr int kPerLane = QZ_MOE_MAX_EXPERTS / 64;
 
 // order of the experts of a token: descending logit, ties to the lower index
 __device__ __forceinline__ bool before(double a, int i, double b, int j) {
   return a > b || (a == b && i < j);
 }
 
-template <int RT>
-__global__ __launch_bounds__(kThreads) void moe_logits_kernel(const MoeArgs a) {
+__device__ __forceinline__ void widen8(uint4 v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// ------------------------------------------------------------------------------ 1. the logits
+// A wavefront per (token, expert), 8 columns a lane at a time.
+template <int RT, bool VEC>
+__global__ __launch_bounds__(256) void moe_logits_kernel(const MoeArgs a) {
   const int lane = threadIdx.x & 63;
-  const int64_t w = blockIdx.x * (int64_t)kWaves + (threadIdx.x >> 6);
+  const int w = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (w >= a.n * a.E) return;
-  const int64_t t = w / a.E, e = w % a.E;
+  const int t = w / a.E, e = w - t * a.E;
+  const uint16_t* x = a.X + t * a.ldx;
   double sum = 0;
-  for (int64_t i = lane; i < a.d; i += 64)
-    sum = fma(static_cast<double>(load_w<QZ_BF16>(a.X, t * a.ldx + i)),
-              static_cast<double>(load_w<RT>(a.router, e * a.d + i)), sum);
+  if constexpr (VEC) {   // d % 8 = 0, both rows on 16-byte boundaries
+#pragma unroll 2
+    for (int64_t i = lane * 8; i < a.d; i += 512) {
+      float xv[8], rv[8];
+      widen8(*reinterpret_cast<const uint4*>(x + i), xv);
+      if constexpr (RT == QZ_BF16) {
+        widen8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.router) + e * a.d + i), rv);
+      } else {
+        const f32x4* p = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.router) + e * a.d + i);
+        const f32x4 lo = p[0], hi = p[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          rv[j] = lo[j];
+          rv[4 + j] = hi[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fma(static_cast<double>(xv[j]), static_cast<double>(rv[j]), sum);
+    }
+  } else {
+    for (int64_t i = lane; i < a.d; i += 64)
+      sum = fma(static_cast<double>(load_w<QZ_BF16>(x, i)),
+                static_cast<double>(load_w<RT>(a.router, e * a.d + i)), sum);
+  }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off);
   // a NaN sorts last, so that the choice is always k different experts
   if (lane == 0) a.logits[w] = sum == sum ? sum : -__builtin_inf();
 }
 
-__global__ __launch_bounds__(kThreads) void moe_up_kernel(const MoeArgs a) {
-  __shared__ f32x4 part[2][kWaves][64];
-  __shared__ int list[QZ_MOE_MAX_TOKENS];   // chosen pairs t k + r of this expert
+// ------------------------------------------------------------------------- 2. gate, up, silu
+// Largest of a 32-bit value over the wavefront.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const uint32_t o = __shfl_xor(v, off);
+    v = o > v ? o : v;
+  }
+  return v;
+}
+
+// The top k of one token by a wavefront, r = 0 .. k - 1 in turn: found(r, expert, logit).  Logits
+// become integers of the same order and are compared upper half first.
+template <class F>
+__device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F found) {
+  const int lane = threadIdx.x & 63;
+  uint32_t hi[kPerLane], lo[kPerLane];
+  bool in[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    in[i] = lane + 64 * i < E;
+    // -0 orders as +0
+    const uint64_t b = __builtin_bit_cast(uint64_t, in[i] ? lg[lane + 64 * i] + 0.0 : 0.0);
+    const uint64_t key = b >> 63 ? ~b : b | uint64_t{1} << 63;
+    hi[i] = static_cast<uint32_t>(key >> 32);
+    lo[i] = static_cast<uint32_t>(key);
+  }
+  for (int r = 0; r < k; ++r) {
+    uint32_t m = 0;   // below every key
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (in[i]) m = hi[i] > m ? hi[i] : m;
+    m = wave_max(m);
+    uint32_t l = 0;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (in[i] && hi[i] == m) l = lo[i] > l ? lo[i] : l;
+    l = wave_max(l);
+    int e = -1;
+#pragma unroll
+    for (int i = kPerLane - 1; i >= 0; --i) {
+      const uint64_t hit = __ballot(in[i] && hi[i] == m && lo[i] == l);
+      if (hit) e = 64 * i + __builtin_ctzll(hit);
+    }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i)
+      if (lane + 64 * i == e) in[i] = false;
+    found(r, e, lg[e]);
+  }
+}
+
+// Workgroup (chunk of 16 hidden columns, slot).  A slot is an expert, or, where the tokens cannot
+// reach all experts (`compact`), the slot-th one that they reach.  The first chunk writes the
+// slot's expert and pairs (t k + r) down for the launches after it.
+__global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(const MoeArgs a, int compact) {
+  __shared__ f32x4 part[kWaves][2][64];
+  __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
+  __shared__ uint32_t reached[QZ_MOE_MAX_EXPERTS / 32];
+  __shared__ int chosen[256];               // compact: n k < 256 experts
   __shared__ int count;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
-  const int e = blockIdx.y;
+  const bool scribe = blockIdx.x == 0;
+  int e = blockIdx.y;
   if (threadIdx.x == 0) count = 0;
+  if (threadIdx.x < QZ_MOE_MAX_EXPERTS / 32) reached[threadIdx.x] = 0;
   __syncthreads();
-  for (int64_t t = wave; t < a.n; t += kWaves) {
-    const double* lg = a.logits + t * a.E;
-    const double mine = lg[e];
-    int ahead = 0;
-    for (int j = lane; j < round_up(a.E, 64); j += 64)
-      ahead += __popcll(__ballot(j < a.E && before(lg[j < a.E ? j : 0], j, mine, e)));
-    if (ahead < a.k && lane == 0) {
-      list[atomicAdd(&count, 1)] = static_cast<int>(t * a.k + ahead);
-      if (blockIdx.x == 0) {
-        a.sel[t * a.k + ahead] = e;
-        a.top[t * a.k + ahead] = mine;
+  if (compact) {
+    for (int t = wave; t < a.n; t += waves)
+      wave_top_k(a.logits + t * a.E, a.E, a.k, [&](int r, int c, double l) {
+        if (lane != 0) return;
+        chosen[t * a.k + r] = c;
+        atomicOr(&reached[c / 32], 1u << (c % 32));
+        if (scribe && blockIdx.y == 0) {
+          a.sel[t * a.k + r] = c;
+          a.top[t * a.k + r] = l;
+        }
+      });
+    __syncthreads();
+    int left = e;
+    e = -1;
+#pragma unroll
+    for (int i = 0; i < QZ_MOE_MAX_EXPERTS / 32; ++i) {
+      uint32_t bits = reached[i];
+      const int here = __popc(bits);
+      if (left >= 0 && left < here) {
+        for (int k = 0; k < left; ++k) bits &= bits - 1;
+        e = 32 * i + __builtin_ctz(bits);
+      }
+      left -= here;
+    }
+    if (e >= 0)
+      for (int i = threadIdx.x; i < a.n * a.k; i += blockDim.x)
+        if (chosen[i] == e) list[atomicAdd(&count, 1)] = i;
+  } else {
+    for (int t = wave; t < a.n; t += waves) {
+      const double* lg = a.logits + t * a.E;
+      const double mine = lg[e];
+      int ahead = 0;
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) {
+        const int j = lane + 64 * i;
+        if (64 * i < a.E) ahead += __popcll(__ballot(j < a.E && before(lg[j < a.E ? j : 0], j, mine, e)));
+      }
+      if (ahead < a.k && lane == 0) {
+        const int pair = t * a.k + ahead;
+        list[atomicAdd(&count, 1)] = pair;
+        if (scribe) {
+          a.sel[pair] = e;
+          a.top[pair] = mine;
+        }
       }
     }
   }
   __syncthreads();
-  const int64_t G = a.Gd, f0 = blockIdx.x * (int64_t)16;
-  const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
-  const uint8_t* gc = a.gu_codes + (e * 2 * a.f + row) * G * 16;
-  const uint8_t* gs = a.gu_scales + (e * 2 * a.f + row) * G;
-  const uint8_t* uc = gc + a.f * G * 16;
-  const uint8_t* us = gs + a.f * G;
-  for (int at = 0; at < count; at += 16) {
-    const int pair = list[at + m < count ? at + m : count - 1];
-    const uint16_t* x = a.X + (pair / a.k) * a.ldx;
-    f32x4 g = {0.f, 0.f, 0.f, 0.f}, u = g;
-    for (int64_t st = wave; st * 4 < G; st += kWaves) {
-      const int64_t b = st * 4 + q;
-      const bool in = b < G;
-      uint4 c0 = make_uint4(0u, 0u, 0u, 0u), c1 = c0;
-      uint32_t e0 = kMxOne, e1 = kMxOne;
-      if (in) {
-        c0 = *reinterpret_cast<const uint4*>(gc + b * 16);
-        c1 = *reinterpret_cast<const uint4*>(uc + b * 16);
-        e0 = gs[b];
-        e1 = us[b];
-      }
-      const uint32_t w0[4] = {c0.x, c0.y, c0.z, c0.w}, w1[4] = {c1.x, c1.y, c1.z, c1.w};
-      const uint4* xp = reinterpret_cast<const uint4*>(x + b * 32);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bf16x8 xv = __builtin_bit_cast(bf16x8, in ? xp[j] : make_uint4(0u, 0u, 0u, 0u));
-        g = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_word_bf16(w0[j], mx_factor(e0)), xv, g, 0, 0, 0);
-        u = __builtin_amdgcn_mfma_f32_16x16x32_bf16(mx_word_bf16(w1[j], mx_factor(e1)), xv, u, 0, 0, 0);
-      }
+  // the order of a list is of no consequence: each pair is a column of its own
+  if (scribe) {
+    if (threadIdx.x == 0) {
+      a.slot_expert[blockIdx.y] = e;
+      a.slot_count[blockIdx.y] = count;
     }
-    part[0][wave][lane] = g;
-    part[1][wave][lane] = u;
+    for (int i = threadIdx.x; i < count; i += blockDim.x) a.slot_pairs[blockIdx.y * a.n + i] = list[i];
+  }
+  const int G = static_cast<int>(a.Gd);
+  const int64_t f0 = blockIdx.x * (int64_t)16;
+  const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
+  FewRows<Few::kBf16, 2, 1> rows;
+  for (int at = 0; at < count; at += 16) {
+    const int64_t base = e * 2 * a.f + row;
+    rows.wc[0] = a.gu_codes + base * G * 16 + 16 * q;
+    rows.ws[0] = a.gu_scales + base * G;
+    rows.wc[1] = rows.wc[0] + a.f * G * 16;
+    rows.ws[1] = rows.ws[0] + a.f * G;
+    rows.have[0] = at + m < count;
+    const int pair = list[rows.have[0] ? at + m : at];
+    rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
+    f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
+    few_products(rows, G, wave, waves, acc);
+    part[wave][0][lane] = acc[0][0];
+    part[wave][1][lane] = acc[1][0];
     __syncthreads();
-    if (wave == 0 && at + m < count) {
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        g += part[0][w][lane];
-        u += part[1][w][lane];
+    if (wave == 0 && rows.have[0]) {
+      f32x4 g = part[0][0][lane], u = part[0][1][lane];
+      for (int w = 1; w < waves; ++w) {
+        g += part[w][0][lane];
+        u += part[w][1][lane];
       }
+      uint16_t hi[4], lo[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t r = f0 + 4 * q + i;   // < 32 Gf: columns past f are zero
-        const float h = r < a.f ? g[i] / (1.f + expf(-g[i])) * u[i] : 0.f;
-        const uint16_t hi = f32_to_bf16(h);
-        a.h_hi[pair * a.ldh + r] = hi;
-        a.h_lo[pair * a.ldh + r] = f32_to_bf16(h - bf16_to_f32(hi));
+      for (int i = 0; i < 4; ++i) {   // columns past f, to the end of the last block, are zero
+        const float h = f0 + 4 * q + i < a.f ? g[i] / (1.f + expf(-g[i])) * u[i] : 0.f;
+        hi[i] = f32_to_bf16(h);
+        lo[i] = f32_to_bf16(h - bf16_to_f32(hi[i]));
       }
+      const int64_t o = pair * a.ldh + f0 + 4 * q;
+      *reinterpret_cast<uint2*>(a.h_hi + o) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(a.h_lo + o) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
     }
     __syncthreads();
   }
 }
 
-__global__ __launch_bounds__(kThreads) void moe_down_kernel(const MoeArgs a) {
-  __shared__ float sums[kWaves][kTokens][16];
-  __shared__ float weight[kTokens * QZ_MOE_MAX_TOP_K];
-  __shared__ int order[kTokens * QZ_MOE_MAX_TOP_K];
-  __shared__ int start[QZ_MOE_MAX_EXPERTS + 1], fill[QZ_MOE_MAX_EXPERTS];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// --------------------------------------------------------------------------------- 3. down
+// Workgroup (32 rows of W_down, slot): the pairs' results, [pair][d] in fp32.
+__global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(const MoeArgs a) {
+  __shared__ f32x4 part[kWaves][2][64];
+  const int count = a.slot_count[blockIdx.y];
+  if (count == 0) return;
+  const int e = a.slot_expert[blockIdx.y];
+  const int32_t* list = a.slot_pairs + blockIdx.y * a.n;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
-  const int64_t t0 = blockIdx.y * (int64_t)kTokens;
-  const int nt = static_cast<int>(a.n - t0 < kTokens ? a.n - t0 : kTokens);
-  const int pairs = nt * a.k;
-  const int32_t* sel = a.sel + t0 * a.k;
+  const int G = static_cast<int>(a.Gf);
+  const int64_t r0 = blockIdx.x * (int64_t)32;
+  FewRows<Few::kBf16Twice, 2, 1> rows;
+  for (int at = 0; at < count; at += 16) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t row = r0 + 16 * i + m < a.d ? r0 + 16 * i + m : a.d - 1;
+      rows.wc[i] = a.dn_codes + (e * a.d + row) * G * 16 + 16 * q;
+      rows.ws[i] = a.dn_scales + (e * a.d + row) * G;
+    }
+    rows.have[0] = at + m < count;
+    const int64_t pair = list[rows.have[0] ? at + m : at];
+    rows.xc[0] = reinterpret_cast<const uint8_t*>(a.h_hi + pair * a.ldh) + 16 * q;
+    rows.xl[0] = reinterpret_cast<const uint8_t*>(a.h_lo + pair * a.ldh) + 16 * q;
+    f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
+    few_products(rows, G, wave, waves, acc);
+    part[wave][0][lane] = acc[0][0];
+    part[wave][1][lane] = acc[1][0];
+    __syncthreads();
+    if (wave < 2 && rows.have[0]) {
+      f32x4 v = part[0][wave][lane];
+      for (int w = 1; w < waves; ++w) v += part[w][wave][lane];
+      const int64_t r = r0 + 16 * wave + 4 * q;
+      if (r < a.ldy)   // rows of the scratch are whole fours
+        *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;
+    }
+    __syncthreads();
+  }
+}
 
-  for (int i = threadIdx.x; i < a.E; i += kThreads) fill[i] = 0;
-  for (int i = threadIdx.x; i < kWaves * kTokens * 16; i += kThreads) (&sums[0][0][0])[i] = 0.f;
-  __syncthreads();
-  for (int i = threadIdx.x; i < pairs; i += kThreads) atomicAdd(&fill[sel[i]], 1);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int i = 0; i < a.E; ++i) {
-      start[i] = s;
-      s += fill[i];
-      fill[i] = start[i];
-    }
-    start[a.E] = s;
-  }
-  __syncthreads();
-  // the order of an expert's pairs is of no consequence: each is a column of its own
-  for (int i = threadIdx.x; i < pairs; i += kThreads) order[atomicAdd(&fill[sel[i]], 1)] = i;
-  for (int t = wave; t < nt; t += kWaves) {
-    const double* top = a.top + (t0 + t) * a.k;
-    const double* lg = a.logits + (t0 + t) * a.E;
-    const double best = top[0];
-    float s = 0.f;
-    if (a.renorm) {
-      for (int r = 0; r < a.k; ++r) s += expf(static_cast<float>(top[r] - best));
-    } else {
-      for (int j = lane; j < a.E; j += 64) s += expf(static_cast<float>(lg[j] - best));
+// -------------------------------------------------------------------------------- 4. the sum
+__global__ __launch_bounds__(256) void moe_sum_kernel(const MoeArgs a) {
+  __shared__ float weight[QZ_MOE_MAX_TOP_K];
+  __shared__ float sums[4];
+  const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const double best = a.top[t * a.k];
+  // weights: exp(l - best) over the sum of the chosen ones, or of all
+  float s = 0.f;
+  if (a.renorm) {
+    for (int r = 0; r < a.k; ++r) s += expf(static_cast<float>(a.top[t * a.k + r] - best));
+  } else {
+    if (tid < a.E) s = expf(static_cast<float>(a.logits[t * a.E + tid] - best));
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
-    }
-    if (lane < a.k) {
-      const float w = expf(static_cast<float>(top[lane] - best)) / s;
-      weight[t * a.k + lane] = w;
-      if (blockIdx.x == 0) {
-        if (a.ids) a.ids[(t0 + t) * a.k + lane] = sel[t * a.k + lane];
-        if (a.weights) a.weights[(t0 + t) * a.k + lane] = w;
-      }
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off);
+    if (lane == 0) sums[tid >> 6] = s;
+    __syncthreads();
+    s = sums[0] + sums[1] + sums[2] + sums[3];
+  }
+  if (tid < a.k) {
+    const float w = expf(static_cast<float>(a.top[t * a.k + tid] - best)) / s;
+    weight[tid] = w;
+    if (blockIdx.x == 0) {
+      if (a.ids) a.ids[t * a.k + tid] = a.sel[t * a.k + tid];
+      if (a.weights) a.weights[t * a.k + tid] = w;
     }
   }
   __syncthreads();
-
-  const int64_t G = a.Gf, r0 = blockIdx.x * (int64_t)16;
-  const int64_t row = r0 + m < a.d ? r0 + m : a.d - 1;
-  for (int e = wave; e < a.E; e += kWaves) {
-    const uint8_t* dc = a.dn_codes + (e * a.d + row) * G * 16;
-    const uint8_t* ds = a.dn_scales + (e * a.d + row) * G;
-    for (int at = start[e]; at < start[e + 1]; at += 16) {
-      const bool mine = at + m < start[e + 1];
-      const int pair = order[mine ? at + m : at];
-      const uint16_t* hi = a.h_hi + (t0 * a.k + pair) * a.ldh;
-      const uint16_t* lo = a.h_lo + (t0 * a.k + pair) * a.ldh;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      for (int64_t st = 0; st * 4 < G; ++st) {
-        const int64_t b = st * 4 + q;
-        const bool in = b < G;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 c = zero;
-        uint32_t f = kMxOne;
-        if (in) {
-          c = *reinterpret_cast<const uint4*>(dc + b * 16);
-          f = ds[b];
-        }
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        const uint4* hp = reinterpret_cast<const uint4*>(hi + b * 32);
-        const uint4* lp = reinterpret_cast<const uint4*>(lo + b * 32);
+  const int64_t c = (blockIdx.x * (int64_t)256 + tid) * 4;
+  if (c >= a.d) return;
+  f32x4 y = {0.f, 0.f, 0.f, 0.f};
+  for (int r = 0; r < a.k; ++r)
+    y += weight[r] * *reinterpret_cast<const f32x4*>(a.y_pairs + (int64_t)(t * a.k + r) * a.ldy + c);
+  uint16_t* o = a.Y + t * a.d + c;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bf16x8 wv = mx_word_bf16(w[j], mx_factor(f));
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, in ? hp[j] : zero), acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, in ? lp[j] : zero), acc, 0, 0, 0);
-        }
-      }
-      if (mine)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[wave][pair / a.k][4 * q + i] += weight[pair] * acc[i];
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < nt * 16; i += kThreads) {
-    const int t = i / 16, r = i % 16;
-    if (r0 + r >= a.d) continue;
-    float s = sums[0][t][r];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += sums[w][t][r];
-    a.Y[(t0 + t) * a.d + r0 + r] = f32_to_bf16(s);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (c + i < a.d) o[i] = f32_to_bf16(y[i]);
 }
 
 }  // namespace
 
+// Slots: one per expert, or one per pair where those are fewer and the tokens so few that every
+// workgroup can find all their experts (a wavefront takes about 1 us for a token's top 8).
+int moe_slots(int64_t n, int E, int k) {
+  return n * k < E && n <= 2 * kWaves ? static_cast<int>(n * k) : E;
+}
+
 int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
-  const dim3 gl(static_cast<unsigned>(ceil_div(a.n * a.E, kWaves)));
-  if (router_type == QZ_BF16)
-    hipLaunchKernelGGL((moe_logits_kernel<QZ_BF16>), gl, dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((moe_logits_kernel<QZ_F32>), gl, dim3(kThreads), 0, s, a);
+  const bool vec = a.d % 8 == 0 && reinterpret_cast<uintptr_t>(a.router) % 16 == 0;
+  const auto logits = router_type == QZ_BF16
+                          ? (vec ? moe_logits_kernel<QZ_BF16, true> : moe_logits_kernel<QZ_BF16, false>)
+                          : (vec ? moe_logits_kernel<QZ_F32, true> : moe_logits_kernel<QZ_F32, false>);
+  hipLaunchKernelGGL(logits, dim3(static_cast<unsigned>(ceil_div(a.n * a.E, 4))), dim3(256), 0, s, a);
   QZ_TRY(check_launch("moe_logits"));
-  hipLaunchKernelGGL(moe_up_kernel, dim3(static_cast<unsigned>(2 * a.Gf), static_cast<unsigned>(a.E)),
-                     dim3(kThreads), 0, s, a);
+  const unsigned slots = static_cast<unsigned>(moe_slots(a.n, a.E, a.k));
+  const auto waves = [](int64_t G) {   // a wavefront per 256 columns, up to eight
+    const int64_t u = ceil_div(G, 8);
+    return static_cast<unsigned>(u < kWaves ? u : kWaves);
+  };
+  hipLaunchKernelGGL(moe_up_kernel, dim3(static_cast<unsigned>(2 * a.Gf), slots), dim3(64 * waves(a.Gd)),
+                     0, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
   QZ_TRY(check_launch("moe_up"));
-  hipLaunchKernelGGL(moe_down_kernel,
-                     dim3(static_cast<unsigned>(ceil_div(a.d, 16)),
-                          static_cast<unsigned>(ceil_div(a.n, kTokens))),
-                     dim3(kThreads), 0, s, a);
-  return check_launch("moe_down");
+  const unsigned dw = waves(a.Gf);
+  hipLaunchKernelGGL(moe_down_kernel, dim3(static_cast<unsigned>(ceil_div(a.d, 32)), slots),
+                     dim3(64 * (dw < 2 ? 2 : dw)), 0, s, a);
+  QZ_TRY(check_launch("moe_down"));
+  hipLaunchKernelGGL(moe_sum_kernel,
+                     dim3(static_cast<unsigned>(ceil_div(a.d, 1024)), static_cast<unsigned>(a.n)),
+                     dim3(256), 0, s, a);
+  return check_launch("moe_sum");
 }
 
 }  // namespace qz

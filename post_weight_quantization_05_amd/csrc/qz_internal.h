@@ -291,8 +291,11 @@ struct MoeArgs {
   uint16_t* Y; int32_t* ids; float* weights;    // ids, weights nullable
   double* logits;                               // [n x E]
   int32_t* sel; double* top;                    // [n x k] chosen expert and its logit
+  int32_t *slot_expert, *slot_count, *slot_pairs;   // [slots], [slots], [slots x n]
   uint16_t *h_hi, *h_lo; int64_t ldh;           // [n k x 32 Gf]
+  float* y_pairs; int64_t ldy;                  // [n k x d rounded up to 4]
 };
+int moe_slots(int64_t n, int E, int k);
 int launch_moe(const MoeArgs& a, int router_type, hipStream_t s);
 
 // eigendecomposition of Sigma H Sigma (k_eig.hip): workspace bytes (asks the solver library

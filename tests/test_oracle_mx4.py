@@ -156,7 +156,7 @@ def test_moe_refusals(lib):
 
     need = lib.qz_mx4_moe_workspace(3, 64, 40, C.byref(params()))
     assert need > 0
-    assert lib.qz_mx4_moe_workspace(1025, 64, 40, C.byref(params())) == 0
+    assert lib.qz_mx4_moe_workspace(257, 64, 40, C.byref(params())) == 0
     assert lib.qz_mx4_moe_workspace(3, 64, 40, C.byref(params(k=9))) == 0
     good = dict(X=A, xt=0, n=3, ldx=64, d=64, f=40, p=C.byref(params()), router=A, rt=0, gc=A, gs=A,
                 dc=A, ds=A, Y=A, ids=None, weights=None, ws=A, ws_bytes=need, stream=None)
@@ -164,7 +164,7 @@ def test_moe_refusals(lib):
     def call(**kw):
         return lib.qz_mx4_moe(*{**good, **kw}.values())
 
-    for kw in (dict(xt=1), dict(rt=4), dict(n=-1), dict(n=1025), dict(ldx=63), dict(d=0), dict(f=0),
+    for kw in (dict(xt=1), dict(rt=4), dict(n=-1), dict(n=257), dict(ldx=63), dict(d=0), dict(f=0),
                dict(p=None), dict(X=None), dict(router=None), dict(Y=None), dict(gc=None),
                dict(gs=None), dict(dc=A + 8), dict(ds=None), dict(Y=A + 1), dict(ids=A + 2),
                dict(weights=A + 1), dict(router=A + 1)):
