@@ -74,7 +74,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  few_products(rows, G, wave, waves, acc);
+  few_products<true>(rows, G, wave, waves, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

@@ -75,14 +75,17 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const MoeArgs a) {
 }
 
 // ------------------------------------------------------------------------- 2. gate, up, silu
-// Largest of a 32-bit value over the wavefront.
+// Largest of a 32-bit value over the wavefront, by data-parallel moves: lanes 1, 2, 4, 8 back in
+// their rows of 16, then the last lane of a row to the next row, and of two rows to the next two.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) {
-    const uint32_t o = __shfl_xor(v, off);
-    v = o > v ? o : v;
-  }
-  return v;
+  auto up = [](uint32_t x, uint32_t o) { return o > x ? o : x; };
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x111, 0xf, 0xf, false));
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x112, 0xf, 0xf, false));
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x114, 0xf, 0xf, false));
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x118, 0xf, 0xf, false));
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x142, 0xa, 0xf, false));
+  v = up(v, __builtin_amdgcn_update_dpp(0u, v, 0x143, 0xc, 0xf, false));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // The top k of one token by a wavefront, r = 0 .. k - 1 in turn: found(r, expert, logit).  Logits
@@ -121,14 +124,15 @@ __device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F fou
 #pragma unroll
     for (int i = 0; i < kPerLane; ++i)
       if (lane + 64 * i == e) in[i] = false;
-    found(r, e, lg[e]);
+    const uint64_t key = static_cast<uint64_t>(m) << 32 | l;
+    found(r, e, __builtin_bit_cast(double, key >> 63 ? key & ~(uint64_t{1} << 63) : ~key));
   }
 }
 
-// Workgroup (chunk of 16 hidden columns, slot).  A slot is an expert, or, where the tokens cannot
-// reach all experts (`compact`), the slot-th one that they reach.  The first chunk writes the
-// slot's expert and pairs (t k + r) down for the launches after it.
-__global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(const MoeArgs a, int compact) {
+// Workgroups (x, slot): 16 hidden columns at a time, chunks x, x + the grid's width, ...  A slot is an expert, or, where the tokens cannot
+// reach all experts (`compact`), the slot-th one that they reach.  The first one of a slot writes
+// its expert and pairs (t k + r) down for the launches after it.
+__global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a, int compact) {
   __shared__ f32x4 part[kWaves][2][64];
   __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
   __shared__ uint32_t reached[QZ_MOE_MAX_EXPERTS / 32];
@@ -199,20 +203,21 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(const MoeArgs a, in
     for (int i = threadIdx.x; i < count; i += blockDim.x) a.slot_pairs[blockIdx.y * a.n + i] = list[i];
   }
   const int G = static_cast<int>(a.Gd);
-  const int64_t f0 = blockIdx.x * (int64_t)16;
-  const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
+  const int n = count;
   FewRows<Few::kBf16, 2, 1> rows;
-  for (int at = 0; at < count; at += 16) {
+  for (int64_t f0 = blockIdx.x * (int64_t)16; f0 < a.ldh; f0 += gridDim.x * (int64_t)16)
+  for (int at = 0; at < n; at += 16) {
+    const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
     const int64_t base = e * 2 * a.f + row;
     rows.wc[0] = a.gu_codes + base * G * 16 + 16 * q;
     rows.ws[0] = a.gu_scales + base * G;
     rows.wc[1] = rows.wc[0] + a.f * G * 16;
     rows.ws[1] = rows.ws[0] + a.f * G;
-    rows.have[0] = at + m < count;
+    rows.have[0] = at + m < n;
     const int pair = list[rows.have[0] ? at + m : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products(rows, G, wave, waves, acc);
+    few_products<false>(rows, G, wave, waves, acc);
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -238,32 +243,33 @@ __global__ __launch_bounds__(kWaves * 64) void moe_up_kernel(const MoeArgs a, in
 }
 
 // --------------------------------------------------------------------------------- 3. down
-// Workgroup (32 rows of W_down, slot): the pairs' results, [pair][d] in fp32.
-__global__ __launch_bounds__(kWaves * 64) void moe_down_kernel(const MoeArgs a) {
+// Workgroups (x, slot), 32 rows of W_down at a time: the pairs' results, [pair][d] in fp32.
+__global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs a) {
   __shared__ f32x4 part[kWaves][2][64];
-  const int count = a.slot_count[blockIdx.y];
-  if (count == 0) return;
-  const int e = a.slot_expert[blockIdx.y];
-  const int32_t* list = a.slot_pairs + blockIdx.y * a.n;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
+  const int32_t* list = a.slot_pairs + blockIdx.y * a.n;
+  // asked for together, as each is a trip to L2 (entries past the slot's count are not used)
+  const int early = list[m < a.n ? m : 0];
+  const int n = a.slot_count[blockIdx.y];
+  const int e = a.slot_expert[blockIdx.y];
   const int G = static_cast<int>(a.Gf);
-  const int64_t r0 = blockIdx.x * (int64_t)32;
   FewRows<Few::kBf16Twice, 2, 1> rows;
-  for (int at = 0; at < count; at += 16) {
+  for (int64_t r0 = blockIdx.x * (int64_t)32; r0 < a.d; r0 += gridDim.x * (int64_t)32)
+  for (int at = 0; at < n; at += 16) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t row = r0 + 16 * i + m < a.d ? r0 + 16 * i + m : a.d - 1;
       rows.wc[i] = a.dn_codes + (e * a.d + row) * G * 16 + 16 * q;
       rows.ws[i] = a.dn_scales + (e * a.d + row) * G;
     }
-    rows.have[0] = at + m < count;
-    const int64_t pair = list[rows.have[0] ? at + m : at];
+    rows.have[0] = at + m < n;
+    const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + m];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.h_hi + pair * a.ldh) + 16 * q;
     rows.xl[0] = reinterpret_cast<const uint8_t*>(a.h_lo + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products(rows, G, wave, waves, acc);
+    few_products<false>(rows, G, wave, waves, acc);
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -332,16 +338,22 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   hipLaunchKernelGGL(logits, dim3(static_cast<unsigned>(ceil_div(a.n * a.E, 4))), dim3(256), 0, s, a);
   QZ_TRY(check_launch("moe_logits"));
   const unsigned slots = static_cast<unsigned>(moe_slots(a.n, a.E, a.k));
-  const auto waves = [](int64_t G) {   // a wavefront per 256 columns, up to eight
-    const int64_t u = ceil_div(G, 8);
-    return static_cast<unsigned>(u < kWaves ? u : kWaves);
+  // As many workgroups as are resident at once (four wavefronts a SIMD): finding its expert's
+  // tokens takes a workgroup 1 to 2 us, so each then goes on through the rows of its slot.  A
+  // wavefront per 256 columns, up to eight where there are few chunks of rows, else up to four.
+  const auto shape = [&](int64_t chunks, int64_t G, dim3* grid, dim3* block) {
+    const int64_t units = ceil_div(G, 8), most = chunks * slots <= 512 ? 8 : 4;
+    const int64_t waves = units < 2 ? 2 : units < most ? units : most;
+    const int64_t width = ceil_div(256 * 16 / waves, slots);
+    *grid = dim3(static_cast<unsigned>(chunks < width ? chunks : width), slots);
+    *block = dim3(static_cast<unsigned>(64 * waves));
   };
-  hipLaunchKernelGGL(moe_up_kernel, dim3(static_cast<unsigned>(2 * a.Gf), slots), dim3(64 * waves(a.Gd)),
-                     0, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
+  dim3 grid, block;
+  shape(2 * a.Gf, a.Gd, &grid, &block);
+  hipLaunchKernelGGL(moe_up_kernel, grid, block, 0, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
   QZ_TRY(check_launch("moe_up"));
-  const unsigned dw = waves(a.Gf);
-  hipLaunchKernelGGL(moe_down_kernel, dim3(static_cast<unsigned>(ceil_div(a.d, 32)), slots),
-                     dim3(64 * (dw < 2 ? 2 : dw)), 0, s, a);
+  shape(ceil_div(a.d, 32), a.Gf, &grid, &block);
+  hipLaunchKernelGGL(moe_down_kernel, grid, block, 0, s, a);
   QZ_TRY(check_launch("moe_down"));
   hipLaunchKernelGGL(moe_sum_kernel,
                      dim3(static_cast<unsigned>(ceil_div(a.d, 1024)), static_cast<unsigned>(a.n)),

@@ -4,7 +4,8 @@
 // A tile is 16 rows of W by 16 tokens.  The wavefront goes along d_i a unit of 256 columns at a
 // time: whole 128-byte lines of codes, straight from global memory to the matrix cores, since
 // every code is used once.  Of each 128 columns lane l loads row l % 16, block l / 16: 16 bytes of
-// codes.  The next unit's loads are issued before the current one's products.
+// codes.  AHEAD: the next unit's loads are issued before the current one's products (for one
+// workgroup a compute unit; with several of them the registers are better spent on more).
 //
 // bf16 X: a load of 16 bytes a lane covers 64 contiguous bytes of each row, so product j of the
 // four takes the columns 32 j + 8 (l / 16) + 0..7 of X, and the codes have to follow: a 4 x 4
@@ -74,7 +75,7 @@ struct FewRows {
 };
 
 // acc += the products over the units first, first + step, ... of G blocks.
-template <Few X, int RT, int NT>
+template <bool AHEAD, Few X, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X, RT, NT>& p, int G, int first, int step,
                                              f32x4 (&acc)[RT][NT]) {
   constexpr bool X4 = X == Few::kMx4;
@@ -140,9 +141,17 @@ __device__ __forceinline__ void few_products(const FewRows<X, RT, NT>& p, int G,
       }
     }
   };
-  Unit u0, u1;
   int b0 = first * 8;
   const int ahead = step * 8;
+  if constexpr (!AHEAD) {
+    for (; b0 < G; b0 += ahead) {
+      Unit u;
+      load(b0, u);
+      multiply(u);
+    }
+    return;
+  }
+  Unit u0, u1;
   if (b0 < G) load(b0, u0);
   while (b0 < G) {
     if (b0 + ahead < G) load(b0 + ahead, u1);
