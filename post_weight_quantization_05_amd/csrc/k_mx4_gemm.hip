@@ -42,20 +42,19 @@ __device__ __forceinline__ void store4(const Mx4Product& p, int64_t t, int64_t r
 }
 
 // ------------------------------------------------------------------------------ few tokens
-// Workgroup of 16 RT rows of W by 16 NT tokens; its wavefronts take turns along d_i (mx4_few.h).
+// Workgroup of 16 RT rows of W by 16 NT tokens; each of its wavefronts has a part of d_i (mx4_few.h).
 // Sums in fp32; the wavefronts' sums are added in their order.
 constexpr int kSkinnyWaves = 8;
 
 template <bool X4, int RT, int NT>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4Product p) {
-  constexpr Few X = X4 ? Few::kMx4 : Few::kBf16;
   __shared__ f32x4 part[kSkinnyWaves][RT * NT][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
   const int64_t r0 = blockIdx.x * (int64_t)(16 * RT), t0 = blockIdx.y * (int64_t)(16 * NT);
   const int G = static_cast<int>(p.G);
-  FewRows<X, RT, NT> rows;
+  FewRows<X4, RT, NT> rows;
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
     const int64_t r = r0 + 16 * a + m < p.d_o ? r0 + 16 * a + m : p.d_o - 1;
@@ -74,7 +73,8 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
   for (int a = 0; a < RT; ++a)
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  few_products<true>(rows, G, wave, waves, acc);
+  const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
+  few_products<true>(rows, G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

@@ -204,7 +204,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
   }
   const int G = static_cast<int>(a.Gd);
   const int n = count;
-  FewRows<Few::kBf16, 2, 1> rows;
+  const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
+  const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
+  FewRows<false, 2, 1> rows;
   for (int64_t f0 = blockIdx.x * (int64_t)16; f0 < a.ldh; f0 += gridDim.x * (int64_t)16)
   for (int at = 0; at < n; at += 16) {
     const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
@@ -217,7 +219,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
     const int pair = list[rows.have[0] ? at + m : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, G, wave, waves, acc);
+    few_products<false>(rows, G, u0, u1, acc);
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -243,7 +245,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
 }
 
 // --------------------------------------------------------------------------------- 3. down
-// Workgroups (x, slot), 32 rows of W_down at a time: the pairs' results, [pair][d] in fp32.
+// Workgroups (x, slot), 32 rows of W_down at a time: the pairs' results, [pair][d] in fp32.  Eight
+// pairs at a time: columns 0 to 7 of a tile are the values of h, 8 to 15 the remainders, and a
+// result is the sum of two columns; so both halves of h cost the loads and products of one.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs a) {
   __shared__ f32x4 part[kWaves][2][64];
   const int lane = threadIdx.x & 63;
@@ -251,31 +255,32 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
   const int m = lane & 15, q = lane >> 4;
   const int32_t* list = a.slot_pairs + blockIdx.y * a.n;
   // asked for together, as each is a trip to L2 (entries past the slot's count are not used)
-  const int early = list[m < a.n ? m : 0];
+  const int early = list[(m & 7) < a.n ? m & 7 : 0];
   const int n = a.slot_count[blockIdx.y];
   const int e = a.slot_expert[blockIdx.y];
   const int G = static_cast<int>(a.Gf);
-  FewRows<Few::kBf16Twice, 2, 1> rows;
+  const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
+  const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
+  FewRows<false, 2, 1> rows;
   for (int64_t r0 = blockIdx.x * (int64_t)32; r0 < a.d; r0 += gridDim.x * (int64_t)32)
-  for (int at = 0; at < n; at += 16) {
+  for (int at = 0; at < n; at += 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t row = r0 + 16 * i + m < a.d ? r0 + 16 * i + m : a.d - 1;
       rows.wc[i] = a.dn_codes + (e * a.d + row) * G * 16 + 16 * q;
       rows.ws[i] = a.dn_scales + (e * a.d + row) * G;
     }
-    rows.have[0] = at + m < n;
-    const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + m];
-    rows.xc[0] = reinterpret_cast<const uint8_t*>(a.h_hi + pair * a.ldh) + 16 * q;
-    rows.xl[0] = reinterpret_cast<const uint8_t*>(a.h_lo + pair * a.ldh) + 16 * q;
+    rows.have[0] = at + (m & 7) < n;
+    const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + (m & 7)];
+    rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, G, wave, waves, acc);
+    few_products<false>(rows, G, u0, u1, acc);
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
-    if (wave < 2 && rows.have[0]) {
-      f32x4 v = part[0][wave][lane];
-      for (int w = 1; w < waves; ++w) v += part[w][wave][lane];
+    if (wave < 2 && rows.have[0] && m < 8) {
+      f32x4 v = part[0][wave][lane] + part[0][wave][lane + 8];
+      for (int w = 1; w < waves; ++w) v += part[w][wave][lane] + part[w][wave][lane + 8];
       const int64_t r = r0 + 16 * wave + 4 * q;
       if (r < a.ldy)   // rows of the scratch are whole fours
         *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;

@@ -19,23 +19,25 @@
 
 namespace qz {
 
-struct __attribute__((packed)) Bytes8 {
-  uint32_t lo, hi;
+struct __attribute__((packed)) Bytes16 {
+  uint32_t w[4];
 };
 
-// Eight factors of a row from block b0 on, at any alignment (1 past the row's end).
-__device__ __forceinline__ uint2 eight_factors(const uint8_t* row, int b0, int G, bool whole) {
-  if (whole) {
-    const Bytes8 v = *reinterpret_cast<const Bytes8*>(row + b0);
-    return make_uint2(v.lo, v.hi);
+// Sixteen factors of a row from block b on, at any alignment (1 past the row's end).
+__device__ __forceinline__ uint4 sixteen_factors(const uint8_t* row, int b, int G) {
+  if (b + 16 <= G) {
+    const Bytes16 v = *reinterpret_cast<const Bytes16*>(row + b);
+    return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
   }
-  uint32_t lo = 0, hi = 0;
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    lo |= (b0 + i < G ? static_cast<uint32_t>(row[b0 + i]) : kMxOne) << (8 * i);
-    hi |= (b0 + 4 + i < G ? static_cast<uint32_t>(row[b0 + 4 + i]) : kMxOne) << (8 * i);
+    w[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[i] |= (b + 4 * i + k < G ? static_cast<uint32_t>(row[b + 4 * i + k]) : kMxOne) << (8 * k);
   }
-  return make_uint2(lo, hi);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Word i of lane group g (16 lanes each) <-> word g of lane group i.
@@ -50,40 +52,53 @@ __device__ __forceinline__ void transpose_words(uint32_t (&w)[4]) {
   w[3] = d[1];
 }
 
-// What the tokens come as: MX4 codes, bf16, or bf16 twice (value and remainder).
-enum class Few { kMx4, kBf16, kBf16Twice };
-
-template <Few X, int RT, int NT>
+template <bool X4, int RT, int NT>
 struct FewUnit {
   uint4 c[2][RT];
-  uint2 e[RT];
-  uint4 x[2][NT][X == Few::kMx4 ? 1 : X == Few::kBf16 ? 4 : 8];
-  uint2 f[NT];
+  uint4 x[2][NT][X4 ? 1 : 4];
 };
 
 // A lane's pointers: wc at its row's codes + 16 q bytes, ws at its row's factors, xc at its
-// token's codes or values + 16 q bytes (xl: the remainders), xs at its token's factors, for
-// q = lane / 16; have: whether the lane has a token.
-template <Few X, int RT, int NT>
+// token's codes or values + 16 q bytes, xs at its token's factors, for q = lane / 16; have:
+// whether the lane has a token.
+template <bool X4, int RT, int NT>
 struct FewRows {
   const uint8_t* wc[RT];
   const uint8_t* ws[RT];
   const uint8_t* xc[NT];
-  const uint8_t* xl[NT];
   const uint8_t* xs[NT];
   bool have[NT];
 };
 
-// acc += the products over the units first, first + step, ... of G blocks.
-template <bool AHEAD, Few X, int RT, int NT>
-__device__ __forceinline__ void few_products(const FewRows<X, RT, NT>& p, int G, int first, int step,
+// acc += the products over the units [unit, end) of G blocks.
+//
+// Factors come 64 blocks (eight units) of a row at a time, 16 bytes to each of the row's four
+// lanes, and go from there to the lanes that need them: fetched a unit at a time they would be a
+// third of all the row segments that a wavefront asks for.
+template <bool AHEAD, bool X4, int RT, int NT>
+__device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, int G, int unit, int end,
                                              f32x4 (&acc)[RT][NT]) {
-  constexpr bool X4 = X == Few::kMx4;
-  constexpr int kX = X4 ? 1 : X == Few::kBf16 ? 4 : 8;
-  const int q = (threadIdx.x & 63) >> 4;
-  using Unit = FewUnit<X, RT, NT>;
+  constexpr int kX = X4 ? 1 : 4;
+  const int lane = threadIdx.x & 63, q = lane >> 4;
+  using Unit = FewUnit<X4, RT, NT>;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-  auto load = [&](int b0, Unit& v) {
+  uint4 fw[RT], fx[NT];
+  auto load_factors = [&](int first) {
+#pragma unroll
+    for (int a = 0; a < RT; ++a) fw[a] = sixteen_factors(p.ws[a], first * 8 + 16 * q, G);
+    if constexpr (X4) {
+#pragma unroll
+      for (int b = 0; b < NT; ++b) fx[b] = sixteen_factors(p.xs[b], first * 8 + 16 * q, G);
+    }
+  };
+  // factors of the four blocks of step s (of the sixteen that a fetch serves)
+  auto four = [&](const uint4& f, int s) {
+    const uint32_t even = s & 2 ? f.z : f.x, odd = s & 2 ? f.w : f.y;
+    return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * ((lane & 15) + 16 * (s >> 2)),
+                                                              static_cast<int>(s & 1 ? odd : even)));
+  };
+  auto load = [&](int u0, Unit& v) {
+    const int b0 = u0 * 8;
     const bool whole = b0 + 8 <= G;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -98,30 +113,28 @@ __device__ __forceinline__ void few_products(const FewRows<X, RT, NT>& p, int G,
 #pragma unroll
         for (int j = 0; j < kX; ++j) {
           v.x[u][b][j] = zero;
-          if (p.have[b] && (whole || blk + (X4 ? q : j % 4) < G))
-            v.x[u][b][j] = *reinterpret_cast<const uint4*>(
-                (j < 4 ? p.xc[b] : p.xl[b]) + blk * (X4 ? 16 : 64) + 64 * (j % 4));
+          if (p.have[b] && (whole || blk + (X4 ? q : j) < G))
+            v.x[u][b][j] = *reinterpret_cast<const uint4*>(p.xc[b] + blk * (X4 ? 16 : 64) + 64 * j);
         }
     }
-#pragma unroll
-    for (int a = 0; a < RT; ++a) v.e[a] = eight_factors(p.ws[a], b0, G, whole);
-    if constexpr (X4) {
-#pragma unroll
-      for (int b = 0; b < NT; ++b) v.f[b] = eight_factors(p.xs[b], b0, G, whole);
-    }
   };
-  auto multiply = [&](const Unit& v) {
+  auto multiply = [&](const Unit& v, int of_fetch) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      uint32_t f[NT];
+      if constexpr (X4) {
+#pragma unroll
+        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], 2 * of_fetch + u) >> (8 * q);
+      }
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
-        const uint32_t e = u ? v.e[a].y : v.e[a].x;
+        const uint32_t e = four(fw[a], 2 * of_fetch + u);
         if constexpr (X4) {
 #pragma unroll
           for (int b = 0; b < NT; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 mx_operand(v.c[u][a]), mx_operand(v.x[u][b][0]), acc[a][b], 4, 4, 0,
-                static_cast<int>(e >> (8 * q)), 0, static_cast<int>((u ? v.f[b].y : v.f[b].x) >> (8 * q)));
+                static_cast<int>(e >> (8 * q)), 0, static_cast<int>(f[b]));
         } else {
           uint32_t w[4] = {v.c[u][a].x, v.c[u][a].y, v.c[u][a].z, v.c[u][a].w};
           transpose_words(w);
@@ -129,38 +142,41 @@ __device__ __forceinline__ void few_products(const FewRows<X, RT, NT>& p, int G,
           for (int j = 0; j < 4; ++j) {
             const bf16x8 wv = mx_word_bf16(w[j], mx_factor((e >> (8 * j)) & 255u));
 #pragma unroll
-            for (int b = 0; b < NT; ++b) {
+            for (int b = 0; b < NT; ++b)
               acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                   wv, __builtin_bit_cast(bf16x8, v.x[u][b][j]), acc[a][b], 0, 0, 0);
-              if constexpr (kX == 8)
-                acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    wv, __builtin_bit_cast(bf16x8, v.x[u][b][4 + j]), acc[a][b], 0, 0, 0);
-            }
           }
         }
       }
     }
   };
-  int b0 = first * 8;
-  const int ahead = step * 8;
+  const int begin = unit;
+  auto fetch = [&](int u) {
+    if (((u - begin) & 7) == 0) load_factors(u);
+  };
   if constexpr (!AHEAD) {
-    for (; b0 < G; b0 += ahead) {
+    for (; unit < end; ++unit) {
       Unit u;
-      load(b0, u);
-      multiply(u);
+      fetch(unit);
+      load(unit, u);
+      multiply(u, (unit - begin) & 7);
     }
     return;
   }
   Unit u0, u1;
-  if (b0 < G) load(b0, u0);
-  while (b0 < G) {
-    if (b0 + ahead < G) load(b0 + ahead, u1);
-    multiply(u0);
-    b0 += ahead;
-    if (b0 >= G) break;
-    if (b0 + ahead < G) load(b0 + ahead, u0);
-    multiply(u1);
-    b0 += ahead;
+  if (unit < end) {
+    fetch(unit);
+    load(unit, u0);
+  }
+  while (unit < end) {
+    if (unit + 1 < end) load(unit + 1, u1);
+    multiply(u0, (unit - begin) & 7);
+    if (++unit >= end) break;
+    fetch(unit);
+    if (unit + 1 < end) load(unit + 1, u0);
+    multiply(u1, (unit - begin) & 7);
+    ++unit;
+    if (unit < end) fetch(unit);
   }
 }
 
