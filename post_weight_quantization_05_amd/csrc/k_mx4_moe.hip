@@ -133,7 +133,7 @@ __device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F fou
 // reach all experts (`compact`), the slot-th one that they reach.  The first one of a slot writes
 // its expert and pairs (t k + r) down for the launches after it.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a, int compact) {
-  __shared__ f32x4 part[kWaves][2][64];
+  __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
   __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
   __shared__ uint32_t reached[QZ_MOE_MAX_EXPERTS / 32];
   __shared__ int chosen[256];               // compact: n k < 256 experts
@@ -206,6 +206,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
   const int n = count;
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
   const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
+  int turn = 0;
   FewRows<false, 2, 1> rows;
   for (int64_t f0 = blockIdx.x * (int64_t)16; f0 < a.ldh; f0 += gridDim.x * (int64_t)16)
   for (int at = 0; at < n; at += 16) {
@@ -220,6 +221,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     few_products<false>(rows, G, u0, u1, acc);
+    auto& part = parts[turn];
+    turn ^= 1;
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -240,7 +243,6 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
       *reinterpret_cast<uint2*>(a.h_hi + o) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
       *reinterpret_cast<uint2*>(a.h_lo + o) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
     }
-    __syncthreads();
   }
 }
 
@@ -249,7 +251,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
 // pairs at a time: columns 0 to 7 of a tile are the values of h, 8 to 15 the remainders, and a
 // result is the sum of two columns; so both halves of h cost the loads and products of one.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs a) {
-  __shared__ f32x4 part[kWaves][2][64];
+  __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
@@ -261,6 +263,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
   const int G = static_cast<int>(a.Gf);
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
   const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
+  int turn = 0;
   FewRows<false, 2, 1> rows;
   for (int64_t r0 = blockIdx.x * (int64_t)32; r0 < a.d; r0 += gridDim.x * (int64_t)32)
   for (int at = 0; at < n; at += 8) {
@@ -275,6 +278,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
     rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     few_products<false>(rows, G, u0, u1, acc);
+    auto& part = parts[turn];
+    turn ^= 1;
     part[wave][0][lane] = acc[0][0];
     part[wave][1][lane] = acc[1][0];
     __syncthreads();
@@ -285,7 +290,6 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
       if (r < a.ldy)   // rows of the scratch are whole fours
         *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;
     }
-    __syncthreads();
   }
 }
 
@@ -348,7 +352,8 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   // wavefront per 256 columns, up to eight where there are few chunks of rows, else up to four.
   const auto shape = [&](int64_t chunks, int64_t G, dim3* grid, dim3* block) {
     const int64_t units = ceil_div(G, 8), most = chunks * slots <= 512 ? 8 : 4;
-    const int64_t waves = units < 2 ? 2 : units < most ? units : most;
+    const int64_t even = ceil_div(units, ceil_div(units, most));   // as many as share them evenly
+    const int64_t waves = even < 2 ? 2 : even;
     const int64_t width = ceil_div(256 * 16 / waves, slots);
     *grid = dim3(static_cast<unsigned>(chunks < width ? chunks : width), slots);
     *block = dim3(static_cast<unsigned>(64 * waves));

@@ -23,19 +23,32 @@ struct __attribute__((packed)) Bytes16 {
   uint32_t w[4];
 };
 
-// Sixteen factors of a row from block b on, at any alignment (1 past the row's end).
+// Sixteen factors of a row from block b on, at any alignment.  Past the row's end they are 0 (any
+// factor but the NaN will do, the codes there are zeros): the row's last sixteen bytes, moved down.
 __device__ __forceinline__ uint4 sixteen_factors(const uint8_t* row, int b, int G) {
-  if (b + 16 <= G) {
-    const Bytes16 v = *reinterpret_cast<const Bytes16*>(row + b);
-    return make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
-  }
-  uint32_t w[4];
+  uint32_t w[4] = {0, 0, 0, 0};
+  if (b < G) {
+    const int past = b + 16 - G;
+    if (past <= 0 || G >= 16) {
+      const Bytes16 v = *reinterpret_cast<const Bytes16*>(row + (past > 0 ? G - 16 : b));
+      uint64_t lo = static_cast<uint64_t>(v.w[1]) << 32 | v.w[0], hi = static_cast<uint64_t>(v.w[3]) << 32 | v.w[2];
+      if (past >= 8) {
+        lo = hi;
+        hi = 0;
+      }
+      if (past > 0 && past % 8) {
+        lo = lo >> (8 * (past % 8)) | hi << (64 - 8 * (past % 8));
+        hi >>= 8 * (past % 8);
+      }
+      w[0] = static_cast<uint32_t>(lo);
+      w[1] = static_cast<uint32_t>(lo >> 32);
+      w[2] = static_cast<uint32_t>(hi);
+      w[3] = static_cast<uint32_t>(hi >> 32);
+    } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      w[i] |= (b + 4 * i + k < G ? static_cast<uint32_t>(row[b + 4 * i + k]) : kMxOne) << (8 * k);
+      for (int i = 0; i < 16; ++i)
+        if (b + i < G) w[i / 4] |= static_cast<uint32_t>(row[b + i]) << (8 * (i % 4));
+    }
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
