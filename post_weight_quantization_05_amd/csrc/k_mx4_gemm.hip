@@ -49,6 +49,7 @@ constexpr int kSkinnyWaves = 8;
 template <bool X4, int RT, int NT>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4Product p) {
   __shared__ f32x4 part[kSkinnyWaves][RT * NT][64];
+  __shared__ __align__(16) uint8_t codes[kSkinnyWaves][RT * 2048];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
@@ -57,9 +58,10 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
   FewRows<X4, RT, NT> rows;
 #pragma unroll
   for (int a = 0; a < RT; ++a) {
-    const int64_t r = r0 + 16 * a + m < p.d_o ? r0 + 16 * a + m : p.d_o - 1;
-    rows.wc[a] = p.codes + r * G * 16 + 16 * q;
-    rows.ws[a] = p.scales + r * G;
+    const int64_t r = r0 + 16 * a < p.d_o ? r0 + 16 * a : p.d_o - 1;
+    rows.codes[a] = p.codes + r * G * 16;
+    rows.scales[a] = p.scales + r * G;
+    rows.last[a] = static_cast<int>(p.d_o - 1 - r < 15 ? p.d_o - 1 - r : 15);
   }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
@@ -74,7 +76,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
-  few_products<true>(rows, G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
+  few_products<true>(rows, codes[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

@@ -134,6 +134,7 @@ __device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F fou
 // its expert and pairs (t k + r) down for the launches after it.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a, int compact) {
   __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
+  __shared__ __align__(16) uint8_t codes[kWaves][2 * 2048];
   __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
   __shared__ uint32_t reached[QZ_MOE_MAX_EXPERTS / 32];
   __shared__ int chosen[256];               // compact: n k < 256 experts
@@ -204,23 +205,25 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
   }
   const int G = static_cast<int>(a.Gd);
   const int n = count;
+  e = __builtin_amdgcn_readfirstlane(e);
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
   const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
   int turn = 0;
   FewRows<false, 2, 1> rows;
   for (int64_t f0 = blockIdx.x * (int64_t)16; f0 < a.ldh; f0 += gridDim.x * (int64_t)16)
   for (int at = 0; at < n; at += 16) {
-    const int64_t row = f0 + m < a.f ? f0 + m : a.f - 1;
-    const int64_t base = e * 2 * a.f + row;
-    rows.wc[0] = a.gu_codes + base * G * 16 + 16 * q;
-    rows.ws[0] = a.gu_scales + base * G;
-    rows.wc[1] = rows.wc[0] + a.f * G * 16;
-    rows.ws[1] = rows.ws[0] + a.f * G;
+    const int64_t first = f0 < a.f ? f0 : a.f - 1;   // of the gate rows; the up rows follow
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      rows.codes[i] = a.gu_codes + (e * 2 * a.f + i * a.f + first) * G * 16;
+      rows.scales[i] = a.gu_scales + (e * 2 * a.f + i * a.f + first) * G;
+      rows.last[i] = static_cast<int>(a.f - 1 - first < 15 ? a.f - 1 - first : 15);
+    }
     rows.have[0] = at + m < n;
     const int pair = list[rows.have[0] ? at + m : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, G, u0, u1, acc);
+    few_products<false>(rows, codes[wave], G, u0, u1, acc);
     auto& part = parts[turn];
     turn ^= 1;
     part[wave][0][lane] = acc[0][0];
@@ -252,6 +255,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
 // result is the sum of two columns; so both halves of h cost the loads and products of one.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs a) {
   __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
+  __shared__ __align__(16) uint8_t codes[kWaves][2 * 2048];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
@@ -269,15 +273,16 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
   for (int at = 0; at < n; at += 8) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t row = r0 + 16 * i + m < a.d ? r0 + 16 * i + m : a.d - 1;
-      rows.wc[i] = a.dn_codes + (e * a.d + row) * G * 16 + 16 * q;
-      rows.ws[i] = a.dn_scales + (e * a.d + row) * G;
+      const int64_t first = r0 + 16 * i < a.d ? r0 + 16 * i : a.d - 1;
+      rows.codes[i] = a.dn_codes + (e * a.d + first) * G * 16;
+      rows.scales[i] = a.dn_scales + (e * a.d + first) * G;
+      rows.last[i] = static_cast<int>(a.d - 1 - first < 15 ? a.d - 1 - first : 15);
     }
     rows.have[0] = at + (m & 7) < n;
     const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + (m & 7)];
     rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, G, u0, u1, acc);
+    few_products<false>(rows, codes[wave], G, u0, u1, acc);
     auto& part = parts[turn];
     turn ^= 1;
     part[wave][0][lane] = acc[0][0];

@@ -2,9 +2,8 @@
 // few-token product and of the expert layer.
 //
 // A tile is 16 rows of W by 16 tokens.  The wavefront goes along d_i a unit of 256 columns at a
-// time: whole 128-byte lines of codes, straight from global memory to the matrix cores, since
-// every code is used once.  Of each 128 columns lane l loads row l % 16, block l / 16: 16 bytes of
-// codes.  AHEAD: the next unit's loads are issued before the current one's products (for one
+// time: whole 128-byte lines of codes.  Of each 128 columns lane l has row l % 16, block l / 16:
+// 16 bytes of codes.  AHEAD: the next unit's loads are issued before the current one's products (for one
 // workgroup a compute unit; with several of them the registers are better spent on more).
 //
 // bf16 X: a load of 16 bytes a lane covers 64 contiguous bytes of each row, so product j of the
@@ -71,13 +70,15 @@ struct FewUnit {
   uint4 x[2][NT][X4 ? 1 : 4];
 };
 
-// A lane's pointers: wc at its row's codes + 16 q bytes, ws at its row's factors, xc at its
-// token's codes or values + 16 q bytes, xs at its token's factors, for q = lane / 16; have:
-// whether the lane has a token.
+// RT tiles of 16 rows of W and a lane's tokens.  codes, scales: at a tile's first row (uniform);
+// last: its last row inside the matrix, counted from the first (rows past it are read as that one).
+// xc at the lane's token's codes or values + 16 q bytes, xs at its token's factors, for
+// q = lane / 16; have: whether the lane has a token.
 template <bool X4, int RT, int NT>
 struct FewRows {
-  const uint8_t* wc[RT];
-  const uint8_t* ws[RT];
+  const uint8_t* codes[RT];
+  const uint8_t* scales[RT];
+  int last[RT];
   const uint8_t* xc[NT];
   const uint8_t* xs[NT];
   bool have[NT];
@@ -88,9 +89,14 @@ struct FewRows {
 // Factors come 64 blocks (eight units) of a row at a time, 16 bytes to each of the row's four
 // lanes, and go from there to the lanes that need them: fetched a unit at a time they would be a
 // third of all the row segments that a wavefront asks for.
+//
+// lds: RT x 2048 bytes of the wavefront's own.  A load that the lanes of an operand made for
+// themselves would have 16 rows in each run of 16 lanes, and the memory pipeline takes four lanes
+// at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, and the lanes of
+// the operand read their blocks back from LDS.
 template <bool AHEAD, bool X4, int RT, int NT>
-__device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, int G, int unit, int end,
-                                             f32x4 (&acc)[RT][NT]) {
+__device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
+                                             int unit, int end, f32x4 (&acc)[RT][NT]) {
   constexpr int kX = X4 ? 1 : 4;
   const int lane = threadIdx.x & 63, q = lane >> 4;
   using Unit = FewUnit<X4, RT, NT>;
@@ -98,17 +104,18 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, int G
   uint4 fw[RT], fx[NT];
   auto load_factors = [&](int first) {
 #pragma unroll
-    for (int a = 0; a < RT; ++a) fw[a] = sixteen_factors(p.ws[a], first * 8 + 16 * q, G);
+    for (int a = 0; a < RT; ++a)
+      fw[a] = sixteen_factors(p.scales[a] + static_cast<int64_t>(lane / 4 < p.last[a] ? lane / 4 : p.last[a]) * G,
+                              first * 8 + 16 * (lane % 4), G);
     if constexpr (X4) {
 #pragma unroll
       for (int b = 0; b < NT; ++b) fx[b] = sixteen_factors(p.xs[b], first * 8 + 16 * q, G);
     }
   };
   // factors of the four blocks of step s (of the sixteen that a fetch serves)
-  auto four = [&](const uint4& f, int s) {
+  auto four = [&](const uint4& f, int s, int from) {
     const uint32_t even = s & 2 ? f.z : f.x, odd = s & 2 ? f.w : f.y;
-    return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * ((lane & 15) + 16 * (s >> 2)),
-                                                              static_cast<int>(s & 1 ? odd : even)));
+    return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * from, static_cast<int>(s & 1 ? odd : even)));
   };
   auto load = [&](int u0, Unit& v) {
     const int b0 = u0 * 8;
@@ -117,9 +124,12 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, int G
     for (int u = 0; u < 2; ++u) {
       const int blk = b0 + 4 * u;
 #pragma unroll
-      for (int a = 0; a < RT; ++a) {
+      for (int a = 0; a < RT; ++a) {   // rows 8 u to 8 u + 7, eight blocks each
+        const int row = 8 * u + lane / 8;
         v.c[u][a] = zero;
-        if (whole || blk + q < G) v.c[u][a] = *reinterpret_cast<const uint4*>(p.wc[a] + blk * 16);
+        if (whole || b0 + lane % 8 < G)
+          v.c[u][a] = *reinterpret_cast<const uint4*>(
+              p.codes[a] + (static_cast<uint32_t>(row < p.last[a] ? row : p.last[a]) * (16u * G) + 16 * (b0 + lane % 8)));
       }
 #pragma unroll
       for (int b = 0; b < NT; ++b)
@@ -131,25 +141,33 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, int G
         }
     }
   };
+  // chunk c of a row lies at chunk c ^ (row / 2 % 8) of its 128 bytes, off its neighbours' banks
+  const auto at = [](int row, int chunk) { return row * 128 + 16 * (chunk ^ (row >> 1 & 7)); };
   auto multiply = [&](const Unit& v, int of_fetch) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int a = 0; a < RT; ++a)
+        *reinterpret_cast<uint4*>(lds + 2048 * a + at(8 * u + lane / 8, lane % 8)) = v.c[u][a];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       uint32_t f[NT];
       if constexpr (X4) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], 2 * of_fetch + u) >> (8 * q);
+        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], 2 * of_fetch + u, (lane & 15) + 16 * ((2 * of_fetch + u) >> 2)) >> (8 * q);
       }
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
-        const uint32_t e = four(fw[a], 2 * of_fetch + u);
+        const uint32_t e = four(fw[a], 2 * of_fetch + u, 4 * (lane & 15) + ((2 * of_fetch + u) >> 2));
+        const uint4 c = *reinterpret_cast<const uint4*>(lds + 2048 * a + at(lane & 15, 4 * u + q));
         if constexpr (X4) {
 #pragma unroll
           for (int b = 0; b < NT; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                mx_operand(v.c[u][a]), mx_operand(v.x[u][b][0]), acc[a][b], 4, 4, 0,
+                mx_operand(c), mx_operand(v.x[u][b][0]), acc[a][b], 4, 4, 0,
                 static_cast<int>(e >> (8 * q)), 0, static_cast<int>(f[b]));
         } else {
-          uint32_t w[4] = {v.c[u][a].x, v.c[u][a].y, v.c[u][a].z, v.c[u][a].w};
+          uint32_t w[4] = {c.x, c.y, c.z, c.w};
           transpose_words(w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
