@@ -18,6 +18,7 @@ namespace qz {
 namespace {
 
 constexpr int kWaves = 8;      // of the logits' and the expert products' workgroups, at most
+constexpr int kWaveLds = 4096 + 2 * 2048;   // two tiles of codes; two tiles of sums, twice
 constexpr int kPerLane = QZ_MOE_MAX_EXPERTS / 64;
 
 // order of the experts of a token: descending logit, ties to the lower index
@@ -133,8 +134,7 @@ __device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F fou
 // reach all experts (`compact`), the slot-th one that they reach.  The first one of a slot writes
 // its expert and pairs (t k + r) down for the launches after it.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a, int compact) {
-  __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
-  __shared__ __align__(16) uint8_t codes[kWaves][2 * 2048];
+  extern __shared__ __align__(16) uint8_t smem[];   // of a wavefront: kWaveLds
   __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
   __shared__ uint32_t reached[QZ_MOE_MAX_EXPERTS / 32];
   __shared__ int chosen[256];               // compact: n k < 256 experts
@@ -209,6 +209,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
   const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
   int turn = 0;
+  auto part = [&](int w, int tile, int further = 0) -> f32x4& {
+    return reinterpret_cast<f32x4*>(smem + w * kWaveLds + 4096 + turn * 2048)[tile * 64 + lane + further];
+  };
   FewRows<false, 2, 1> rows;
   for (int64_t f0 = blockIdx.x * (int64_t)16; f0 < a.ldh; f0 += gridDim.x * (int64_t)16)
   for (int at = 0; at < n; at += 16) {
@@ -223,17 +226,16 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
     const int pair = list[rows.have[0] ? at + m : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, codes[wave], G, u0, u1, acc);
-    auto& part = parts[turn];
-    turn ^= 1;
-    part[wave][0][lane] = acc[0][0];
-    part[wave][1][lane] = acc[1][0];
+    few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
+    turn ^= 1;   // sums of two rounds in turn: one barrier each
+    part(wave, 0) = acc[0][0];
+    part(wave, 1) = acc[1][0];
     __syncthreads();
     if (wave == 0 && rows.have[0]) {
-      f32x4 g = part[0][0][lane], u = part[0][1][lane];
+      f32x4 g = part(0, 0), u = part(0, 1);
       for (int w = 1; w < waves; ++w) {
-        g += part[w][0][lane];
-        u += part[w][1][lane];
+        g += part(w, 0);
+        u += part(w, 1);
       }
       uint16_t hi[4], lo[4];
 #pragma unroll
@@ -254,8 +256,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
 // pairs at a time: columns 0 to 7 of a tile are the values of h, 8 to 15 the remainders, and a
 // result is the sum of two columns; so both halves of h cost the loads and products of one.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs a) {
-  __shared__ f32x4 parts[2][kWaves][2][64];   // of two rounds in turn: one barrier each
-  __shared__ __align__(16) uint8_t codes[kWaves][2 * 2048];
+  extern __shared__ __align__(16) uint8_t smem[];   // of a wavefront: kWaveLds
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
@@ -268,6 +269,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
   const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
   int turn = 0;
+  auto part = [&](int w, int tile, int further = 0) -> f32x4& {
+    return reinterpret_cast<f32x4*>(smem + w * kWaveLds + 4096 + turn * 2048)[tile * 64 + lane + further];
+  };
   FewRows<false, 2, 1> rows;
   for (int64_t r0 = blockIdx.x * (int64_t)32; r0 < a.d; r0 += gridDim.x * (int64_t)32)
   for (int at = 0; at < n; at += 8) {
@@ -282,15 +286,14 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
     const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + (m & 7)];
     rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, codes[wave], G, u0, u1, acc);
-    auto& part = parts[turn];
-    turn ^= 1;
-    part[wave][0][lane] = acc[0][0];
-    part[wave][1][lane] = acc[1][0];
+    few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
+    turn ^= 1;   // sums of two rounds in turn: one barrier each
+    part(wave, 0) = acc[0][0];
+    part(wave, 1) = acc[1][0];
     __syncthreads();
     if (wave < 2 && rows.have[0] && m < 8) {
-      f32x4 v = part[0][wave][lane] + part[0][wave][lane + 8];
-      for (int w = 1; w < waves; ++w) v += part[w][wave][lane] + part[w][wave][lane + 8];
+      f32x4 v = part(0, wave) + part(0, wave, 8);
+      for (int w = 1; w < waves; ++w) v += part(w, wave) + part(w, wave, 8);
       const int64_t r = r0 + 16 * wave + 4 * q;
       if (r < a.ldy)   // rows of the scratch are whole fours
         *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;
@@ -365,10 +368,10 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   };
   dim3 grid, block;
   shape(2 * a.Gf, a.Gd, &grid, &block);
-  hipLaunchKernelGGL(moe_up_kernel, grid, block, 0, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
+  hipLaunchKernelGGL(moe_up_kernel, grid, block, block.x / 64 * kWaveLds, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
   QZ_TRY(check_launch("moe_up"));
   shape(ceil_div(a.d, 32), a.Gf, &grid, &block);
-  hipLaunchKernelGGL(moe_down_kernel, grid, block, 0, s, a);
+  hipLaunchKernelGGL(moe_down_kernel, grid, block, block.x / 64 * kWaveLds, s, a);
   QZ_TRY(check_launch("moe_down"));
   hipLaunchKernelGGL(moe_sum_kernel,
                      dim3(static_cast<unsigned>(ceil_div(a.d, 1024)), static_cast<unsigned>(a.n)),
