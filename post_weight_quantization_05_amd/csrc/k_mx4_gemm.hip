@@ -65,8 +65,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
   }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    rows.have[b] = t0 + 16 * b + m < p.n;   // lanes without a token read nothing
-    const int64_t t = rows.have[b] ? t0 + 16 * b + m : p.n - 1;
+    const int64_t t = t0 + 16 * b + m < p.n ? t0 + 16 * b + m : p.n - 1;
     rows.xc[b] = (X4 ? p.xcodes + t * G * 16 : reinterpret_cast<const uint8_t*>(p.X + t * p.ldx)) + 16 * q;
     rows.xs[b] = X4 ? p.xscales + t * G : nullptr;
   }
@@ -76,7 +75,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
-  few_products<true>(rows, codes[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
+  few_products<X4 || RT * NT == 1>(rows, codes[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

@@ -222,8 +222,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
       rows.scales[i] = a.gu_scales + (e * 2 * a.f + i * a.f + first) * G;
       rows.last[i] = static_cast<int>(a.f - 1 - first < 15 ? a.f - 1 - first : 15);
     }
-    rows.have[0] = at + m < n;
-    const int pair = list[rows.have[0] ? at + m : at];
+    const bool have = at + m < n;
+    const int pair = list[have ? at + m : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
     part(wave, 0) = acc[0][0];
     part(wave, 1) = acc[1][0];
     __syncthreads();
-    if (wave == 0 && rows.have[0]) {
+    if (wave == 0 && have) {
       f32x4 g = part(0, 0), u = part(0, 1);
       for (int w = 1; w < waves; ++w) {
         g += part(w, 0);
@@ -282,8 +282,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
       rows.scales[i] = a.dn_scales + (e * a.d + first) * G;
       rows.last[i] = static_cast<int>(a.d - 1 - first < 15 ? a.d - 1 - first : 15);
     }
-    rows.have[0] = at + (m & 7) < n;
-    const int64_t pair = !rows.have[0] ? 0 : at == 0 ? early : list[at + (m & 7)];
+    const bool have = at + (m & 7) < n;
+    const int64_t pair = at == 0 ? (have ? early : list[0]) : list[have ? at + (m & 7) : at];
     rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
     few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
     part(wave, 0) = acc[0][0];
     part(wave, 1) = acc[1][0];
     __syncthreads();
-    if (wave < 2 && rows.have[0] && m < 8) {
+    if (wave < 2 && have && m < 8) {
       f32x4 v = part(0, wave) + part(0, wave, 8);
       for (int w = 1; w < waves; ++w) v += part(w, wave) + part(w, wave, 8);
       const int64_t r = r0 + 16 * wave + 4 * q;

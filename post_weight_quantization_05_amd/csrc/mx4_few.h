@@ -3,8 +3,7 @@
 //
 // A tile is 16 rows of W by 16 tokens.  The wavefront goes along d_i a unit of 256 columns at a
 // time: whole 128-byte lines of codes.  Of each 128 columns lane l has row l % 16, block l / 16:
-// 16 bytes of codes.  AHEAD: the next unit's loads are issued before the current one's products (for one
-// workgroup a compute unit; with several of them the registers are better spent on more).
+// 16 bytes of codes.
 //
 // bf16 X: a load of 16 bytes a lane covers 64 contiguous bytes of each row, so product j of the
 // four takes the columns 32 j + 8 (l / 16) + 0..7 of X, and the codes have to follow: a 4 x 4
@@ -64,16 +63,10 @@ __device__ __forceinline__ void transpose_words(uint32_t (&w)[4]) {
   w[3] = d[1];
 }
 
-template <bool X4, int RT, int NT>
-struct FewUnit {
-  uint4 c[2][RT];
-  uint4 x[2][NT][X4 ? 1 : 4];
-};
-
 // RT tiles of 16 rows of W and a lane's tokens.  codes, scales: at a tile's first row (uniform);
 // last: its last row inside the matrix, counted from the first (rows past it are read as that one).
 // xc at the lane's token's codes or values + 16 q bytes, xs at its token's factors, for
-// q = lane / 16; have: whether the lane has a token.
+// q = lane / 16; lanes without a token take another's (their columns are not stored).
 template <bool X4, int RT, int NT>
 struct FewRows {
   const uint8_t* codes[RT];
@@ -81,7 +74,6 @@ struct FewRows {
   int last[RT];
   const uint8_t* xc[NT];
   const uint8_t* xs[NT];
-  bool have[NT];
 };
 
 // acc += the products over the units [unit, end) of G blocks.
@@ -94,13 +86,18 @@ struct FewRows {
 // themselves would have 16 rows in each run of 16 lanes, and the memory pipeline takes four lanes
 // at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, and the lanes of
 // the operand read their blocks back from LDS.
+//
+// AHEAD (one workgroup a compute unit): the codes of the next unit are asked for before the products of the
+// current one, its tokens before them: results come back in the order of the requests, so waiting for the tokens leaves
+// the codes in flight.  Every lane always loads, at clamped places: behind a branch the compiler
+// does not know how many loads are in flight and waits for all.  Without AHEAD the registers go to
+// more wavefronts a compute unit, which wait in turn.
 template <bool AHEAD, bool X4, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
                                              int unit, int end, f32x4 (&acc)[RT][NT]) {
   constexpr int kX = X4 ? 1 : 4;
+  if (unit >= end) return;
   const int lane = threadIdx.x & 63, q = lane >> 4;
-  using Unit = FewUnit<X4, RT, NT>;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   uint4 fw[RT], fx[NT];
   auto load_factors = [&](int first) {
 #pragma unroll
@@ -112,38 +109,55 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
       for (int b = 0; b < NT; ++b) fx[b] = sixteen_factors(p.xs[b], first * 8 + 16 * q, G);
     }
   };
-  // factors of the four blocks of step s (of the sixteen that a fetch serves)
+  // factors of the four blocks of step s (of the sixteen that a fetch serves), held by lane `from`
   auto four = [&](const uint4& f, int s, int from) {
     const uint32_t even = s & 2 ? f.z : f.x, odd = s & 2 ? f.w : f.y;
     return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(4 * from, static_cast<int>(s & 1 ? odd : even)));
   };
-  auto load = [&](int u0, Unit& v) {
-    const int b0 = u0 * 8;
-    const bool whole = b0 + 8 <= G;
+  struct Codes {
+    uint4 c[2][RT];
+  };
+  uint4 x[2][NT][kX];
+  auto load_codes = [&](int u0, Codes& v) {   // eight lanes a row; rows 8 u to 8 u + 7
+    const int blk = u0 * 8 + lane % 8 < G ? u0 * 8 + lane % 8 : G - 1;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int blk = b0 + 4 * u;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int a = 0; a < RT; ++a) {   // rows 8 u to 8 u + 7, eight blocks each
+      for (int a = 0; a < RT; ++a) {
         const int row = 8 * u + lane / 8;
-        v.c[u][a] = zero;
-        if (whole || b0 + lane % 8 < G)
-          v.c[u][a] = *reinterpret_cast<const uint4*>(
-              p.codes[a] + (static_cast<uint32_t>(row < p.last[a] ? row : p.last[a]) * (16u * G) + 16 * (b0 + lane % 8)));
+        v.c[u][a] = *reinterpret_cast<const uint4*>(
+            p.codes[a] + (static_cast<uint32_t>(row < p.last[a] ? row : p.last[a]) * (16u * G) + 16 * blk));
       }
+  };
+  auto load_tokens = [&](int u0) {
 #pragma unroll
-      for (int b = 0; b < NT; ++b)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < kX; ++j) {
-          v.x[u][b][j] = zero;
-          if (p.have[b] && (whole || blk + (X4 ? q : j) < G))
-            v.x[u][b][j] = *reinterpret_cast<const uint4*>(p.xc[b] + blk * (X4 ? 16 : 64) + 64 * j);
-        }
-    }
+      for (int j = 0; j < kX; ++j) {
+        const int want = u0 * 8 + 4 * u + (X4 ? q : j);   // the lane's block
+        const int blk = want < G ? want : G - 1;
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+          x[u][b][j] = *reinterpret_cast<const uint4*>(p.xc[b] + (X4 ? 16 * (blk - q) : 64 * blk));
+      }
   };
   // chunk c of a row lies at chunk c ^ (row / 2 % 8) of its 128 bytes, off its neighbours' banks
   const auto at = [](int row, int chunk) { return row * 128 + 16 * (chunk ^ (row >> 1 & 7)); };
-  auto multiply = [&](const Unit& v, int of_fetch) {
+  auto multiply = [&](Codes& v, int u0, int of_fetch) {
+    if (u0 * 8 + 8 > G) {   // blocks past the end: zeros on both sides
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int a = 0; a < RT; ++a)
+          if (u0 * 8 + lane % 8 >= G) v.c[u][a] = zero;
+#pragma unroll
+        for (int b = 0; b < NT; ++b)
+#pragma unroll
+          for (int j = 0; j < kX; ++j)
+            if (u0 * 8 + 4 * u + (X4 ? q : j) >= G) x[u][b][j] = zero;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -151,20 +165,21 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
         *reinterpret_cast<uint4*>(lds + 2048 * a + at(8 * u + lane / 8, lane % 8)) = v.c[u][a];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
+      const int step = 2 * of_fetch + u;
       uint32_t f[NT];
       if constexpr (X4) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], 2 * of_fetch + u, (lane & 15) + 16 * ((2 * of_fetch + u) >> 2)) >> (8 * q);
+        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], step, (lane & 15) + 16 * (step >> 2)) >> (8 * q);
       }
 #pragma unroll
       for (int a = 0; a < RT; ++a) {
-        const uint32_t e = four(fw[a], 2 * of_fetch + u, 4 * (lane & 15) + ((2 * of_fetch + u) >> 2));
+        const uint32_t e = four(fw[a], step, 4 * (lane & 15) + (step >> 2));
         const uint4 c = *reinterpret_cast<const uint4*>(lds + 2048 * a + at(lane & 15, 4 * u + q));
         if constexpr (X4) {
 #pragma unroll
           for (int b = 0; b < NT; ++b)
             acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                mx_operand(c), mx_operand(v.x[u][b][0]), acc[a][b], 4, 4, 0,
+                mx_operand(c), mx_operand(x[u][b][0]), acc[a][b], 4, 4, 0,
                 static_cast<int>(e >> (8 * q)), 0, static_cast<int>(f[b]));
         } else {
           uint32_t w[4] = {c.x, c.y, c.z, c.w};
@@ -175,39 +190,45 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
 #pragma unroll
             for (int b = 0; b < NT; ++b)
               acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  wv, __builtin_bit_cast(bf16x8, v.x[u][b][j]), acc[a][b], 0, 0, 0);
+                  wv, __builtin_bit_cast(bf16x8, x[u][b][j]), acc[a][b], 0, 0, 0);
           }
         }
       }
     }
   };
   const int begin = unit;
-  auto fetch = [&](int u) {
-    if (((u - begin) & 7) == 0) load_factors(u);
-  };
   if constexpr (!AHEAD) {
     for (; unit < end; ++unit) {
-      Unit u;
-      fetch(unit);
-      load(unit, u);
-      multiply(u, (unit - begin) & 7);
+      Codes c;
+      load_codes(unit, c);
+      load_tokens(unit);
+      if (((unit - begin) & 7) == 0) load_factors(unit);
+      multiply(c, unit, (unit - begin) & 7);
     }
     return;
   }
-  Unit u0, u1;
-  if (unit < end) {
-    fetch(unit);
-    load(unit, u0);
-  }
-  while (unit < end) {
-    if (unit + 1 < end) load(unit + 1, u1);
-    multiply(u0, (unit - begin) & 7);
-    if (++unit >= end) break;
-    fetch(unit);
-    if (unit + 1 < end) load(unit + 1, u0);
-    multiply(u1, (unit - begin) & 7);
+  Codes c0, c1;
+  load_factors(unit);
+  load_codes(unit, c0);
+  while (true) {
+    load_tokens(unit);
+    if (unit + 1 == end) {
+      multiply(c0, unit, (unit - begin) & 7);
+      return;
+    }
+    load_codes(unit + 1, c1);
+    multiply(c0, unit, (unit - begin) & 7);
     ++unit;
-    if (unit < end) fetch(unit);
+    if (((unit - begin) & 7) == 0) load_factors(unit);
+    load_tokens(unit);
+    if (unit + 1 == end) {
+      multiply(c1, unit, (unit - begin) & 7);
+      return;
+    }
+    load_codes(unit + 1, c0);
+    multiply(c1, unit, (unit - begin) & 7);
+    ++unit;
+    if (((unit - begin) & 7) == 0) load_factors(unit);
   }
 }
 
