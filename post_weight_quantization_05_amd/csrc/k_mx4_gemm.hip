@@ -44,12 +44,13 @@ __device__ __forceinline__ void store4(const Mx4Product& p, int64_t t, int64_t r
 // ------------------------------------------------------------------------------ few tokens
 // Workgroup of 16 RT rows of W by 16 NT tokens; each of its wavefronts has a part of d_i (mx4_few.h).
 // Sums in fp32; the wavefronts' sums are added in their order.
-constexpr int kSkinnyWaves = 8;
+template <int RT, int NT>
+constexpr int kSkinnyWaves = RT * NT == 1 ? 8 : 4;
 
 template <bool X4, int RT, int NT>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4Product p) {
-  __shared__ f32x4 part[kSkinnyWaves][RT * NT][64];
-  __shared__ __align__(16) uint8_t codes[kSkinnyWaves][RT * 2048];
+__global__ __launch_bounds__((kSkinnyWaves<RT, NT>) * 64) void mx4_skinny_kernel(const Mx4Product p) {
+  __shared__ f32x4 part[kSkinnyWaves<RT, NT>][RT * NT][64];
+  __shared__ __align__(16) uint8_t lds[kSkinnyWaves<RT, NT>][kFewLds<true, X4, RT, NT>];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int m = lane & 15, q = lane >> 4;
@@ -65,9 +66,13 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
   }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
-    const int64_t t = t0 + 16 * b + m < p.n ? t0 + 16 * b + m : p.n - 1;
-    rows.xc[b] = (X4 ? p.xcodes + t * G * 16 : reinterpret_cast<const uint8_t*>(p.X + t * p.ldx)) + 16 * q;
-    rows.xs[b] = X4 ? p.xscales + t * G : nullptr;
+    const auto token = [&](int i) { return t0 + 16 * b + i < p.n ? t0 + 16 * b + i : p.n - 1; };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t t = token(8 * h + lane / 8);
+      rows.x[b][h] = X4 ? p.xcodes + t * G * 16 : reinterpret_cast<const uint8_t*>(p.X + t * p.ldx);
+    }
+    rows.xs[b] = X4 ? p.xscales + token(m) * G : nullptr;
   }
   f32x4 acc[RT][NT];
 #pragma unroll
@@ -75,7 +80,7 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void mx4_skinny_kernel(const Mx4
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
-  few_products<X4 || RT * NT == 1>(rows, codes[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
+  few_products<X4 || RT * NT == 1, true>(rows, lds[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

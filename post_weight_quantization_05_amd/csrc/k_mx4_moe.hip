@@ -224,9 +224,9 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
     }
     const bool have = at + m < n;
     const int pair = list[have ? at + m : at];
-    rows.xc[0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx) + 16 * q;
+    rows.x[0][0] = reinterpret_cast<const uint8_t*>(a.X + pair / a.k * a.ldx);
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
+    few_products<false, false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
     turn ^= 1;   // sums of two rounds in turn: one barrier each
     part(wave, 0) = acc[0][0];
     part(wave, 1) = acc[1][0];
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
       for (int i = 0; i < 4; ++i) {   // columns past f, to the end of the last block, are zero
         const float h = f0 + 4 * q + i < a.f ? g[i] / (1.f + expf(-g[i])) * u[i] : 0.f;
         hi[i] = f32_to_bf16(h);
-        lo[i] = f32_to_bf16(h - bf16_to_f32(hi[i]));
+        lo[i] = (hi[i] & 0x7f80) == 0x7f80 ? 0 : f32_to_bf16(h - bf16_to_f32(hi[i]));   // not inf - inf
       }
       const int64_t o = pair * a.ldh + f0 + 4 * q;
       *reinterpret_cast<uint2*>(a.h_hi + o) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
   const int m = lane & 15, q = lane >> 4;
   const int32_t* list = a.slot_pairs + blockIdx.y * a.n;
   // asked for together, as each is a trip to L2 (entries past the slot's count are not used)
-  const int early = list[(m & 7) < a.n ? m & 7 : 0];
+  const int early = list[(m & 7) < a.n ? m & 7 : 0], top = list[0];
   const int n = a.slot_count[blockIdx.y];
   const int e = a.slot_expert[blockIdx.y];
   const int G = static_cast<int>(a.Gf);
@@ -283,10 +283,10 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
       rows.last[i] = static_cast<int>(a.d - 1 - first < 15 ? a.d - 1 - first : 15);
     }
     const bool have = at + (m & 7) < n;
-    const int64_t pair = at == 0 ? (have ? early : list[0]) : list[have ? at + (m & 7) : at];
-    rows.xc[0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh) + 16 * q;
+    const int64_t pair = at == 0 ? (have ? early : top) : list[have ? at + (m & 7) : at];
+    rows.x[0][0] = reinterpret_cast<const uint8_t*>((m < 8 ? a.h_hi : a.h_lo) + pair * a.ldh);
     f32x4 acc[2][1] = {{f32x4{0.f, 0.f, 0.f, 0.f}}, {f32x4{0.f, 0.f, 0.f, 0.f}}};
-    few_products<false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
+    few_products<false, false>(rows, smem + wave * kWaveLds, G, u0, u1, acc);
     turn ^= 1;   // sums of two rounds in turn: one barrier each
     part(wave, 0) = acc[0][0];
     part(wave, 1) = acc[1][0];
@@ -358,19 +358,19 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   // As many workgroups as are resident at once (four wavefronts a SIMD): finding its expert's
   // tokens takes a workgroup 1 to 2 us, so each then goes on through the rows of its slot.  A
   // wavefront per 256 columns, up to eight where there are few chunks of rows, else up to four.
-  const auto shape = [&](int64_t chunks, int64_t G, dim3* grid, dim3* block) {
+  const auto shape = [&](int64_t chunks, int64_t G, int per_cu, dim3* grid, dim3* block) {
     const int64_t units = ceil_div(G, 8), most = chunks * slots <= 512 ? 8 : 4;
     const int64_t even = ceil_div(units, ceil_div(units, most));   // as many as share them evenly
     const int64_t waves = even < 2 ? 2 : even;
-    const int64_t width = ceil_div(256 * 16 / waves, slots);
+    const int64_t width = ceil_div(256 * 4 * per_cu / waves, slots);
     *grid = dim3(static_cast<unsigned>(chunks < width ? chunks : width), slots);
     *block = dim3(static_cast<unsigned>(64 * waves));
   };
   dim3 grid, block;
-  shape(2 * a.Gf, a.Gd, &grid, &block);
+  shape(2 * a.Gf, a.Gd, 4, &grid, &block);
   hipLaunchKernelGGL(moe_up_kernel, grid, block, block.x / 64 * kWaveLds, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
   QZ_TRY(check_launch("moe_up"));
-  shape(ceil_div(a.d, 32), a.Gf, &grid, &block);
+  shape(ceil_div(a.d, 32), a.Gf, 6, &grid, &block);
   hipLaunchKernelGGL(moe_down_kernel, grid, block, block.x / 64 * kWaveLds, s, a);
   QZ_TRY(check_launch("moe_down"));
   hipLaunchKernelGGL(moe_sum_kernel,

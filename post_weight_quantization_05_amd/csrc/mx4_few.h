@@ -65,16 +65,22 @@ __device__ __forceinline__ void transpose_words(uint32_t (&w)[4]) {
 
 // RT tiles of 16 rows of W and a lane's tokens.  codes, scales: at a tile's first row (uniform);
 // last: its last row inside the matrix, counted from the first (rows past it are read as that one).
-// xc at the lane's token's codes or values + 16 q bytes, xs at its token's factors, for
-// q = lane / 16; lanes without a token take another's (their columns are not stored).
+// x: codes or values of the tokens lane / 8 and lane / 8 + 8 of a tile, or, where the lanes of the
+// operand load them (not SHARED), of token lane % 16 at [0]; xs: factors of token lane % 16.
+// Places without a token take another's (their columns are not stored).
 template <bool X4, int RT, int NT>
 struct FewRows {
   const uint8_t* codes[RT];
   const uint8_t* scales[RT];
   int last[RT];
-  const uint8_t* xc[NT];
+  const uint8_t* x[NT][2];
   const uint8_t* xs[NT];
 };
+
+// LDS of a wavefront, bytes: its codes of a unit, and where the tokens pass through it (SHARED),
+// half a unit of 16 of them in bf16.
+template <bool SHARED, bool X4, int RT, int NT>
+constexpr int kFewLds = !SHARED ? 2048 * RT : X4 ? 2048 * (RT > NT ? RT : NT) : RT > 2 ? 2048 * RT : 4096;
 
 // acc += the products over the units [unit, end) of G blocks.
 //
@@ -82,17 +88,20 @@ struct FewRows {
 // lanes, and go from there to the lanes that need them: fetched a unit at a time they would be a
 // third of all the row segments that a wavefront asks for.
 //
-// lds: RT x 2048 bytes of the wavefront's own.  A load that the lanes of an operand made for
+// lds: kFewLds bytes of the wavefront's own.  A load that the lanes of an operand made for
 // themselves would have 16 rows in each run of 16 lanes, and the memory pipeline takes four lanes
-// at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, and the lanes of
-// the operand read their blocks back from LDS.
+// at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, of W and (SHARED) of X, and
+// the lanes of the operand read their parts back from LDS: codes first, then the tokens, half a
+// unit at a time, through the same bytes (a wavefront's LDS instructions stay in order).
+// 13 tokens, 12288 -> 4096: 10.2 us with X SHARED, 12.3 without; in the expert layer, where a tile
+// has a token or two and the other lanes repeat them, 143 and 129 us (7 tokens, 2 of 8 x 12288).
 //
 // AHEAD (one workgroup a compute unit): the codes of the next unit are asked for before the products of the
 // current one, its tokens before them: results come back in the order of the requests, so waiting for the tokens leaves
 // the codes in flight.  Every lane always loads, at clamped places: behind a branch the compiler
 // does not know how many loads are in flight and waits for all.  Without AHEAD the registers go to
 // more wavefronts a compute unit, which wait in turn.
-template <bool AHEAD, bool X4, int RT, int NT>
+template <bool AHEAD, bool SHARED, bool X4, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
                                              int unit, int end, f32x4 (&acc)[RT][NT]) {
   constexpr int kX = X4 ? 1 : 4;
@@ -117,7 +126,8 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
   struct Codes {
     uint4 c[2][RT];
   };
-  uint4 x[2][NT][kX];
+  // SHARED: [tile][rows 0 to 7, 8 to 15][piece of 128 bytes], else [tile][half of the unit][product]
+  uint4 x[NT][2][kX];
   auto load_codes = [&](int u0, Codes& v) {   // eight lanes a row; rows 8 u to 8 u + 7
     const int blk = u0 * 8 + lane % 8 < G ? u0 * 8 + lane % 8 : G - 1;
 #pragma unroll
@@ -130,67 +140,111 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
       }
   };
   auto load_tokens = [&](int u0) {
+    if constexpr (!SHARED) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < kX; ++j) {
-        const int want = u0 * 8 + 4 * u + (X4 ? q : j);   // the lane's block
-        const int blk = want < G ? want : G - 1;
+        for (int j = 0; j < kX; ++j) {
+          const int want = u0 * 8 + 4 * u + (X4 ? q : j);   // the lane's block
+          const int blk = want < G ? want : G - 1;
 #pragma unroll
-        for (int b = 0; b < NT; ++b)
-          x[u][b][j] = *reinterpret_cast<const uint4*>(p.xc[b] + (X4 ? 16 * (blk - q) : 64 * blk));
-      }
+          for (int b = 0; b < NT; ++b)
+            x[b][u][j] = *reinterpret_cast<const uint4*>(p.x[b][0] + (X4 ? 16 * blk : 64 * blk + 16 * q));
+        }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < kX; ++j) {
+      const int want = 8 * (kX * u0 + j) + lane % 8;   // chunk of 16 bytes
+      const int chunk = want < kX * G ? want : kX * G - 1;
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[b][h][j] = *reinterpret_cast<const uint4*>(p.x[b][h] + 16 * chunk);
+    }
   };
-  // chunk c of a row lies at chunk c ^ (row / 2 % 8) of its 128 bytes, off its neighbours' banks
+  // Rows of 128 bytes: chunk c of a row lies at chunk c ^ (row / 2 % 8), off its neighbours' banks.
+  // Rows of 256: at c ^ a permutation of the sixteen rows that puts neighbours into other halves.
   const auto at = [](int row, int chunk) { return row * 128 + 16 * (chunk ^ (row >> 1 & 7)); };
+  const auto at256 = [](int row, int chunk) { return row * 256 + 16 * (chunk ^ ((row >> 1 & 7) | (row & 1) << 3)); };
+  const auto put = [&](int place, const uint4& v) { *reinterpret_cast<uint4*>(lds + place) = v; };
+  const auto get = [&](int place) { return *reinterpret_cast<const uint4*>(lds + place); };
   auto multiply = [&](Codes& v, int u0, int of_fetch) {
+    const int r8 = lane / 8, c8 = lane % 8, m = lane & 15;
     if (u0 * 8 + 8 > G) {   // blocks past the end: zeros on both sides
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int a = 0; a < RT; ++a)
-          if (u0 * 8 + lane % 8 >= G) v.c[u][a] = zero;
+          if (u0 * 8 + c8 >= G) v.c[h][a] = zero;
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
           for (int j = 0; j < kX; ++j)
-            if (u0 * 8 + 4 * u + (X4 ? q : j) >= G) x[u][b][j] = zero;
+            if (SHARED ? 8 * (kX * u0 + j) + c8 >= kX * G : u0 * 8 + 4 * h + (X4 ? q : j) >= G) x[b][h][j] = zero;
       }
     }
 #pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int a = 0; a < RT; ++a) put(2048 * a + at(8 * h + r8, c8), v.c[h][a]);
+    uint4 c[2][RT];
+#pragma unroll
     for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int a = 0; a < RT; ++a)
-        *reinterpret_cast<uint4*>(lds + 2048 * a + at(8 * u + lane / 8, lane % 8)) = v.c[u][a];
+      for (int a = 0; a < RT; ++a) c[u][a] = get(2048 * a + at(m, 4 * u + q));
+    if constexpr (X4 && SHARED) {
+#pragma unroll
+      for (int b = 0; b < NT; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) put(2048 * b + at(8 * h + r8, c8), x[b][h][0]);
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int step = 2 * of_fetch + u;
-      uint32_t f[NT];
+      uint32_t e[RT];
+#pragma unroll
+      for (int a = 0; a < RT; ++a) e[a] = four(fw[a], step, 4 * m + (step >> 2));
       if constexpr (X4) {
 #pragma unroll
-        for (int b = 0; b < NT; ++b) f[b] = four(fx[b], step, (lane & 15) + 16 * (step >> 2)) >> (8 * q);
-      }
+        for (int b = 0; b < NT; ++b) {
+          const uint32_t f = four(fx[b], step, m + 16 * (step >> 2)) >> (8 * q);
+          const uint4 t = SHARED ? get(2048 * b + at(m, 4 * u + q)) : x[b][u][0];
 #pragma unroll
-      for (int a = 0; a < RT; ++a) {
-        const uint32_t e = four(fw[a], step, 4 * (lane & 15) + (step >> 2));
-        const uint4 c = *reinterpret_cast<const uint4*>(lds + 2048 * a + at(lane & 15, 4 * u + q));
-        if constexpr (X4) {
-#pragma unroll
-          for (int b = 0; b < NT; ++b)
+          for (int a = 0; a < RT; ++a)
             acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                mx_operand(c), mx_operand(x[u][b][0]), acc[a][b], 4, 4, 0,
-                static_cast<int>(e >> (8 * q)), 0, static_cast<int>(f[b]));
-        } else {
-          uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                mx_operand(c[u][a]), mx_operand(t), acc[a][b], 4, 4, 0,
+                static_cast<int>(e[a] >> (8 * q)), 0, static_cast<int>(f));
+        }
+      } else {
+        uint4 t[NT][4];
+#pragma unroll
+        for (int b = 0; b < NT; ++b) {
+          if constexpr (!SHARED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) t[b][j] = x[b][u][j % kX];
+            continue;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) put(at256(8 * h + r8, 8 * j + c8), x[b][h][(2 * u + j) % kX]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) t[b][j] = get(at256(m, 4 * j + q));
+        }
+#pragma unroll
+        for (int a = 0; a < RT; ++a) {
+          uint32_t w[4] = {c[u][a].x, c[u][a].y, c[u][a].z, c[u][a].w};
           transpose_words(w);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bf16x8 wv = mx_word_bf16(w[j], mx_factor((e >> (8 * j)) & 255u));
+            const bf16x8 wv = mx_word_bf16(w[j], mx_factor((e[a] >> (8 * j)) & 255u));
 #pragma unroll
             for (int b = 0; b < NT; ++b)
               acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  wv, __builtin_bit_cast(bf16x8, x[u][b][j]), acc[a][b], 0, 0, 0);
+                  wv, __builtin_bit_cast(bf16x8, t[b][j]), acc[a][b], 0, 0, 0);
           }
         }
       }
