@@ -175,21 +175,33 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
       for (int i = threadIdx.x; i < a.n * a.k; i += blockDim.x)
         if (chosen[i] == e) list[atomicAdd(&count, 1)] = i;
   } else {
-    for (int t = wave; t < a.n; t += waves) {
-      const double* lg = a.logits + t * a.E;
-      const double mine = lg[e];
-      int ahead = 0;
+    // four tokens at a time: their logits are one trip to L2
+    for (int t0 = 4 * wave; t0 < a.n; t0 += 4 * waves) {
+      double mine[4], lg[4][kPerLane];
 #pragma unroll
-      for (int i = 0; i < kPerLane; ++i) {
-        const int j = lane + 64 * i;
-        if (64 * i < a.E) ahead += __popcll(__ballot(j < a.E && before(lg[j < a.E ? j : 0], j, mine, e)));
+      for (int s = 0; s < 4; ++s) {
+        const double* row = a.logits + (t0 + s < a.n ? t0 + s : t0) * a.E;
+        mine[s] = row[e];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+          if (64 * i < a.E) lg[s][i] = row[lane + 64 * i < a.E ? lane + 64 * i : 0];
       }
-      if (ahead < a.k && lane == 0) {
-        const int pair = t * a.k + ahead;
-        list[atomicAdd(&count, 1)] = pair;
-        if (scribe) {
-          a.sel[pair] = e;
-          a.top[pair] = mine;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (t0 + s >= a.n) break;
+        int ahead = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+          const int j = lane + 64 * i;
+          if (64 * i < a.E) ahead += __popcll(__ballot(j < a.E && before(lg[s][i], j, mine[s], e)));
+        }
+        if (ahead < a.k && lane == 0) {
+          const int pair = (t0 + s) * a.k + ahead;
+          list[atomicAdd(&count, 1)] = pair;
+          if (scribe) {
+            a.sel[pair] = e;
+            a.top[pair] = mine[s];
+          }
         }
       }
     }
@@ -357,10 +369,14 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   const unsigned slots = static_cast<unsigned>(moe_slots(a.n, a.E, a.k));
   // As many workgroups as are resident at once (four wavefronts a SIMD): finding its expert's
   // tokens takes a workgroup 1 to 2 us, so each then goes on through the rows of its slot.  A
-  // wavefront per 256 columns, up to eight where there are few chunks of rows, else up to four.
+  // wavefront per 256 columns, up to eight, where there are few chunks of rows; else one per 1024,
+  // up to four (us: 48 tokens, 64 experts, 2048 columns: 2 58.9, 4 58.5, 1 82.2; 1408 columns: 2
+  // 35, 4 37.4; 7 tokens, 8 experts, 12288 columns: 2 48.8, 4 47.2, 1 66.2).
   const auto shape = [&](int64_t chunks, int64_t G, int per_cu, dim3* grid, dim3* block) {
-    const int64_t units = ceil_div(G, 8), most = chunks * slots <= 512 ? 8 : 4;
-    const int64_t even = ceil_div(units, ceil_div(units, most));   // as many as share them evenly
+    const int64_t units = ceil_div(G, 8);
+    const bool few = chunks * slots <= 512;
+    const int64_t want = few ? units : ceil_div(units, 4), most = few ? 8 : 4;
+    const int64_t even = ceil_div(units, ceil_div(units, want < most ? want : most));   // shares alike
     const int64_t waves = even < 2 ? 2 : even;
     const int64_t width = ceil_div(256 * 4 * per_cu / waves, slots);
     *grid = dim3(static_cast<unsigned>(chunks < width ? chunks : width), slots);
