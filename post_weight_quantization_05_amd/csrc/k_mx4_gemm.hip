@@ -650,22 +650,41 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
 // for each of the up to two resident ones when those are busy; then a launch, and for a split
 // contraction the pass that joins the sums.  Fitted to 400 measurements (20 to 2048 tokens, seven
 // layers of 512 to 12288 columns, 1 to 16 splits; 9% root mean square) and choosing within 8% of
-// the best one measured there in all but two, where it is 12% off.  For few tokens a workgroup's
-// time is the row segments it reads, 1.8 ns each (checked at 1 to 64 tokens: 2.4 ns at one token,
-// where HBM counts, 1.7 to 1.9 from 13 on).
-// Both sides, measured: 64 tokens 4096 -> 4096 bf16, few-token kernel 13.3 and best tile 16.4; 64
-// tokens 4096 -> 12288, 33 and 21.9 (128 x 32, four splits); 2048 tokens 4096 -> 4096, tiles of
-// 256 x 256 104, of 256 x 128 72; 128 tokens 12288 -> 4096, unsplit 97 or more, 16 splits 31.
+// the best one measured there in all but six, where it is up to 20% off.  A few-token kernel's unit
+// of 256 columns costs a wavefront `alone`, or `share` of the compute unit's time; fitted to 900
+// measurements (1 to 1024 tokens, nine layers of 512 to 25600 columns; 4 to 9%).
+// Both sides, measured, us (few-token shapes RT x NT of 16): 13 tokens 12288 -> 4096 bf16, 1 x 1 in
+// eight wavefronts 10.1, in four 13.3; one token 5120 -> 25600 bf16, 1 x 1 26.7, 2 x 1 17.0; 64
+// tokens 4096 -> 12288 bf16, 2 x 2 16.1 and the best tile, 128 x 32 in four splits, 21.8; 256 tokens
+// 4096 -> 4096 bf16, 4 x 2 18.2, 2 x 2 20.0, tile 24.9; 512 tokens there, 31.9 and 31.8; 2048
+// tokens, tiles of 256 x 256 81, of 256 x 128 72; MX4 X, 128 tokens 4096 -> 4096, 2 x 2 7.4, tile
+// 11.7; 256 tokens 4096 -> 12288, 36.7 and 17.0.
 namespace {
 
 struct Choice {
-  enum Kind { kFew11, kFew12, kFew22, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
+  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
   int splits;
 };
 struct TileTime {
   int bm, bn, resident;
   double alone, share;
 };
+struct FewTime {
+  int rt, nt, waves, resident;
+  double fixed, alone, share;   // us; per unit of 256 columns of a wavefront
+};
+constexpr FewTime kFew[2][6] = {   // shapes without a time: slower everywhere for that type
+    {{1, 1, 8, 1, 2.4, 1.50, 1.50}, {1, 1, 4, 2, 2.4, 0.87, 0.62}, {1, 2, 4, 0, 0, 0, 0},
+     {2, 1, 4, 4, 3.0, 1.07, 0.67}, {2, 2, 4, 4, 2.8, 1.50, 1.07}, {4, 2, 4, 2, 3.2, 2.25, 1.83}},
+    {{1, 1, 8, 1, 2.6, 0.62, 0.62}, {1, 1, 4, 4, 2.6, 0.39, 0.24}, {1, 2, 4, 3, 3.0, 0.51, 0.39},
+     {2, 1, 4, 0, 0, 0, 0}, {2, 2, 4, 2, 3.0, 0.81, 0.67}, {4, 2, 4, 0, 0, 0, 0}}};
+
+// `groups` workgroups of a compute unit, `resident` at once: one takes `alone`, r together at
+// least r times `share`.
+double rounds_time(double groups, int resident, double alone, double share) {
+  const double full = std::floor(groups / resident), rest = groups - full * resident;
+  return full * std::fmax(alone, resident * share) + (rest > 0 ? std::fmax(alone, rest * share) : 0.);
+}
 constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 of MX4
     {{256, 256, 1, 1.746, 1.746}, {256, 128, 1, 1.021, 1.021}, {128, 128, 2, 1.027, 0.513},
      {128, 64, 2, 0.592, 0.369}, {64, 64, 2, 0.477, 0.239}, {128, 32, 2, 0.427, 0.256}},
@@ -673,7 +692,6 @@ constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 o
      {128, 64, 2, 0.760, 0.495}, {64, 64, 2, 0.527, 0.264}, {128, 32, 2, 0.616, 0.308}}};
 
 Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
-  if (n <= 16) return {Choice::kFew11, 1};   // one tile of tokens: nothing to share
   Choice best{Choice::kFew11, 1};
   double best_t = 1e30;
   const auto consider = [&](Choice::Kind kind, int splits, double t) {
@@ -682,14 +700,13 @@ Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
       best = {kind, splits};
     }
   };
-  const int few[3][2] = {{1, 1}, {1, 2}, {2, 2}};
-  for (int i = 0; i < 3; ++i) {
-    const int rt = few[i][0], nt = few[i][1];
-    const double groups = static_cast<double>(ceil_div(d_o, 16 * rt)) * ceil_div(n, 16 * nt);
-    const int tokens = static_cast<int>(n < 16 * nt ? n : 16 * nt);
-    const double segments = 48 * rt + tokens * (x4 ? 3 : 8);
-    consider(static_cast<Choice::Kind>(Choice::kFew11 + i), 1,
-             3.0 + 1.8e-3 * std::ceil(groups / 256) * std::ceil(G / 8.0) * segments);
+  for (int i = 0; i < 6; ++i) {
+    const FewTime& c = kFew[x4][i];
+    if (!c.resident) continue;
+    const double groups = static_cast<double>(ceil_div(d_o, 16 * c.rt)) * ceil_div(n, 16 * c.nt);
+    const double units = static_cast<double>(ceil_div(ceil_div(G, 8), c.waves));
+    consider(static_cast<Choice::Kind>(Choice::kFew11x8 + i), 1,
+             c.fixed + units * rounds_time(std::ceil(groups / 256), c.resident, c.alone, c.share));
   }
   const int blocks = x4 ? 8 : 2, even = x4 ? 1 : 2;
   const int64_t all = ceil_div(G, blocks);
@@ -699,11 +716,7 @@ Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
     for (const int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
       const int64_t per = round_up(ceil_div(all, want), even), splits = ceil_div(all, per);
       if (splits != want || (want > 1 && (per < 2 || want * n * d_o > (int64_t{1} << 26)))) continue;
-      const double groups = std::ceil(tiles * splits / 256);
-      const double full = std::floor(groups / c.resident), rest = groups - full * c.resident;
-      double t = full * std::fmax(c.alone, c.resident * c.share);
-      if (rest > 0) t += std::fmax(c.alone, rest * c.share);
-      t = 4.0 + per * t;
+      double t = 4.0 + per * rounds_time(std::ceil(tiles * splits / 256), c.resident, c.alone, c.share);
       if (splits > 1) t += 4.0 + 1.3e-6 * splits * n * d_o;   // written and read, fp32
       consider(static_cast<Choice::Kind>(Choice::k256x256 + i), static_cast<int>(splits), t);
     }
@@ -715,10 +728,18 @@ template <bool X4>
 int launch_product(const Mx4Product& p, hipStream_t s) {
   const Choice c = choose(X4, p.n, p.d_o, p.G);
   switch (c.kind) {
-    // eight wavefronts along d_i; four where three or more workgroups share a compute unit
-    case Choice::kFew11: return launch_skinny<X4, 1, 1>(p, p.d_o > 512 * 16 ? 4 : 8, s);
-    case Choice::kFew12: return launch_skinny<X4, 1, 2>(p, 4, s);
+    case Choice::kFew11x8: return launch_skinny<X4, 1, 1>(p, 8, s);
+    case Choice::kFew11: return launch_skinny<X4, 1, 1>(p, 4, s);
+    case Choice::kFew12:
+      if constexpr (X4) return launch_skinny<X4, 1, 2>(p, 4, s);
+      break;
+    case Choice::kFew21:
+      if constexpr (!X4) return launch_skinny<X4, 2, 1>(p, 4, s);
+      break;
     case Choice::kFew22: return launch_skinny<X4, 2, 2>(p, 4, s);
+    case Choice::kFew42:
+      if constexpr (!X4) return launch_skinny<X4, 4, 2>(p, 4, s);
+      break;
     case Choice::k256x256: return launch_tile<X4, 2, 4, 4, 2>(p, c.splits, s);
     case Choice::k256x128: return launch_tile<X4, 4, 2, 2, 2>(p, c.splits, s);
     case Choice::k128x128: return launch_tile<X4, 2, 2, 2, 2>(p, c.splits, s);
