@@ -688,7 +688,7 @@ double rounds_time(double groups, int resident, double alone, double share) {
 constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 of MX4
     {{256, 256, 1, 1.746, 1.746}, {256, 128, 1, 1.021, 1.021}, {128, 128, 2, 1.027, 0.513},
      {128, 64, 2, 0.592, 0.369}, {64, 64, 2, 0.477, 0.239}, {128, 32, 2, 0.427, 0.256}},
-    {{256, 256, 1, 2.072, 2.072}, {256, 128, 1, 1.419, 1.419}, {128, 128, 2, 1.272, 0.636},
+    {{256, 256, 1, 2.072, 2.072}, {256, 128, 1, 1.419, 1.419}, {128, 128, 2, 1.272, 0.72},
      {128, 64, 2, 0.760, 0.495}, {64, 64, 2, 0.527, 0.264}, {128, 32, 2, 0.616, 0.308}}};
 
 Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {

@@ -253,6 +253,117 @@ def test_strided_inputs_and_outputs(n, d_i, d_o):
             assert torch.equal(y, ref), (off, dtype, four)
 
 
+# Sizes that reach each kernel shape of the products, unsplit and split along d_i: (n, d_i, d_o).
+EACH_LINEAR = [
+    (3, 95, 45), (2, 1179, 33), (16, 2080, 97), (1, 64, 9737), (13, 200, 9741), (17, 15, 4231), (21, 352, 4117),
+    (582, 475, 1365), (75, 1056, 2049), (18, 9, 9839), (25, 96, 8517), (17, 12123, 2833), (231, 27, 8457),
+    (747, 9209, 351), (66, 35, 10915), (300, 12079, 231), (1547, 21, 4875), (1615, 8991, 359), (514, 15, 7289),
+    (328, 12069, 901), (725, 9, 10891), (1074, 3343, 3985), (1996, 3531, 2059)]
+EACH_MATMUL = [
+    (3, 95, 45), (2, 1179, 33), (16, 2080, 97), (325, 305, 1763), (217, 9, 2077), (171, 96, 2635), (52, 9, 8251),
+    (49, 29, 8525), (618, 9719, 423), (154, 13, 11019), (522, 12065, 587), (194, 13, 9753), (678, 11513, 1693), (1343, 11213, 1799),
+    (647, 19, 6225), (1487, 283, 10851), (833, 7663, 2307), (1651, 15, 2519), (1098, 9, 7213), (849, 9907, 3141)]
+
+
+def _each(sizes, seed, matmul, integer):
+    """(result, 64-bit result) of integers against random codes, computed on the GPU; integer: the
+    values are multiples of `integer` and sums of their magnitudes stay below 2^24 of it."""
+    q, torch = qz(), _t()
+    n, d_i, d_o = sizes
+    rng = np.random.default_rng([n, d_i, d_o, seed])
+    codes, scales = _random_codes(rng, d_o, d_i)
+    w = to_dev(mx4.values(codes, scales, d_i))
+    bias = rng.integers(-50, 50, d_o).astype(np.float32) if (n + d_o) % 2 else None
+    b = None if bias is None else to_dev(bias)
+    if matmul:
+        xc, xs = _random_codes(rng, n, d_i)
+        x = to_dev(mx4.values(xc, xs, d_i))
+        got = q.qz_mx4_matmul(to_dev(xc), to_dev(xs), to_dev(codes), to_dev(scales), d_i, bias=b,
+                              out_dtype=torch.float32)
+    else:
+        xv, xd = _bf16(rng.integers(-8, 9, (n, d_i)))
+        x = to_dev(xv)
+        got = q.qz_mx4_linear(xd, to_dev(codes), to_dev(scales), bias=b, out_dtype=torch.float32)
+    assert float((x.abs() @ w.abs().T).max()) + 50 < integer * 2.0 ** 24
+    return got.double(), x @ w.T + (0 if b is None else b.double())
+
+
+@pytest.mark.parametrize("sizes", EACH_LINEAR)
+def test_linear_in_every_shape(sizes):
+    got, want = _each(sizes, 0, False, 2.0 ** -2)
+    assert _t().equal(got, want)
+
+
+@pytest.mark.parametrize("sizes", EACH_MATMUL)
+def test_matmul_in_every_shape(sizes):
+    got, want = _each(sizes, 1, True, 2.0 ** -4)
+    assert _t().equal(got, want)
+
+
+@pytest.mark.parametrize("n", [1, 13, 40, 200, 700])
+@pytest.mark.parametrize("d_i", [96, 544, 1056, 2080])
+def test_factors_and_codes_at_any_address(n, d_i):
+    """Factors at odd addresses, codes at an odd multiple of 16 bytes, as in one packed file."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng([n, d_i])
+
+    def moved(a, off):
+        buf = torch.full((a.size + off,), 255, dtype=torch.uint8, device="cuda")
+        buf[off:] = to_dev(a).reshape(-1)
+        return buf[off:].view(a.shape)
+
+    codes, scales = _random_codes(rng, 77, d_i)
+    x, xd = _bf16(rng.integers(-8, 9, (n, d_i)))
+    xc, xs = _random_codes(rng, n, d_i)
+    for off in (1, 2, 3):
+        got = q.qz_mx4_linear(xd, moved(codes, 16 * off), moved(scales, off), out_dtype=torch.float32)
+        np.testing.assert_array_equal(_host(got), x @ mx4.values(codes, scales, d_i).T)
+        got = q.qz_mx4_matmul(moved(xc, 16), moved(xs, 4 - off), moved(codes, 16 * off), moved(scales, off),
+                              d_i, out_dtype=torch.float32)
+        np.testing.assert_array_equal(_host(got), mx4.values(xc, xs, d_i) @ mx4.values(codes, scales, d_i).T)
+
+
+def test_products_past_32_bits():
+    """Codes, inputs and outputs whose last bytes lie more than 2^32 bytes from their first."""
+    q, torch = qz(), _t()
+    d_o, d_i = 600_000, 16384
+    g = torch.Generator("cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (d_o, d_i // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = torch.randint(126, 129, (d_o, d_i // 32), dtype=torch.uint8, device="cuda", generator=g)
+    pick = torch.tensor([0, 1, 262143, 262144, 524287, 524288, d_o - 2, d_o - 1], device="cuda")
+    w = mx4.values(to_host(codes[pick]), to_host(scales[pick]), d_i)
+    for n in (1, 9, 300):
+        x = torch.randint(-3, 4, (n, d_i), device="cuda", generator=g).to(torch.bfloat16)
+        y = q.qz_mx4_linear(x, codes, scales, out_dtype=torch.float32)[:, pick]
+        np.testing.assert_array_equal(_host(y), _host(x.double()) @ w.T)
+        xc, xs = q.qz_mx4_quantize(x)     # -3 .. 3: exact in E2M1
+        y = q.qz_mx4_matmul(xc, xs, codes, scales, d_i, out_dtype=torch.float32)[:, pick]
+        np.testing.assert_array_equal(_host(y), _host(x.double()) @ w.T)
+    del codes, scales, y
+    wide = torch.zeros((1100, 1 << 21), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((1100, 1 << 21), dtype=torch.bfloat16, device="cuda")
+    wide[:, :64] = torch.randint(-3, 4, (1100, 64), device="cuda", generator=g).to(torch.bfloat16)
+    c, s = _random_codes(np.random.default_rng(2), 48, 64)
+    q.qz_mx4_linear(wide[:, :64], to_dev(c), to_dev(s), out=out[:, 5:53])
+    want = torch.from_numpy(_host(wide[:, :64].double()) @ mx4.values(c, s, 64).T).to(torch.bfloat16)
+    assert torch.equal(out[:, 5:53].cpu(), want)
+    assert not out[:, :5].any() and not out[:, 53:101].any()
+
+
+def test_quantize_past_32_bits():
+    q, torch = qz(), _t()
+    rows, cols = 330_000, 8200
+    w = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    w.normal_(generator=torch.Generator("cuda").manual_seed(4))
+    pick = torch.tensor([0, 1, 131071, 131072, 261887, 261888, 261889, rows - 1], device="cuda")
+    for rule in ("floor", "least"):
+        c, s, v = q.qz_mx4_quantize(w, rule=rule, values=True)
+        c_ref, s_ref = mx4.quantize(w[pick].float().cpu().numpy(), rule)
+        np.testing.assert_array_equal(to_host(c[pick]), c_ref)
+        np.testing.assert_array_equal(to_host(s[pick]), s_ref)
+        np.testing.assert_array_equal(_host(v[pick].double()), mx4.values(c_ref, s_ref, cols))
+
+
 def test_empty_products():
     q, torch = qz(), _t()
     codes, scales = _random_codes(np.random.default_rng(0), 8, 64)
@@ -317,6 +428,71 @@ def test_moe(case):
     assert (np.abs(_host(w) - p) <= 2.0 ** -20 * p).all()
     assert (np.abs(_host(y) - want) <= bound).all(), np.max(np.abs(_host(y) - want) / bound)
     assert _t().equal(y, q.qz_mx4_moe(xd, rd, *dev, k, renorm=renorm))     # and again, to the bit
+
+
+MOE_CROWDED = [  # experts that get many tokens: several tiles of pairs, the last one part full
+    (256, 64, 40, 2, 1, True, "bf16"), (256, 96, 33, 3, 3, False, "f32"), (100, 256, 96, 1, 1, True, "bf16"),
+    (33, 544, 300, 5, 4, True, "bf16"), (256, 33, 65, 256, 2, False, "bf16"), (16, 64, 96, 256, 15, True, "f32"),
+    (15, 64, 96, 256, 16, True, "bf16"), (2, 2080, 1100, 12, 6, True, "bf16"), (48, 160, 520, 17, 16, False, "bf16")]
+
+
+@pytest.mark.parametrize("case", MOE_CROWDED)
+def test_moe_crowded(case):
+    test_moe(case)
+
+
+def test_moe_all_tokens_to_one_expert():
+    """Every token takes the same two experts of many; the others' slots stay empty."""
+    q, torch = qz(), _t()
+    n, d, f, E, k = 70, 128, 48, 40, 2
+    x, xd, router, rd, st, dev = _moe_inputs((n, d, f, E, k, True, "f32"))
+    xd = xd.abs()
+    rd[:] = 0
+    rd[39], rd[7] = 2.0, 1.0
+    x, router = _host(xd), _host(rd)
+    want, ids, p, bound = _moe_bound(x, router, mx4.values(st[0], st[1], d), mx4.values(st[2], st[3], f), k, True)
+    y, got, w = q.qz_mx4_moe(xd, rd, *dev, k, routing=True)
+    assert (to_host(got) == [39, 7]).all() and (ids == [39, 7]).all()
+    assert (np.abs(_host(y) - want) <= bound).all()
+
+
+def test_moe_past_32_bits():
+    """Experts whose weights begin more than 2^32 bytes from the first one's."""
+    q, torch = qz(), _t()
+    E, d, f = 256, 4096, 4160
+    g = torch.Generator("cuda").manual_seed(3)
+    gu = torch.randint(0, 256, (E, 2 * f, d // 2), dtype=torch.uint8, device="cuda", generator=g)
+    dn = torch.randint(0, 256, (E, d, f // 2), dtype=torch.uint8, device="cuda", generator=g)
+    gs = torch.full((E, 2 * f, d // 32), 118, dtype=torch.uint8, device="cuda")
+    ds = torch.full((E, d, f // 32), 118, dtype=torch.uint8, device="cuda")
+    x = torch.randn((2, d), device="cuda", generator=g).to(torch.bfloat16)
+    router = torch.zeros((E, d), device="cuda")
+    router[255], router[0], router[250] = x[0].float(), x[1].float(), x.float().sum(0) / 2
+    xh, ids = _host(x), [255, 250, 0]
+    # the same layer with those three experts alone
+    parts = [to_host(a[ids]) for a in (gu, gs, dn, ds)]
+    guv, dnv = mx4.values(parts[0], parts[1], d), mx4.values(parts[2], parts[3], f)
+    want, sub, p, bound = _moe_bound(xh, _host(router[ids]), guv, dnv, 2, True)
+    y, got, w = q.qz_mx4_moe(x, router, gu, gs, dn, ds, 2, routing=True)
+    np.testing.assert_array_equal(to_host(got), np.array(ids)[sub])
+    assert (np.abs(_host(y) - want) <= bound).all()
+
+
+def test_moe_without_renorm_and_a_nan_router_row():
+    """A NaN logit counts as -inf in the softmax over all experts too."""
+    q, torch = qz(), _t()
+    x, xd, router, rd, st, dev = _moe_inputs((6, 64, 32, 8, 2, False, "bf16"))
+    r2 = rd.clone()
+    r2[3] = float("nan")
+    y, ids, w = q.qz_mx4_moe(xd, r2, *dev, 2, renorm=False, routing=True)
+    keep = [0, 1, 2, 4, 5, 6, 7]
+    logits = x @ router[keep].T
+    p = np.exp(logits - logits.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    order = np.argsort(-logits, axis=1, kind="stable")[:, :2]
+    np.testing.assert_array_equal(to_host(ids), np.array(keep)[order])
+    assert (np.abs(_host(w) - np.take_along_axis(p, order, 1)) <= 2.0 ** -20).all()
+    assert not torch.isnan(y).any()
 
 
 def test_moe_ties_and_strides():
@@ -385,6 +561,49 @@ def test_streams_and_graph_replays():
         want = chain(fresh)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want)), seed
+
+
+def test_two_streams_at_once():
+    """The same operators on two streams at a time, each call with its own workspace."""
+    q, torch = qz(), _t()
+    x, xd, router, rd, st, dev = _moe_inputs((12, 512, 128, 16, 4, True, "bf16"))
+    codes, scales = q.qz_mx4_quantize(torch.randn((2059, 3531), device="cuda"))
+    big = torch.randn((1996, 3531), device="cuda").to(torch.bfloat16)     # split sums, padded rows
+
+    def work():
+        c, s = q.qz_mx4_quantize(big)
+        return (q.qz_mx4_moe(xd, rd, *dev, 4), q.qz_mx4_linear(big, codes, scales),
+                q.qz_mx4_matmul(c, s, codes, scales, 3531), q.qz_mx4_linear(big[:7], codes, scales))
+
+    want = work()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(work())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+
+
+def test_tensors_of_another_device_are_refused():
+    q, torch = qz(), _t()
+    x = torch.ones((2, 64), dtype=torch.bfloat16, device="cuda")
+    c, s = q.qz_mx4_quantize(x)
+    for bad in ((x, c.cpu(), s), (x, c, s.cpu()), (x.cpu(), c, s)):
+        with pytest.raises(ValueError):
+            q.qz_mx4_linear(*bad)
+    with pytest.raises(ValueError):
+        q.qz_mx4_linear(x, c, s, bias=torch.zeros(2))
+    with pytest.raises(ValueError):
+        q.qz_mx4_linear(x, c, s, out=torch.zeros((2, 2), dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        q.qz_mx4_matmul(c, s.cpu(), c, s, 64)
+    with pytest.raises(ValueError):
+        q.qz_mx4_unpack(c, s.cpu(), 64)
+    with pytest.raises(ValueError):
+        q.qz_mx4_quantize(x, rule="least", colw=torch.ones(64))
 
 
 def test_calibrate_quantise_and_use():
