@@ -654,15 +654,15 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
 // of 256 columns costs a wavefront `alone`, or `share` of the compute unit's time; fitted to 900
 // measurements (1 to 1024 tokens, nine layers of 512 to 25600 columns; 4 to 9%).
 // Both sides, measured, us (few-token shapes RT x NT of 16): 13 tokens 12288 -> 4096 bf16, 1 x 1 in
-// eight wavefronts 10.1, in four 13.3; one token 5120 -> 25600 bf16, 1 x 1 26.7, 2 x 1 17.0; 64
+// eight wavefronts 8.9, in four 11.2; one token 5120 -> 25600 bf16, 1 x 1 18.8, 2 x 1 17.0; 64
 // tokens 4096 -> 12288 bf16, 2 x 2 16.1 and the best tile, 128 x 32 in four splits, 21.8; 256 tokens
 // 4096 -> 4096 bf16, 4 x 2 18.2, 2 x 2 20.0, tile 24.9; 512 tokens there, 31.9 and 31.8; 2048
-// tokens, tiles of 256 x 256 81, of 256 x 128 72; MX4 X, 128 tokens 4096 -> 4096, 2 x 2 7.4, tile
-// 11.7; 256 tokens 4096 -> 12288, 36.7 and 17.0.
+// tokens, tiles of 256 x 256 81, of 256 x 128 72; MX4 X, 128 tokens 4096 -> 4096, 2 x 2 7.1, 2 x 4
+// 7.7, tile 11.7; 256 tokens there, 11.1, 10.0, 11.9; 256 tokens 4096 -> 12288, 28.2, 27.7, 17.0.
 namespace {
 
 struct Choice {
-  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
+  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
   int splits;
 };
 struct TileTime {
@@ -673,11 +673,13 @@ struct FewTime {
   int rt, nt, waves, resident;
   double fixed, alone, share;   // us; per unit of 256 columns of a wavefront
 };
-constexpr FewTime kFew[2][6] = {   // shapes without a time: slower everywhere for that type
-    {{1, 1, 8, 1, 2.4, 1.50, 1.50}, {1, 1, 4, 2, 2.4, 0.87, 0.62}, {1, 2, 4, 0, 0, 0, 0},
-     {2, 1, 4, 4, 3.0, 1.07, 0.67}, {2, 2, 4, 4, 2.8, 1.50, 1.07}, {4, 2, 4, 2, 3.2, 2.25, 1.83}},
-    {{1, 1, 8, 1, 2.6, 0.62, 0.62}, {1, 1, 4, 4, 2.6, 0.39, 0.24}, {1, 2, 4, 3, 3.0, 0.51, 0.39},
-     {2, 1, 4, 0, 0, 0, 0}, {2, 2, 4, 2, 3.0, 0.81, 0.67}, {4, 2, 4, 0, 0, 0, 0}}};
+constexpr FewTime kFew[2][7] = {   // shapes without a time: slower everywhere for that type
+    {{1, 1, 8, 3, 3.0, 1.00, 0.93}, {1, 1, 4, 4, 3.2, 0.62, 0.44}, {1, 2, 4, 0, 0, 0, 0},
+     {2, 1, 4, 4, 3.2, 1.00, 0.67}, {2, 2, 4, 4, 3.0, 1.50, 1.07}, {2, 4, 4, 0, 0, 0, 0},
+     {4, 2, 4, 2, 3.2, 2.40, 1.71}},
+    {{1, 1, 8, 1, 3.2, 0.54, 0.54}, {1, 1, 4, 4, 3.2, 0.36, 0.21}, {1, 2, 4, 4, 3.2, 0.51, 0.34},
+     {2, 1, 4, 0, 0, 0, 0}, {2, 2, 4, 3, 3.2, 0.71, 0.54}, {2, 4, 4, 2, 3.2, 1.22, 0.93},
+     {4, 2, 4, 0, 0, 0, 0}}};
 
 // `groups` workgroups of a compute unit, `resident` at once: one takes `alone`, r together at
 // least r times `share`.
@@ -700,7 +702,7 @@ Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
       best = {kind, splits};
     }
   };
-  for (int i = 0; i < 6; ++i) {
+  for (int i = 0; i < 7; ++i) {
     const FewTime& c = kFew[x4][i];
     if (!c.resident) continue;
     const double groups = static_cast<double>(ceil_div(d_o, 16 * c.rt)) * ceil_div(n, 16 * c.nt);
@@ -708,6 +710,7 @@ Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
     consider(static_cast<Choice::Kind>(Choice::kFew11x8 + i), 1,
              c.fixed + units * rounds_time(std::ceil(groups / 256), c.resident, c.alone, c.share));
   }
+  if (n <= 16) return best;   // a large tile would be mostly empty
   const int blocks = x4 ? 8 : 2, even = x4 ? 1 : 2;
   const int64_t all = ceil_div(G, blocks);
   for (int i = 0; i < 6; ++i) {
@@ -737,6 +740,9 @@ int launch_product(const Mx4Product& p, hipStream_t s) {
       if constexpr (!X4) return launch_skinny<X4, 2, 1>(p, 4, s);
       break;
     case Choice::kFew22: return launch_skinny<X4, 2, 2>(p, 4, s);
+    case Choice::kFew24:
+      if constexpr (X4) return launch_skinny<X4, 2, 4>(p, 4, s);
+      break;
     case Choice::kFew42:
       if constexpr (!X4) return launch_skinny<X4, 4, 2>(p, 4, s);
       break;

@@ -96,11 +96,13 @@ constexpr int kFewLds = !SHARED ? 2048 * RT : X4 ? 2048 * (RT > NT ? RT : NT) : 
 // 13 tokens, 12288 -> 4096: 10.2 us with X SHARED, 12.3 without; in the expert layer, where a tile
 // has a token or two and the other lanes repeat them, 143 and 129 us (7 tokens, 2 of 8 x 12288).
 //
-// AHEAD (one workgroup a compute unit): the codes of the next unit are asked for before the products of the
-// current one, its tokens before them: results come back in the order of the requests, so waiting for the tokens leaves
-// the codes in flight.  Every lane always loads, at clamped places: behind a branch the compiler
-// does not know how many loads are in flight and waits for all.  Without AHEAD the registers go to
-// more wavefronts a compute unit, which wait in turn.
+// AHEAD: the codes of the next unit are asked for before the products of the current one, its
+// tokens before them: results come back in the order of the requests, so waiting for the tokens
+// leaves the codes in flight.  Every lane always loads, at clamped places: behind a branch the
+// compiler does not know how many loads are in flight and waits for all.  Where the tile needs so
+// many registers that this costs wavefronts, those hide the latency better (us, with and without:
+// 13 tokens 12288 -> 4096, 1 x 1 tiles, 8.9 and 10.1; 256 tokens 4096 -> 4096, 4 x 2 tiles, 23.5
+// and 18.2; the same in MX4, 2 x 2, 11.1 and 13.0).
 template <bool AHEAD, bool SHARED, bool X4, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
                                              int unit, int end, f32x4 (&acc)[RT][NT]) {
@@ -261,29 +263,18 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
     }
     return;
   }
-  Codes c0, c1;
+  Codes c, next;
   load_factors(unit);
-  load_codes(unit, c0);
-  while (true) {
+  load_codes(unit, c);
+  for (; unit + 1 < end; ++unit) {
     load_tokens(unit);
-    if (unit + 1 == end) {
-      multiply(c0, unit, (unit - begin) & 7);
-      return;
-    }
-    load_codes(unit + 1, c1);
-    multiply(c0, unit, (unit - begin) & 7);
-    ++unit;
-    if (((unit - begin) & 7) == 0) load_factors(unit);
-    load_tokens(unit);
-    if (unit + 1 == end) {
-      multiply(c1, unit, (unit - begin) & 7);
-      return;
-    }
-    load_codes(unit + 1, c0);
-    multiply(c1, unit, (unit - begin) & 7);
-    ++unit;
-    if (((unit - begin) & 7) == 0) load_factors(unit);
+    load_codes(unit + 1, next);
+    multiply(c, unit, (unit - begin) & 7);
+    c = next;
+    if (((unit + 1 - begin) & 7) == 0) load_factors(unit + 1);
   }
+  load_tokens(unit);
+  multiply(c, unit, (unit - begin) & 7);
 }
 
 }  // namespace qz

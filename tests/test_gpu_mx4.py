@@ -258,11 +258,11 @@ EACH_LINEAR = [
     (3, 95, 45), (2, 1179, 33), (16, 2080, 97), (1, 64, 9737), (13, 200, 9741), (17, 15, 4231), (21, 352, 4117),
     (582, 475, 1365), (75, 1056, 2049), (18, 9, 9839), (25, 96, 8517), (17, 12123, 2833), (231, 27, 8457),
     (747, 9209, 351), (66, 35, 10915), (300, 12079, 231), (1547, 21, 4875), (1615, 8991, 359), (514, 15, 7289),
-    (328, 12069, 901), (725, 9, 10891), (1074, 3343, 3985), (1996, 3531, 2059)]
+    (34, 19, 4289), (185, 11509, 803), (95, 10327, 2773), (328, 12069, 901), (725, 9, 10891), (1074, 3343, 3985), (1996, 3531, 2059)]
 EACH_MATMUL = [
     (3, 95, 45), (2, 1179, 33), (16, 2080, 97), (325, 305, 1763), (217, 9, 2077), (171, 96, 2635), (52, 9, 8251),
     (49, 29, 8525), (618, 9719, 423), (154, 13, 11019), (522, 12065, 587), (194, 13, 9753), (678, 11513, 1693), (1343, 11213, 1799),
-    (647, 19, 6225), (1487, 283, 10851), (833, 7663, 2307), (1651, 15, 2519), (1098, 9, 7213), (849, 9907, 3141)]
+    (688, 645, 1089), (720, 10461, 359), (647, 19, 6225), (1487, 283, 10851), (833, 7663, 2307), (1651, 15, 2519), (1098, 9, 7213), (849, 9907, 3141)]
 
 
 def _each(sizes, seed, matmul, integer):
