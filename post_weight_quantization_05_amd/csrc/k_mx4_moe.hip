@@ -11,6 +11,11 @@
 // (mx4_few.h); what bounds the layer is reading them from HBM.  h is kept as two bf16 numbers
 // (value and remainder, 16 bits of mantissa together): the matrix cores take bf16, and rounding h
 // once to bf16 would be as large an error as the final rounding of y.
+//
+// Measured, us (launch 2 and 3; all four): one token, 8 of 128 experts, 4096 x 1024, 54 MB: 14.6,
+// 7.4; 29; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 56, 37; 101; 7 tokens, 2 of 8, 4096 x 12288,
+// seven reached, 561 MB: 87, 46; 132 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
+// and 4 are 4.7 and 4.5, of which a launch alone is 3.3.
 #include "mx4_few.h"
 
 namespace qz {

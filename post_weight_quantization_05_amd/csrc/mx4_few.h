@@ -93,8 +93,9 @@ constexpr int kFewLds = !SHARED ? 2048 * RT : X4 ? 2048 * (RT > NT ? RT : NT) : 
 // at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, of W and (SHARED) of X, and
 // the lanes of the operand read their parts back from LDS: codes first, then the tokens, half a
 // unit at a time, through the same bytes (a wavefront's LDS instructions stay in order).
-// 13 tokens, 12288 -> 4096: 10.2 us with X SHARED, 12.3 without; in the expert layer, where a tile
-// has a token or two and the other lanes repeat them, 143 and 129 us (7 tokens, 2 of 8 x 12288).
+// 13 tokens, 12288 -> 4096, before the codes were loaded ahead: 10.2 us with X SHARED, 12.3 without;
+// in the expert layer, where a tile has a token or two and the other lanes repeat them, 143 and 129
+// us (7 tokens, 2 of 8 x 12288).
 //
 // AHEAD: the codes of the next unit are asked for before the products of the current one, its
 // tokens before them: results come back in the order of the requests, so waiting for the tokens
