@@ -364,6 +364,23 @@ def test_quantize_past_32_bits():
         np.testing.assert_array_equal(_host(v[pick].double()), mx4.values(c_ref, s_ref, cols))
 
 
+def test_quantize_past_2_32_pieces():
+    """More than 2^32 pieces of eight columns: the index is 64 bits wide."""
+    q, torch = qz(), _t()
+    rows, cols = 4_200_000, 8192
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GB of free GPU memory")
+    w = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
+    pick = torch.tensor([0, 1, 2097151, 2097152, 4194303, 4194304, rows - 1], device="cuda")
+    w[pick] = torch.randn((7, cols), device="cuda").to(torch.bfloat16)
+    c, s = q.qz_mx4_quantize(w)
+    c_ref, s_ref = mx4.quantize(w[pick].float().cpu().numpy())
+    np.testing.assert_array_equal(to_host(c[pick]), c_ref)
+    np.testing.assert_array_equal(to_host(s[pick]), s_ref)
+    others = torch.tensor([2, 2097150, 2097153, 4194302, 4194305, rows - 2], device="cuda")
+    assert not c[others].any() and not s[others].any()
+
+
 def test_empty_products():
     q, torch = qz(), _t()
     codes, scales = _random_codes(np.random.default_rng(0), 8, 64)
