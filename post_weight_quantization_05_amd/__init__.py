@@ -379,12 +379,14 @@ def _mx4_pair(codes, scales, rows, cols, name, index):
     """Checks that codes and scales store `rows` rows of `cols` columns, on GPU `index`."""
     blocks = (cols + 31) >> 5
     u8 = _torch().uint8
-    if codes.dtype != u8 or scales.dtype != u8:
+    if codes.dtype is not u8 or scales.dtype is not u8:
         raise TypeError(f"{name}: codes and scales must be uint8")
     if codes.get_device() != index or scales.get_device() != index:
         raise ValueError(f"{name}: codes and scales must be on GPU {index}")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous")
+    if codes.shape == (rows, 16 * blocks) and scales.shape == (rows, blocks):
+        return
     if codes.shape[-1] != 16 * blocks or scales.shape[-1] != blocks \
             or codes.numel() != 16 * blocks * rows or scales.numel() != blocks * rows:
         raise ValueError(f"{name}: expected {rows} rows of {16 * blocks} code bytes and {blocks} factors")
@@ -440,9 +442,9 @@ def qz_mx4_quantize(W, rule="floor", colw=None, values=False):
     if rule not in ("floor", "least"):
         raise ValueError(f"rule must be 'floor' or 'least', not {rule!r}")
     dev, blocks = W.device, (cols + 31) >> 5
-    codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=dev)
-    scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
-    out = torch.empty((rows, cols), dtype=W.dtype, device=dev) if values else None
+    codes = W.new_empty((rows, 16 * blocks), dtype=torch.uint8)
+    scales = codes.new_empty((rows, blocks))
+    out = W.new_empty((rows, cols)) if values else None
     _run(dev.index, lib().qz_mx4_quantize, W.data_ptr(), wt, rows, cols, ld,
          _lib.QZ_MX4_LEAST if rule == "least" else _lib.QZ_MX4_FLOOR,
          _vector(colw, cols, "colw", dev.index), codes.data_ptr(), scales.data_ptr(),
@@ -465,12 +467,15 @@ def qz_mx4_unpack(codes, scales, cols):
     return out, s, z
 
 
-def _product_out(out, n, d_o, dtype, device):
-    """(out, its row stride, its dtype code) for a product's result."""
+def _product_out(out, like, n, d_o, dtype, device):
+    """(out, its row stride, its dtype code) for a product's result, on the GPU of `like`."""
     torch = _torch()
     if out is None:
-        out = torch.empty((n, d_o), dtype=dtype or torch.bfloat16, device=device)
-        return out, d_o, _dtype_code(out)
+        if dtype is None or dtype is torch.bfloat16:
+            return like.new_empty((n, d_o), dtype=torch.bfloat16), d_o, _lib.QZ_BF16
+        if dtype is not torch.float32:
+            raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
+        return like.new_empty((n, d_o), dtype=dtype), d_o, _lib.QZ_F32
     if tuple(out.shape) != (n, d_o) or (dtype is not None and out.dtype != dtype):
         raise ValueError(f"out must be [{n} x {d_o}]" + (f" {dtype}" if dtype is not None else ""))
     if out.device != device:
@@ -493,7 +498,7 @@ def qz_mx4_linear(X, codes, scales, bias=None, out_dtype=None, out=None, ws=None
     (n, d_i), d_o, dev, x = X.shape, codes.shape[0], X.device, X.data_ptr()
     index = dev.index
     _mx4_pair(codes, scales, d_o, d_i, "W", index)
-    out, ldy, yt = _product_out(out, n, d_o, out_dtype, dev)
+    out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
     wp, wn, ws = _scratch(ws, L.qz_mx4_linear_workspace(x, n, ldx, d_o, d_i), dev)
     _run(index, L.qz_mx4_linear, x, _lib.QZ_BF16, n, ldx, codes.data_ptr(), scales.data_ptr(), d_o,
          d_i, _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy, wp, wn)
@@ -512,7 +517,7 @@ def qz_mx4_matmul(xcodes, xscales, codes, scales, d_i, bias=None, out_dtype=None
     index = dev.index
     _mx4_pair(xcodes, xscales, n, d_i, "X", index)
     _mx4_pair(codes, scales, d_o, d_i, "W", index)
-    out, ldy, yt = _product_out(out, n, d_o, out_dtype, dev)
+    out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
     wp, wn, ws = _scratch(ws, L.qz_mx4_matmul_workspace(n, d_o, d_i), dev)
     _run(index, L.qz_mx4_matmul, xcodes.data_ptr(), xscales.data_ptr(), n, codes.data_ptr(),
          scales.data_ptr(), d_o, d_i, _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy,

@@ -43,14 +43,16 @@ bool direct_x(const void* X, int64_t d_i, int64_t ldx) {
 struct ProductWs {
   uint16_t* xpad;
   float* partial;
+  Mx4Choice choice;
   size_t bytes;
 };
 ProductWs product_ws(void* base, bool x4, bool pad, int64_t n, int64_t d_o, int64_t d_i) {
   Carver c(base);
   ProductWs w;
   w.xpad = c.take<uint16_t>(pad ? static_cast<size_t>(n) * mx_blocks(d_i) * kMxBlock : 0);
-  const int64_t splits = n > 0 && d_o > 0 ? mx4_product_splits(x4, n, d_o, mx_blocks(d_i)) : 1;
-  w.partial = c.take<float>(splits > 1 ? static_cast<size_t>(splits) * n * d_o : 0);
+  w.choice = mx4_choose(x4, n, d_o, mx_blocks(d_i));
+  const size_t splits = w.choice.splits;
+  w.partial = c.take<float>(splits > 1 ? splits * n * d_o : 0);
   w.bytes = c.used;
   if (splits <= 1) w.partial = nullptr;
   return w;
@@ -186,6 +188,7 @@ int qz_mx4_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const uint8
   p.G = mx_blocks(d_i);
   p.X = static_cast<const uint16_t*>(X);
   p.ldx = ldx;
+  p.choice = w.choice;
   p.partial = w.partial;
   if (pad) {
     p.ldx = p.G * kMxBlock;
@@ -223,6 +226,7 @@ int qz_mx4_matmul(const uint8_t* xcodes, const uint8_t* xscales, int64_t n, cons
   p.G = mx_blocks(d_i);
   p.xcodes = xcodes;
   p.xscales = xscales;
+  p.choice = w.choice;
   p.partial = w.partial;
   p.codes = codes;
   p.scales = scales;

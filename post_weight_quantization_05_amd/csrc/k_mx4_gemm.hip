@@ -671,10 +671,7 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
 // 7.7, tile 11.7; 256 tokens there, 11.1, 10.0, 11.9; 256 tokens 4096 -> 12288, 28.2, 27.7, 17.0.
 namespace {
 
-struct Choice {
-  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
-  int splits;
-};
+using Choice = Mx4Choice;
 struct TileTime {
   int bm, bn, resident;
   double alone, share;
@@ -693,9 +690,10 @@ constexpr FewTime kFew[2][7] = {   // shapes without a time: slower everywhere f
 
 // `groups` workgroups of a compute unit, `resident` at once: one takes `alone`, r together at
 // least r times `share`.
-double rounds_time(double groups, int resident, double alone, double share) {
-  const double full = std::floor(groups / resident), rest = groups - full * resident;
-  return full * std::fmax(alone, resident * share) + (rest > 0 ? std::fmax(alone, rest * share) : 0.);
+double rounds_time(int64_t groups, int resident, double alone, double share) {
+  const int64_t full = groups / resident, rest = groups % resident;
+  const auto together = [&](int64_t r) { return alone > r * share ? alone : r * share; };
+  return full * together(resident) + (rest ? together(rest) : 0.);
 }
 constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 of MX4
     {{256, 256, 1, 1.746, 1.746}, {256, 128, 1, 1.021, 1.021}, {128, 128, 2, 1.027, 0.513},
@@ -703,35 +701,39 @@ constexpr TileTime kTiles[2][6] = {   // of a stage: 64 columns of bf16 X, 256 o
     {{256, 256, 1, 2.072, 2.072}, {256, 128, 1, 1.419, 1.419}, {128, 128, 2, 1.272, 0.72},
      {128, 64, 2, 0.760, 0.495}, {64, 64, 2, 0.527, 0.264}, {128, 32, 2, 0.616, 0.308}}};
 
-Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
+Choice choose(bool x4, int n, int d_o, int G) {
   Choice best{Choice::kFew11, 1};
   double best_t = 1e30;
-  const auto consider = [&](Choice::Kind kind, int splits, double t) {
+  const auto consider = [&](int kind, int splits, double t) {
     if (t < best_t) {
       best_t = t;
-      best = {kind, splits};
+      best = {static_cast<Choice::Kind>(kind), splits};
     }
   };
+  const auto parts = [](int a, int b) { return (a + b - 1) / b; };
   for (int i = 0; i < 7; ++i) {
     const FewTime& c = kFew[x4][i];
     if (!c.resident) continue;
-    const double groups = static_cast<double>(ceil_div(d_o, 16 * c.rt)) * ceil_div(n, 16 * c.nt);
-    const double units = static_cast<double>(ceil_div(ceil_div(G, 8), c.waves));
-    consider(static_cast<Choice::Kind>(Choice::kFew11x8 + i), 1,
-             c.fixed + units * rounds_time(std::ceil(groups / 256), c.resident, c.alone, c.share));
+    const int64_t groups = static_cast<int64_t>(parts(d_o, 16 * c.rt)) * parts(n, 16 * c.nt);
+    const int units = parts(parts(G, 8), c.waves);
+    consider(Choice::kFew11x8 + i, 1,
+             c.fixed + units * rounds_time((groups + 255) / 256, c.resident, c.alone, c.share));
   }
   if (n <= 16) return best;   // a large tile would be mostly empty
   const int blocks = x4 ? 8 : 2, even = x4 ? 1 : 2;
-  const int64_t all = ceil_div(G, blocks);
+  const int all = parts(G, blocks);
+  const double outputs = static_cast<double>(n) * d_o;
   for (int i = 0; i < 6; ++i) {
     const TileTime& c = kTiles[x4][i];
-    const double tiles = static_cast<double>(ceil_div(d_o, c.bm)) * ceil_div(n, c.bn);
+    const int64_t tiles = static_cast<int64_t>(parts(d_o, c.bm)) * parts(n, c.bn);
     for (const int want : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      const int64_t per = round_up(ceil_div(all, want), even), splits = ceil_div(all, per);
-      if (splits != want || (want > 1 && (per < 2 || want * n * d_o > (int64_t{1} << 26)))) continue;
-      double t = 4.0 + per * rounds_time(std::ceil(tiles * splits / 256), c.resident, c.alone, c.share);
-      if (splits > 1) t += 4.0 + 1.3e-6 * splits * n * d_o;   // written and read, fp32
-      consider(static_cast<Choice::Kind>(Choice::k256x256 + i), static_cast<int>(splits), t);
+      const double join = want > 1 ? 4.0 + 1.3e-6 * want * outputs : 0.;   // written and read, fp32
+      if (4.0 + join >= best_t || (want > 1 && want * outputs > 67108864.)) break;
+      const int per = parts(parts(all, want), even) * even, splits = parts(all, per);
+      if (splits != want || (want > 1 && per < 2)) continue;
+      const int64_t groups = (tiles * splits + 255) / 256;
+      consider(Choice::k256x256 + i, splits,
+               4.0 + join + per * rounds_time(groups, c.resident, c.alone, c.share));
     }
   }
   return best;
@@ -739,7 +741,7 @@ Choice choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
 
 template <bool X4>
 int launch_product(const Mx4Product& p, hipStream_t s) {
-  const Choice c = choose(X4, p.n, p.d_o, p.G);
+  const Choice c = p.choice;
   switch (c.kind) {
     case Choice::kFew11x8: return launch_skinny<X4, 1, 1>(p, 8, s);
     case Choice::kFew11: return launch_skinny<X4, 1, 1>(p, 4, s);
@@ -768,8 +770,8 @@ int launch_product(const Mx4Product& p, hipStream_t s) {
 
 }  // namespace
 
-int mx4_product_splits(bool x4, int64_t n, int64_t d_o, int64_t G) {
-  return choose(x4, n, d_o, G).splits;
+Mx4Choice mx4_choose(bool x4, int64_t n, int64_t d_o, int64_t G) {
+  return choose(x4, static_cast<int>(n), static_cast<int>(d_o), static_cast<int>(G));
 }
 
 int launch_mx4_product(const Mx4Product& p, hipStream_t s) {

@@ -268,6 +268,13 @@ int launch_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows,
 // out [n x ldo] = X [n x d_i] (bf16), zero in columns d_i .. ldo
 int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint16_t* out,
                    int64_t ldo, hipStream_t s);
+// A product's kernel, from its sizes; splits: parts of the contraction whose sums go through
+// Mx4Product::partial (1: none, partial unused).
+struct Mx4Choice {
+  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
+  int splits;
+};
+Mx4Choice mx4_choose(bool x4, int64_t n, int64_t d_o, int64_t G);
 struct Mx4Product {   // Y = X W^T + bias
   int64_t n, d_o, G;                            // G: blocks of a row
   const uint16_t* X; int64_t ldx;               // bf16 [n x 32 G], rows 16-byte aligned, or null:
@@ -277,10 +284,9 @@ struct Mx4Product {   // Y = X W^T + bias
   void* Y; int yt; int64_t ldy;
   int y_vec;                                    // four consecutive outputs are 4-element aligned
   int factors_aligned;                          // both arrays of factors start on 4-byte boundaries
+  Mx4Choice choice;
   float* partial;                               // split sums [splits][n][d_o], or null
 };
-// parts of the contraction whose sums go through p.partial (1: none, partial unused)
-int mx4_product_splits(bool x4, int64_t n, int64_t d_o, int64_t G);
 int launch_mx4_product(const Mx4Product& p, hipStream_t s);
 struct MoeArgs {
   int64_t n, d, f, Gd, Gf;                      // Gd, Gf: blocks of rows of d and f columns
