@@ -201,7 +201,7 @@ struct TileShape {
   // the results of 32 tokens of a wavefront, on their way to whole lines of Y
   static constexpr int kOutPitch = 32 * MT * 4 + 16;
   static constexpr int kOut = kWaves * 32 * kOutPitch;
-  static constexpr int kShared = kLds > kOut ? kLds : kOut;
+  static constexpr int kShared = kLds > kOut + 4 * BM ? kLds : kOut + 4 * BM;   // the bias behind them
   static_assert(kShared <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -541,7 +541,14 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_tile_kernel(const Mx4Prod
   const bool lines = ld * osize % 16 == 0 && reinterpret_cast<uintptr_t>(ybase) % 16 == 0;
   lds_u8* const out = (lds_u8*)smem + wave * 32 * T::kOutPitch;
   const int64_t wr0 = r0 + wm * 32 * MT;
+  const bool biased = p.bias && !p.partial;
+  lds_u8* const bias = (lds_u8*)smem + T::kOut;
   __syncthreads();
+  if (biased) {   // once into LDS: a load for every four results cost a fifth of the kernel's time
+    for (int i = tid; i < T::BM; i += T::kThreads)
+      *(__attribute__((address_space(3))) float*)(bias + 4 * i) = r0 + i < p.d_o ? p.bias[r0 + i] : 0.f;
+    __syncthreads();
+  }
 #pragma unroll
   for (int b = 0; b < NT; ++b) {
 #pragma unroll
@@ -550,11 +557,7 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_tile_kernel(const Mx4Prod
       for (int r4 = 0; r4 < 4; ++r4) {
         const int rr = a * 32 + 8 * r4 + 4 * half;
         f32x4 v = {acc[a][b][4 * r4], acc[a][b][4 * r4 + 1], acc[a][b][4 * r4 + 2], acc[a][b][4 * r4 + 3]};
-        if (p.bias && !p.partial) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (wr0 + rr + i < p.d_o) v[i] += p.bias[wr0 + rr + i];
-        }
+        if (biased) v += *(__attribute__((address_space(3))) f32x4*)(bias + 4 * (wm * 32 * MT + rr));
         if (osize == 4) {
           *(__attribute__((address_space(3))) f32x4*)(out + row * T::kOutPitch + 4 * rr) = v;
         } else {
