@@ -126,10 +126,10 @@ int launch_skinny(const Mx4Product& p, int waves, hipStream_t s) {
 // once per 128 bytes cost half of the LDS cycles in conflicts).  The copies keep LDS linear and
 // permute their global sources instead.
 //
-// Measured: 8192 tokens 5120 -> 25600 bf16 1.87 ms, 1.15 PFLOP/s (a large library product reaches
+// Measured: 8192 tokens 5120 -> 25600 bf16 1.86 ms, 1.15 PFLOP/s (a large library product reaches
 // 1.41 on this card, at its power limit like this one; of the kernel's parts alone the products
 // take 1.38 to 1.57 ms, the copies 0.74); 2048 tokens 4096 -> 4096 68 us (1.01 PFLOP/s); MX4 X, 4096
-// tokens 4096 -> 12288 119 to 127 us warm (3.2 to 3.5 PFLOP/s): products alone 85% of that, copies
+// tokens 4096 -> 12288 119 to 130 us warm (3.2 to 3.5 PFLOP/s): products alone 85% of that, copies
 // 67%, the epilogue 12%.
 template <bool X4>
 struct TileGeom;
