@@ -13,8 +13,8 @@
 // once to bf16 would be as large an error as the final rounding of y.
 //
 // Measured, us (launch 2 and 3; all four): one token, 8 of 128 experts, 4096 x 1024, 54 MB: 14.6,
-// 7.4; 29; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 56, 37; 101; 7 tokens, 2 of 8, 4096 x 12288,
-// seven reached, 561 MB: 87, 46; 132 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
+// 7.4; 28; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 57, 32; 97; 7 tokens, 2 of 8, 4096 x 12288,
+// seven reached, 561 MB: 82, 46; 123 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
 // and 4 are 4.7 and 4.5, of which a launch alone is 3.3.
 #include "mx4_few.h"
 
@@ -308,13 +308,14 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_down_kernel(const MoeArgs 
     part(wave, 0) = acc[0][0];
     part(wave, 1) = acc[1][0];
     __syncthreads();
-    if (wave < 2 && have && m < 8) {
-      f32x4 v = part(0, wave) + part(0, wave, 8);
-      for (int w = 1; w < waves; ++w) v += part(w, wave) + part(w, wave, 8);
-      const int64_t r = r0 + 16 * wave + 4 * q;
-      if (r < a.ldy)   // rows of the scratch are whole fours
-        *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;
-    }
+    if (have && m < 8)
+      for (int i = wave; i < 2; i += waves) {
+        f32x4 v = part(0, i) + part(0, i, 8);
+        for (int w = 1; w < waves; ++w) v += part(w, i) + part(w, i, 8);
+        const int64_t r = r0 + 16 * i + 4 * q;
+        if (r < a.ldy)   // rows of the scratch are whole fours
+          *reinterpret_cast<f32x4*>(a.y_pairs + pair * a.ldy + r) = v;
+      }
   }
 }
 
@@ -373,25 +374,27 @@ int launch_moe(const MoeArgs& a, int router_type, hipStream_t s) {
   QZ_TRY(check_launch("moe_logits"));
   const unsigned slots = static_cast<unsigned>(moe_slots(a.n, a.E, a.k));
   // As many workgroups as are resident at once (four wavefronts a SIMD): finding its expert's
-  // tokens takes a workgroup 1 to 2 us, so each then goes on through the rows of its slot.  A
-  // wavefront per 256 columns, up to eight, where there are few chunks of rows; else one per 1024,
-  // up to four (us: 48 tokens, 64 experts, 2048 columns: 2 58.9, 4 58.5, 1 82.2; 1408 columns: 2
-  // 35, 4 37.4; 7 tokens, 8 experts, 12288 columns: 2 48.8, 4 47.2, 1 66.2).
-  const auto shape = [&](int64_t chunks, int64_t G, int per_cu, dim3* grid, dim3* block) {
-    const int64_t units = ceil_div(G, 8);
-    const bool few = chunks * slots <= 512;
-    const int64_t want = few ? units : ceil_div(units, 4), most = few ? 8 : 4;
-    const int64_t even = ceil_div(units, ceil_div(units, want < most ? want : most));   // shares alike
-    const int64_t waves = even < 2 ? 2 : even;
-    const int64_t width = ceil_div(256 * 4 * per_cu / waves, slots);
+  // tokens takes a workgroup 1 to 2 us, so each then goes on through the rows of its slot.  As many
+  // wavefronts share a chunk of rows as it takes to fill the chip, with two units or more each (one
+  // where even eight do not fill it), and for finding the tokens at least two.  us, with (1, 2, 4)
+  // wavefronts: 48 tokens, 6 of 64 experts, 2048 x 1408, gate and up 78, 57, 58, down 32, 35, 37; 7
+  // tokens, 2 of 8, 4096 x 12288, 104, 87, 89, and 66, 49, 47.
+  const auto shape = [&](int64_t chunks, int64_t G, int64_t least, dim3* grid, dim3* block) {
+    const int64_t units = ceil_div(G, 8), items = chunks * slots;
+    const int64_t most = items <= 512 ? units : units / 2, fill = ceil_div(256 * 16, items);
+    int64_t waves = fill < kWaves ? fill : kWaves;
+    if (waves > most) waves = most;
+    if (waves < least) waves = least;
+    if (waves < units) waves = ceil_div(units, ceil_div(units, waves));   // shares alike
+    const int64_t width = ceil_div(256 * 16 / waves, slots);
     *grid = dim3(static_cast<unsigned>(chunks < width ? chunks : width), slots);
     *block = dim3(static_cast<unsigned>(64 * waves));
   };
   dim3 grid, block;
-  shape(2 * a.Gf, a.Gd, 4, &grid, &block);
+  shape(2 * a.Gf, a.Gd, 2, &grid, &block);
   hipLaunchKernelGGL(moe_up_kernel, grid, block, block.x / 64 * kWaveLds, s, a, static_cast<int>(static_cast<int>(slots) < a.E));
   QZ_TRY(check_launch("moe_up"));
-  shape(ceil_div(a.d, 32), a.Gf, 6, &grid, &block);
+  shape(ceil_div(a.d, 32), a.Gf, 1, &grid, &block);
   hipLaunchKernelGGL(moe_down_kernel, grid, block, block.x / 64 * kWaveLds, s, a);
   QZ_TRY(check_launch("moe_down"));
   hipLaunchKernelGGL(moe_sum_kernel,
