@@ -107,7 +107,8 @@ constexpr int kFewLds = !SHARED ? 2048 * RT : X4 ? 2048 * (RT > NT ? RT : NT) : 
 template <bool AHEAD, bool SHARED, bool X4, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
                                              int unit, int end, f32x4 (&acc)[RT][NT]) {
-  constexpr int kX = X4 ? 1 : 4;
+  static_assert(SHARED || !X4, "tokens in MX4 pass through LDS");
+  constexpr int kX = X4 ? 1 : 4;   // 16-byte pieces of a lane for half a unit, or 128-byte pieces of a token's unit
   if (unit >= end) return;
   const int lane = threadIdx.x & 63, q = lane >> 4;
   uint4 fw[RT], fx[NT];
@@ -147,12 +148,12 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < kX; ++j) {
-          const int want = u0 * 8 + 4 * u + (X4 ? q : j);   // the lane's block
+        for (int j = 0; j < 4; ++j) {
+          const int want = u0 * 8 + 4 * u + j;   // block
           const int blk = want < G ? want : G - 1;
 #pragma unroll
           for (int b = 0; b < NT; ++b)
-            x[b][u][j] = *reinterpret_cast<const uint4*>(p.x[b][0] + (X4 ? 16 * blk : 64 * blk + 16 * q));
+            x[b][u][j] = *reinterpret_cast<const uint4*>(p.x[b][0] + 64 * blk + 16 * q);
         }
       return;
     }
@@ -186,7 +187,7 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
         for (int b = 0; b < NT; ++b)
 #pragma unroll
           for (int j = 0; j < kX; ++j)
-            if (SHARED ? 8 * (kX * u0 + j) + c8 >= kX * G : u0 * 8 + 4 * h + (X4 ? q : j) >= G) x[b][h][j] = zero;
+            if (SHARED ? 8 * (kX * u0 + j) + c8 >= kX * G : u0 * 8 + 4 * h + j >= G) x[b][h][j] = zero;
       }
     }
 #pragma unroll
@@ -198,7 +199,7 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int a = 0; a < RT; ++a) c[u][a] = get(2048 * a + at(m, 4 * u + q));
-    if constexpr (X4 && SHARED) {
+    if constexpr (X4) {
 #pragma unroll
       for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -214,7 +215,7 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
 #pragma unroll
         for (int b = 0; b < NT; ++b) {
           const uint32_t f = four(fx[b], step, m + 16 * (step >> 2)) >> (8 * q);
-          const uint4 t = SHARED ? get(2048 * b + at(m, 4 * u + q)) : x[b][u][0];
+          const uint4 t = get(2048 * b + at(m, 4 * u + q));
 #pragma unroll
           for (int a = 0; a < RT; ++a)
             acc[a][b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
@@ -227,7 +228,7 @@ __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8
         for (int b = 0; b < NT; ++b) {
           if constexpr (!SHARED) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) t[b][j] = x[b][u][j % kX];
+            for (int j = 0; j < 4; ++j) t[b][j] = x[b][u][j];
             continue;
           }
 #pragma unroll

@@ -452,7 +452,7 @@ MOE_CROWDED = [  # experts that get many tokens: several tiles of pairs, the las
     (33, 544, 300, 5, 4, True, "bf16"), (256, 33, 65, 256, 2, False, "bf16"), (16, 64, 96, 256, 15, True, "f32"),
     (15, 64, 96, 256, 16, True, "bf16"), (2, 2080, 1100, 12, 6, True, "bf16"), (48, 160, 520, 17, 16, False, "bf16"),
     (200, 2080, 40, 3, 3, True, "bf16"), (16, 2050, 40, 140, 3, False, "bf16"), (40, 2112, 33, 130, 5, True, "f32"),
-    (256, 2056, 16, 256, 16, False, "f32")]
+    (256, 2056, 16, 256, 16, False, "f32"), (20, 4100, 300, 33, 4, True, "bf16")]
 
 
 @pytest.mark.parametrize("case", MOE_CROWDED)
