@@ -716,7 +716,7 @@ Choice choose(bool x4, int n, int d_o, int G) {
   const auto parts = [](int a, int b) { return (a + b - 1) / b; };
   for (int i = 0; i < 7; ++i) {
     const FewTime& c = kFew[x4][i];
-    if (!c.resident) continue;
+    if (!c.resident || parts(n, 16 * c.nt) > 65535) continue;   // a launch's limit
     const int64_t groups = static_cast<int64_t>(parts(d_o, 16 * c.rt)) * parts(n, 16 * c.nt);
     const int units = parts(parts(G, 8), c.waves);
     consider(Choice::kFew11x8 + i, 1,

@@ -364,6 +364,23 @@ def test_quantize_past_32_bits():
         np.testing.assert_array_equal(_host(v[pick].double()), mx4.values(c_ref, s_ref, cols))
 
 
+def test_most_tokens():
+    """2^20 tokens, the most that a call takes, through few and through ordinary rows of W."""
+    q, torch = qz(), _t()
+    g = torch.Generator("cuda").manual_seed(6)
+    for d_i, d_o in ((2000, 5), (1024, 16), (320, 100)):
+        codes, scales = _random_codes(np.random.default_rng(d_i), d_o, d_i)
+        w = mx4.values(codes, scales, d_i)
+        x = torch.randint(-3, 4, (1 << 20, d_i), device="cuda", generator=g).to(torch.bfloat16)
+        pick = torch.tensor([0, 1, 65535, 524288, (1 << 20) - 17, (1 << 20) - 2, (1 << 20) - 1], device="cuda")
+        want = _host(x[pick].double()) @ w.T
+        y = q.qz_mx4_linear(x, to_dev(codes), to_dev(scales), out_dtype=torch.float32)
+        np.testing.assert_array_equal(_host(y[pick]), want)
+        xc, xs = q.qz_mx4_quantize(x)
+        y = q.qz_mx4_matmul(xc, xs, to_dev(codes), to_dev(scales), d_i, out_dtype=torch.float32)
+        np.testing.assert_array_equal(_host(y[pick]), want)
+
+
 def test_quantize_past_2_32_pieces():
     """More than 2^32 pieces of eight columns: the index is 64 bits wide."""
     q, torch = qz(), _t()
