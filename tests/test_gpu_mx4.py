@@ -381,6 +381,28 @@ def test_most_tokens():
         np.testing.assert_array_equal(_host(y[pick]), want)
 
 
+@pytest.mark.parametrize("n,d_i,d_o", [(1, 32, 1 << 24), (33, 20, 1 << 24), (1, 1 << 20, 40), (17, 1 << 20, 9),
+                                       (100, (1 << 20) - 3, 70), (300, 1 << 20, 33)])
+def test_most_rows_and_columns(n, d_i, d_o):
+    """The largest d_o and d_i.  Inputs -1 .. 1, factors 1/2 .. 2: sums of magnitudes below 2^24
+    quarters for 2^20 columns only on average, so bounds there and equality for the short rows."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng([n, d_i])
+    codes, scales = _random_codes(rng, d_o, d_i)
+    pick = np.unique(np.r_[:8, d_o // 2, d_o - 8:d_o])
+    w = mx4.values(codes[pick], scales[pick], d_i)
+    x, xd = _bf16(rng.integers(-1, 2, (n, d_i)))
+    want, total = x @ w.T, np.abs(x) @ np.abs(w).T
+    xc, xs = q.qz_mx4_quantize(xd)
+    for y in (q.qz_mx4_linear(xd, to_dev(codes), to_dev(scales), out_dtype=torch.float32),
+              q.qz_mx4_matmul(xc, xs, to_dev(codes), to_dev(scales), d_i, out_dtype=torch.float32)):
+        got = _host(y[:, torch.from_numpy(pick).cuda()])
+        if d_i <= 32:
+            np.testing.assert_array_equal(got, want)
+        else:
+            assert (np.abs(got - want) <= _sum_bound(d_i, total, "f32", want)).all()
+
+
 def test_quantize_past_2_32_pieces():
     """More than 2^32 pieces of eight columns: the index is 64 bits wide."""
     q, torch = qz(), _t()
@@ -474,6 +496,11 @@ MOE_CROWDED = [  # experts that get many tokens: several tiles of pairs, the las
 
 @pytest.mark.parametrize("case", MOE_CROWDED)
 def test_moe_crowded(case):
+    test_moe(case)
+
+
+@pytest.mark.parametrize("case", [(2, 64, 1 << 20, 1, 1, True, "bf16"), (3, 1 << 20, 32, 1, 1, False, "f32")])
+def test_moe_longest_rows(case):
     test_moe(case)
 
 
