@@ -84,7 +84,8 @@ __global__ __launch_bounds__((kSkinnyWaves<RT, NT>) * 64) void mx4_skinny_kernel
 #pragma unroll
     for (int b = 0; b < NT; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int units = (G + 7) / 8, mine = (units + waves - 1) / waves;
-  few_products<X4 || RT * NT == 1, true>(rows, lds[wave], G, wave * mine, wave * mine + mine < units ? wave * mine + mine : units, acc);
+  const int u0 = wave * mine, u1 = u0 + mine < units ? u0 + mine : units;
+  few_products<X4 || RT * NT == 1, true>(rows, lds[wave], G, u0, u1, acc);
 
 #pragma unroll
   for (int a = 0; a < RT; ++a)

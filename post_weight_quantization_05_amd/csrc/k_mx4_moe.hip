@@ -13,8 +13,8 @@
 // once to bf16 would be as large an error as the final rounding of y.
 //
 // Measured, us (launch 2 and 3; all four): one token, 8 of 128 experts, 4096 x 1024, 54 MB: 14.6,
-// 7.4; 28; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 57, 32; 97; 7 tokens, 2 of 8, 4096 x 12288,
-// seven reached, 561 MB: 82, 46; 123 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
+// 7.4; 28; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 55, 32; 95; 7 tokens, 2 of 8, 4096 x 12288,
+// seven reached, 561 MB: 82, 46; 123 to 128 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
 // and 4 are 4.7 and 4.5, of which a launch alone is 3.3.
 #include "mx4_few.h"
 
@@ -135,9 +135,10 @@ __device__ __forceinline__ void wave_top_k(const double* lg, int E, int k, F fou
   }
 }
 
-// Workgroups (x, slot): 16 hidden columns at a time, chunks x, x + the grid's width, ...  A slot is an expert, or, where the tokens cannot
-// reach all experts (`compact`), the slot-th one that they reach.  The first one of a slot writes
-// its expert and pairs (t k + r) down for the launches after it.
+// Workgroups (x, slot): 16 hidden columns at a time, chunks x, x + the grid's width, ...  A slot is
+// an expert, or, where the tokens cannot reach all experts (`compact`), the slot-th one that they
+// reach.  The first one of a slot writes its expert and pairs (t k + r) down for the launches after
+// it.
 __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a, int compact) {
   extern __shared__ __align__(16) uint8_t smem[];   // of a wavefront: kWaveLds
   __shared__ int list[QZ_MOE_MAX_TOKENS];   // pairs of this expert
@@ -180,11 +181,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
       for (int i = threadIdx.x; i < a.n * a.k; i += blockDim.x)
         if (chosen[i] == e) list[atomicAdd(&count, 1)] = i;
   } else {
-    // four tokens at a time: their logits are one trip to L2
-    for (int t0 = 4 * wave; t0 < a.n; t0 += 4 * waves) {
-      double mine[4], lg[4][kPerLane];
+    // eight tokens at a time: their logits are one trip to L2
+    constexpr int kTogether = 8;
+    for (int t0 = kTogether * wave; t0 < a.n; t0 += kTogether * waves) {
+      double mine[kTogether], lg[kTogether][kPerLane];
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < kTogether; ++s) {
         const double* row = a.logits + (t0 + s < a.n ? t0 + s : t0) * a.E;
         mine[s] = row[e];
 #pragma unroll
@@ -192,7 +194,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void moe_up_kernel(const MoeArgs a,
           if (64 * i < a.E) lg[s][i] = row[lane + 64 * i < a.E ? lane + 64 * i : 0];
       }
 #pragma unroll
-      for (int s = 0; s < 4; ++s) {
+      for (int s = 0; s < kTogether; ++s) {
         if (t0 + s >= a.n) break;
         int ahead = 0;
 #pragma unroll

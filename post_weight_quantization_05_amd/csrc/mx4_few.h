@@ -90,9 +90,9 @@ constexpr int kFewLds = !SHARED ? 2048 * RT : X4 ? 2048 * (RT > NT ? RT : NT) : 
 //
 // lds: kFewLds bytes of the wavefront's own.  A load that the lanes of an operand made for
 // themselves would have 16 rows in each run of 16 lanes, and the memory pipeline takes four lanes
-// at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, of W and (SHARED) of X, and
-// the lanes of the operand read their parts back from LDS: codes first, then the tokens, half a
-// unit at a time, through the same bytes (a wavefront's LDS instructions stay in order).
+// at a time: 64 accesses of 16 bytes.  So eight lanes load 128 bytes of a row, of W and (SHARED) of
+// X, and the lanes of the operand read their parts back from LDS: codes first, then the tokens, half
+// a unit at a time, through the same bytes (a wavefront's LDS instructions stay in order).
 // 13 tokens, 12288 -> 4096, before the codes were loaded ahead: 10.2 us with X SHARED, 12.3 without;
 // in the expert layer, where a tile has a token or two and the other lanes repeat them, 143 and 129
 // us (7 tokens, 2 of 8 x 12288).
@@ -108,7 +108,7 @@ template <bool AHEAD, bool SHARED, bool X4, int RT, int NT>
 __device__ __forceinline__ void few_products(const FewRows<X4, RT, NT>& p, uint8_t* lds, int G,
                                              int unit, int end, f32x4 (&acc)[RT][NT]) {
   static_assert(SHARED || !X4, "tokens in MX4 pass through LDS");
-  constexpr int kX = X4 ? 1 : 4;   // 16-byte pieces of a lane for half a unit, or 128-byte pieces of a token's unit
+  constexpr int kX = X4 ? 1 : 4;   // 128-byte pieces of a token's unit
   if (unit >= end) return;
   const int lane = threadIdx.x & 63, q = lane >> 4;
   uint4 fw[RT], fx[NT];

@@ -271,7 +271,10 @@ int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint1
 // A product's kernel, from its sizes; splits: parts of the contraction whose sums go through
 // Mx4Product::partial (1: none, partial unused).
 struct Mx4Choice {
-  enum Kind { kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42, k256x256, k256x128, k128x128, k128x64, k64x64, k128x32 } kind;
+  enum Kind {
+    kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42,
+    k256x256, k256x128, k128x128, k128x64, k64x64, k128x32
+  } kind;
   int splits;
 };
 Mx4Choice mx4_choose(bool x4, int64_t n, int64_t d_o, int64_t G);
