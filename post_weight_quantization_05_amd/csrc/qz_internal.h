@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <string>
 
+#include "mx4_plan.h"
 #include "qz.h"
 
 namespace qz {
@@ -268,15 +269,6 @@ int launch_mx4_unpack(const uint8_t* codes, const uint8_t* scales, int64_t rows,
 // out [n x ldo] = X [n x d_i] (bf16), zero in columns d_i .. ldo
 int launch_mx4_pad(const uint16_t* X, int64_t n, int64_t d_i, int64_t ldx, uint16_t* out,
                    int64_t ldo, hipStream_t s);
-// A product's kernel, from its sizes; splits: parts of the contraction whose sums go through
-// Mx4Product::partial (1: none, partial unused).
-struct Mx4Choice {
-  enum Kind {
-    kFew11x8, kFew11, kFew12, kFew21, kFew22, kFew24, kFew42,
-    k256x256, k256x128, k128x128, k128x64, k64x64, k128x32
-  } kind;
-  int splits;
-};
 Mx4Choice mx4_choose(bool x4, int64_t n, int64_t d_o, int64_t G);
 struct Mx4Product {   // Y = X W^T + bias
   int64_t n, d_o, G;                            // G: blocks of a row
