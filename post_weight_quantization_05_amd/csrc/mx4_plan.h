@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <initializer_list>
 
 namespace qz {
 
@@ -50,13 +51,15 @@ struct TileShape {
 // What a wavefront may leave in flight at the join of stage st, where stage st + 1 has to have
 // landed: with two buffers nothing.  With three, the batch issued last (stage st + 2) may be in
 // flight where it is whole, so that the wavefront has issued its full number of copies; but where
-// st + 1 begins a W buffer, that batch holds the second half of it, ahead of the copies of X.  (A
-// fetch of factors only makes the wait longer.)
+// st + 1 begins a W buffer, that batch holds the second half of it, ahead of the copies of X.
+// Copies land in the order of their issue: where st + 1 begins a fetch of factors, the fetch was
+// issued behind that batch and nothing may be left.
 enum class TileWait { kAll, kButX, kButStage };
 template <bool X4>
 constexpr TileWait tile_wait(int st, int nst, int whole) {
   using G = TileGeom<X4>;
   if (G::kRing == 2 || st + 2 >= nst || st + 2 + G::kWParts > whole) return TileWait::kAll;
+  if ((st + 1) % (kFetch / G::kBlocks) == 0) return TileWait::kAll;
   return st % G::kWParts == G::kWParts - 1 ? TileWait::kButX : TileWait::kButStage;
 }
 
