@@ -47,8 +47,8 @@ TRAFFIC = {
                           "4b3b79ff82303147030bf74c271647bb946e67de79935df19ec0b3d93bad1e6a"),
     "admm_project": (932.4e6, "k_admm.hip",
                     "e3f70300b61a47cdee85889e1ec3a8654dbc49310bc60d5cd8d2f4e4b4851f12"),
-    "hessian_gram_bf16": (14558.0e6, "k_hessian.hip",
-                         "2a1ccf1ce62306db32ddea42ac13c0a6dcc82e25da215221220577df49397698"),
+    "hessian_gram_bf16": (14014.4e6, "k_hessian.hip",
+                         "511f6d9566058597eca4972686f716e9ebe7d496106c221340a8b3e357a441b8"),
 }
 TRAFFIC_WORKLOAD = "up_4096x12288_w3g128"
 

@@ -225,7 +225,10 @@ __device__ __forceinline__ void dma_row(uint16_t* dst_row, const uint16_t* src, 
   const uint32_t s_hi =
       static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(sa >> 32)));
   const uint64_t su = (static_cast<uint64_t>(s_hi) << 32) | s_lo;
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+  // s_nop: the wait state that the copy needs after the write of m0, which the compiler does not
+  // count inside the statement.  The five after a vector write of its base are not needed, since the
+  // base is a scalar result (the kernel's work item is; a test reads both distances off the library).
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(lds_off), "v"(voff), "s"(reinterpret_cast<const uint16_t*>(su))
                : "memory", "m0");
@@ -258,7 +261,10 @@ __global__ __launch_bounds__(kThreads, 1) void gram_bf16_dma_kernel(const HArgs 
     const int64_t r = pid / kSlots, in = pid % kSlots;
     if ((r + 1) * kSlots <= nblk) pid = r * kSlots + (in & 7) * (kSlots / 8) + (in >> 3);
   }
-  const int64_t split = pid / g.n_tiles, t = pid % g.n_tiles;
+  // (the divisions leave the uniform item in vector registers, and with it every base of a copy: 4.13
+  // ms for 262144 x 4096 with the item made scalar, 4.46 with bases moved over and the wait for it)
+  const int64_t split = __builtin_amdgcn_readfirstlane(static_cast<int>(pid / g.n_tiles));
+  const int64_t t = __builtin_amdgcn_readfirstlane(static_cast<int>(pid % g.n_tiles));
   const int64_t I = g.tiles[2 * t], J = g.tiles[2 * t + 1];
   const bool diag = (I == J);
   const int64_t i0 = I * HT, j0 = J * HT;
