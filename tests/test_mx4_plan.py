@@ -132,3 +132,14 @@ def test_the_long_products_reach_every_tile(tmp_path):
         ("128x64", 1), ("128x64", 3), ("64x64", 1), ("128x32", 3)]
     assert all(per >= 70 for _, _, per in got)
     assert all(d_i % 128 == 0 for _, d_i, _ in LONG_LINEAR)
+
+
+def test_the_listed_products_reach_every_kernel(tmp_path):
+    """Every few-token shape, and every tile with one split and with several."""
+    from test_gpu_mx4 import EACH_LINEAR, EACH_MATMUL
+    tiles = {(t, split) for t in ("256x256", "256x128", "128x128", "128x64", "64x64", "128x32")
+             for split in (False, True)}
+    for sizes, x4, few in ((EACH_LINEAR, False, {"few 1x1 of 8", "few 1x1", "few 2x1", "few 2x2", "few 4x2"}),
+                           (EACH_MATMUL, True, {"few 1x1 of 8", "few 1x1", "few 1x2", "few 2x2", "few 2x4"})):
+        got = {(k, s > 1) for k, s, _ in _choices(tmp_path, sizes, x4)}
+        assert got == tiles | {(f, False) for f in few}, (x4, (tiles | {(f, False) for f in few}) ^ got)
