@@ -526,7 +526,10 @@ def qz_mx4_matmul(xcodes, xscales, codes, scales, d_i, bias=None, out_dtype=None
 
 
 def _moe_params(n_experts, top_k, renorm):
-    return QzMoe(C.sizeof(QzMoe), int(n_experts), int(top_k), _lib.QZ_MOE_RENORM if renorm else 0)
+    n_experts, top_k = int(n_experts), int(top_k)
+    if abs(n_experts) >> 31 or abs(top_k) >> 31:      # ctypes would cut them to 32 bits
+        raise ValueError("the number of experts and top_k must fit 32 bits")
+    return QzMoe(C.sizeof(QzMoe), n_experts, top_k, _lib.QZ_MOE_RENORM if renorm else 0)
 
 
 def qz_mx4_moe_workspace(n, d, f, n_experts, top_k) -> int:
