@@ -46,8 +46,8 @@ __device__ __forceinline__ void store4(const Mx4Product& p, int64_t t, int64_t r
 // Sums in fp32; the wavefronts' sums are added in their order.
 //
 // Bound by reading W, and below about 10 MB by the launch (3 us): 13 tokens 12288 -> 4096 bf16 8.9
-// us (26.7 MB; 4.3 at 6.2 TB/s), one token 4096 -> 1024 4.7, one token 5120 -> 25600 18.8 (69.6 MB,
-// 3.7 TB/s).  More rows a workgroup (RT) load the tokens less often, more tokens (NT) the rows.
+// us (26.7 MB; 4.3 at 6.2 TB/s), one token 4096 -> 1024 4.7, one token 5120 -> 25600 17.0 (2 x 1; 69.6
+// MB, 4.1 TB/s).  More rows a workgroup (RT) load the tokens less often, more tokens (NT) the rows.
 template <int RT, int NT>
 constexpr int kSkinnyWaves = RT * NT == 1 ? 8 : 4;
 
@@ -127,11 +127,12 @@ int launch_skinny(const Mx4Product& p, int waves, hipStream_t s) {
 // once per 128 bytes cost half of the LDS cycles in conflicts).  The copies keep LDS linear and
 // permute their global sources instead.
 //
-// Measured: 8192 tokens 5120 -> 25600 bf16 1.86 ms, 1.15 PFLOP/s (a large library product reaches
-// 1.41 on this card, at its power limit like this one; of the kernel's parts alone the products
-// take 1.38 to 1.57 ms, the copies 0.74); 2048 tokens 4096 -> 4096 68 us (1.01 PFLOP/s); MX4 X, 4096
-// tokens 4096 -> 12288 119 to 130 us warm (3.2 to 3.5 PFLOP/s): products alone 85% of that, copies
-// 67%, the epilogue 12%.
+// Measured: 8192 tokens 5120 -> 25600 bf16 1.85 to 1.89 ms, 1.14 to 1.16 PFLOP/s (the library's bf16
+// product of the same sizes, on widened weights, 1.63 ms; both draw the card's 1400 W; matrix cores
+// busy 51% at 2.13 GHz; of the kernel's parts alone the products take 1.38 to 1.57 ms, the copies
+// 0.74); 2048 tokens 4096 -> 4096 71 to 72 us (0.96 PFLOP/s; the library 55 to 58; busy 37%); MX4 X,
+// 4096 tokens 4096 -> 12288 123 to 133 us (3.1 to 3.35 PFLOP/s; busy 35% at 2.26 GHz, 1329 W):
+// products alone 85% of that, copies 67%, the epilogue 12%.
 template <int RB>
 __device__ __forceinline__ int swz(int row) {
   return (row / (256 / RB)) & (RB / 16 - 1);

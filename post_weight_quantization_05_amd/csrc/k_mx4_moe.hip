@@ -10,12 +10,14 @@
 // Weights are read once per 16 tokens of an expert, 16 rows by 16 tokens on the matrix cores
 // (mx4_few.h); what bounds the layer is reading them from HBM.  h is kept as two bf16 numbers
 // (value and remainder, 16 bits of mantissa together): the matrix cores take bf16, and rounding h
-// once to bf16 would be as large an error as the final rounding of y.
+// once to bf16 would be as large an error as the final rounding of y.  Before that rounding y is
+// 2.4e-6 from 64 bits (one token, 8 of 128; relative, 2-norm) and 0.9e-7 with h in fp32; after it
+// 0.00164561 either way.
 //
-// Measured, us (launch 2 and 3; all four): one token, 8 of 128 experts, 4096 x 1024, 54 MB: 14.6,
-// 7.4; 28; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 55, 32; 95; 7 tokens, 2 of 8, 4096 x 12288,
-// seven reached, 561 MB: 82, 46; 123 to 128 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
-// and 4 are 4.7 and 4.5, of which a launch alone is 3.3.
+// Measured, us (launch 2 and 3; all four): one token, 8 of 128 experts, 4096 x 1024, 54 MB: 14.3,
+// 7.4; 28 to 29; 48 tokens, 6 of 64, 2048 x 1408, 294 MB: 55, 34; 96; 7 tokens, 2 of 8, 4096 x 12288,
+// seven reached, 561 MB: 78, 44; 127 (92 at the 6.1 TB/s of a kernel that only reads).  Launches 1
+// and 4 are 4.7 each, of which a launch alone is 3.3.
 #include "mx4_few.h"
 
 namespace qz {

@@ -45,3 +45,28 @@ def test_factors_of_many_runs(n, d_i, d_o):
     xc, xs = q.qz_mx4_quantize(xd)
     got = q.qz_mx4_matmul(xc, xs, codes, scales, d_i, out_dtype=torch.float32)
     assert torch.equal(got.double(), want)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", [(262, 13184, 3687), (388, 5248, 4383)])
+def test_long_products_in_a_graph(n, d_i, d_o):
+    """Split sums and a single launch, replayed between eager calls on other data."""
+    import torch
+    q = qz()
+    gen = torch.Generator("cuda").manual_seed(d_i)
+    codes, scales, _ = _stored(d_o, d_i, gen)
+    static = torch.zeros((n, d_i), dtype=torch.bfloat16, device="cuda")
+
+    def chain(x):
+        xc, xs = q.qz_mx4_quantize(x)
+        return q.qz_mx4_linear(x, codes, scales), q.qz_mx4_matmul(xc, xs, codes, scales, d_i)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = chain(static)
+    for _ in range(4):
+        x = torch.randn((n, d_i), device="cuda", generator=gen).to(torch.bfloat16)
+        want = chain(x)
+        static.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))

@@ -69,7 +69,7 @@ def test_copies_into_lds_keep_their_distance(tmp_path):
     here = tmp_path / "libqz.so"
     here.symlink_to(_lib.LIB_PATH)
     subprocess.run([OBJDUMP, "--offloading", str(here)], cwd=tmp_path, capture_output=True, check=True, timeout=100)
-    found, copies = [], 0
+    found, copies, writes = [], 0, 0
     for code in sorted(glob.glob(str(tmp_path / "*gfx950"))):
         text = subprocess.run([OBJDUMP, "-d", "--no-show-raw-insn", "--no-leading-addr", code], capture_output=True,
                               text=True, check=True, timeout=100).stdout
@@ -77,5 +77,7 @@ def test_copies_into_lds_keep_their_distance(tmp_path):
             f, c = _short(text.splitlines())
             found += f
             copies += c
+            writes += len(re.findall(r"^\s*\w+ m0,", text, re.M))
     assert copies > 100     # the tile products' and the Hessian's
     assert not found, f"{len(found)} of {copies}: {found[:4]}"
+    assert writes == copies     # the compiler keeps nothing of its own in m0 there
