@@ -446,6 +446,113 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
                void* Y, int32_t* ids, float* weights, void* ws, size_t ws_bytes,
                hipStream_t stream);
 
+/* ------------------------------------------------------- 8-bit integer products --
+ * The solvers' codes at up to 8 bits with one grid per output channel (group_size == d_i),
+ * multiplied as integers by the matrix cores.  Storage of a [rows x cols] matrix:
+ *   codes   [rows x qz_i8_pitch(cols)] int8, the pitch being cols rounded up to 128; columns past
+ *           `cols` hold zeros.  16-byte aligned.
+ *   scales  [rows] fp32.
+ *   zeros   [rows] u8, weights only, nullable: the zero points of the solvers' unsigned codes, so
+ *           that value = scale (code + 128 - zero); null: 128 everywhere (value = scale code).
+ *   1 <= cols <= 65536 (then every sum of products fits 32 bits).
+ *
+ * qz_i8_quantize: rows onto this format, symmetric: activations per token, weights per channel.
+ *   v = x, or fl32(x colf) with colf [cols] fp32 (nullable; smoothing factors: quantise the weights
+ *   with their reciprocals); s = fl32(max |v| / 127); code = the whole number nearest to v / s, ties
+ *   to the even one, within -127 .. 127 (the quotient itself, not its rounding to 32 bits, decides).
+ *   s = 0 (zero rows) gives zero codes; a row with a NaN or an infinity gets s = NaN and zero codes.
+ *   X       [rows x cols], dtype xt, row stride ldx >= cols elements.
+ *   sums    nullable: [rows] int32, each row's sum of codes (what zero points are multiplied by).
+ *   values  nullable: [rows x cols] dense, dtype xt: code s in 32 bits, then in xt, in the same
+ *           pass.  Must not overlap X.
+ * Asynchronous, no workspace.
+ *
+ * qz_i8_pack: the solvers' codes [rows x cols] u8 (qz_rtn, qz_gptq, qz_admmq with group_size == cols)
+ *   as int8 codes, each less 128, in padded rows; their scales and zeros are used as they are.
+ * qz_i8_unpack: back: out [rows x cols] u8 = code + 128, for qz_objective (group_size = cols) and
+ *   qz_pack; with zero points of 128 for matrices of qz_i8_quantize.  Both asynchronous.          */
+#define QZ_I8_MAX_COLS 65536
+int64_t qz_i8_pitch(int64_t cols);   /* -1 for cols outside 1 .. 65536 */
+int qz_i8_quantize(const void* X, int32_t xt, int64_t rows, int64_t cols, int64_t ldx,
+                   const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
+                   hipStream_t stream);
+int qz_i8_pack(const uint8_t* codes, int64_t rows, int64_t cols, int8_t* out, hipStream_t stream);
+int qz_i8_unpack(const int8_t* codes, int64_t rows, int64_t cols, uint8_t* out, hipStream_t stream);
+
+/* Products Y = X W^T + bias of that format:
+ *   a = sum_j x_j w_j - (zero - 128) sum_j x_j, exact in integers;
+ *   y = fl(fl32(fl32(sx a) sw + bias)): a to fp32, times sx, then one fused step, then Y's type.
+ *   qz_i8_matmul: X [n x d_i] as codes, scales and (needed with zeros) row sums.
+ *   qz_i8_linear: X [n x d_i] in dtype xt, row stride ldx >= d_i, quantized in the same call as
+ *     qz_i8_quantize does (colf nullable); the same bytes as the two calls.
+ *   W [d_o x d_i]: codes, scales, zeros (nullable).  bias [d_o] fp32, nullable.
+ *   Y [n x d_o], dtype yt (QZ_BF16 or QZ_F32), row stride ldy >= d_o (elements between the rows are
+ *   left alone).  Must not overlap the inputs.
+ *   n <= 2^20, d_o <= 2^24, d_i <= 65536; n = 0 or d_o = 0 does nothing.
+ *   ws: as many bytes as the query says for the same sizes, 256-byte aligned; 0 bytes: may be null (0
+ *   for bad sizes too); calls that may overlap need different workspaces.  Asynchronous.        */
+size_t qz_i8_matmul_workspace(int64_t n, int64_t d_o, int64_t d_i);
+int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsums, int64_t n,
+                 const int8_t* codes, const float* scales, const uint8_t* zeros, int64_t d_o,
+                 int64_t d_i, const float* bias, void* Y, int32_t yt, int64_t ldy, void* ws,
+                 size_t ws_bytes, hipStream_t stream);
+size_t qz_i8_linear_workspace(int64_t n, int64_t d_o, int64_t d_i);
+int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float* colf,
+                 const int8_t* codes, const float* scales, const uint8_t* zeros, int64_t d_o,
+                 int64_t d_i, const float* bias, void* Y, int32_t yt, int64_t ldy, void* ws,
+                 size_t ws_bytes, hipStream_t stream);
+
+/* qz_route: the experts of each token and their weights, from the router's logits, in 64 bits.
+ *   score = softmax over the row, or with QZ_ROUTE_SIGMOID 1 / (1 + exp(-logit)).
+ *   choice = score + bias (bias [n_experts] fp32, nullable: moves the choice, not the weight).
+ *   A logit of -inf or NaN (or a choice that is NaN) makes the expert's choice -inf and its score 0.
+ *   n_groups groups of n_experts / n_groups neighbours: a group counts as the sum of its group_best
+ *     (1 or 2) largest choices above -inf; the top_groups best groups stay.
+ *   ids: the top_k experts of those by descending choice; weights: their scores, with
+ *     QZ_ROUTE_RENORM divided by their sum, times `scale`; a sum of zero leaves weights of zero.
+ *   Ties go to the lower index, for groups and experts.  ids are always top_k different experts.
+ *   logits [n x n_experts], dtype lt, row stride ldl >= n_experts; ids [n x top_k] int32 and weights
+ *   [n x top_k] fp32, dense.
+ *   1 <= n_experts <= 512, n_groups <= 64 divides it, 1 <= top_k <= 16 and at most the experts of
+ *   top_groups groups, n <= 2^24.  Asynchronous, no workspace.                                 */
+#define QZ_ROUTE_SIGMOID 0x1u
+#define QZ_ROUTE_RENORM 0x2u
+#define QZ_ROUTE_MAX_EXPERTS 512
+#define QZ_ROUTE_MAX_GROUPS 64
+#define QZ_ROUTE_MAX_TOP_K 16
+typedef struct {
+  uint32_t struct_size;   /* sizeof(qz_router) */
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t n_groups;       /* 1: no groups */
+  int32_t top_groups;
+  int32_t group_best;
+  uint32_t flags;         /* QZ_ROUTE_SIGMOID, QZ_ROUTE_RENORM */
+  float scale;            /* finite */
+} qz_router;
+int qz_route(const void* logits, int32_t lt, int64_t n, int64_t ldl, const qz_router* params,
+             const float* bias, int32_t* ids, float* weights, hipStream_t stream);
+
+/* qz_i8_moe: a routed expert layer on 8-bit integer weights, from one token to prefill sizes:
+ *   y_t = fl16(sum_r weights[t, r] W_down[e] Q(silu(g) * u)), [g; u] = W_gate_up[e] Q(x_t),
+ *   e = ids[t, r], Q: qz_i8_quantize of the row (x per token, the hidden vector, held in fp32, per
+ *   token and expert).  The sum is in fp32 in the order of r.  An id outside [0, n_experts) is
+ *   skipped (an expert held elsewhere); a token with none left gets zeros.  The same id may appear
+ *   twice.
+ *   X [n x d] dtype xt, row stride ldx >= d; ids, weights [n x top_k] as qz_route writes them.
+ *   gu_codes/gu_scales/gu_zeros: [n_experts x 2 f] rows of d columns, gate rows before up rows;
+ *   dn_codes/dn_scales/dn_zeros: [n_experts x d] rows of f columns; zeros nullable.  Y [n x d] bf16,
+ *   dense.  Must not overlap the inputs.
+ *   1 <= n_experts <= 512, 1 <= top_k <= 16, n <= 2^20 and n pitch(d) < 2^31, d and f <= 65536.
+ *   ws: qz_i8_moe_workspace(...) bytes, 256-byte aligned; calls that may overlap need different
+ *   workspaces.  Asynchronous.                                                                 */
+size_t qz_i8_moe_workspace(int64_t n, int64_t d, int64_t f, int32_t n_experts, int32_t top_k);
+int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int64_t f,
+              int32_t n_experts, int32_t top_k, const int32_t* ids, const float* weights,
+              const int8_t* gu_codes, const float* gu_scales, const uint8_t* gu_zeros,
+              const int8_t* dn_codes, const float* dn_scales, const uint8_t* dn_zeros, void* Y,
+              void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* ----------------------------------------------------------------- timing --
  * Per-kernel timing for measurement tools: while enabled, the library records a
  * HIP event pair around each of its kernel launches, on the stream the kernel
@@ -455,7 +562,7 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
  *   QZ_TIMING_KINDS) (host arrays, may be NULL), waits for the recorded events
  *   (SYNC), then, if reset != 0, drops the records.  Returns the number of kinds.
  *   qz_timing_kind_name(k) names kind k ("" when out of range).              */
-#define QZ_TIMING_KINDS 21
+#define QZ_TIMING_KINDS 25
 int qz_timing_enable(int on);
 int qz_timing_read(int64_t* launches, double* total_ms, int max_kinds, int reset);
 const char* qz_timing_kind_name(int kind);

@@ -15,8 +15,8 @@ import ctypes as C
 from . import _lib
 from ._lib import (QZ_ADMM_DUAL_NO_RESCALE, QZ_ADMM_REFRESH_FROM_Z, QZ_ADMM_REFRESH_UNCLAMPED,  # noqa: F401
                    QZ_ADMM_WARM_START, QZ_BF16, QZ_F32, QZ_GRID_CALLER, QZ_H_ACCUMULATE,
-                   QZ_H_NO_FINALIZE, QZ_MOE_RENORM, QZ_MX4_FLOOR, QZ_MX4_LEAST, QzAdmm, QzGrid,
-                   QzMoe)
+                   QZ_H_NO_FINALIZE, QZ_I8_MAX_COLS, QZ_MOE_RENORM, QZ_MX4_FLOOR, QZ_MX4_LEAST,
+                   QZ_ROUTE_RENORM, QZ_ROUTE_SIGMOID, QzAdmm, QzGrid, QzMoe, QzRouter)
 
 
 class QzError(RuntimeError):
@@ -569,6 +569,208 @@ def qz_mx4_moe(X, router, gu_codes, gu_scales, dn_codes, dn_scales, top_k, renor
          _dtype_code(router), gu_codes.data_ptr(), gu_scales.data_ptr(), dn_codes.data_ptr(),
          dn_scales.data_ptr(), y.data_ptr(), ip, kp, wp, wn)
     return (y, ids, w) if routing else y
+
+
+# ------------------------------------------------------------------ 8-bit integer products
+def qz_i8_pitch(cols) -> int:
+    return lib().qz_i8_pitch(cols)
+
+
+def _i8_rows(codes, scales, rows, cols, name, index):
+    """Checks that codes and scales store `rows` rows of `cols` columns, on GPU `index`."""
+    torch = _torch()
+    if not 1 <= cols <= QZ_I8_MAX_COLS:
+        raise ValueError(f"{name} must have 1 to {QZ_I8_MAX_COLS} columns")
+    pitch = (cols + 127) & ~127
+    if codes.dtype is not torch.int8 or scales.dtype is not torch.float32:
+        raise TypeError(f"{name}: codes must be int8 and scales fp32")
+    if codes.get_device() != index or scales.get_device() != index:
+        raise ValueError(f"{name}: codes and scales must be on GPU {index}")
+    if not (codes.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{name}: codes and scales must be contiguous")
+    if codes.shape == (rows, pitch) and scales.shape == (rows,):
+        return
+    if codes.shape[-1] != pitch or codes.numel() != pitch * rows or scales.numel() != rows:
+        raise ValueError(f"{name}: expected {rows} rows of {pitch} codes and {rows} scales")
+
+
+def _i8_zeros(t, rows, name, index):
+    if t is None:
+        return None
+    if t.dtype is not _torch().uint8:
+        raise TypeError(f"{name}: zeros must be uint8")
+    if t.get_device() != index or t.numel() != rows or not t.is_contiguous():
+        raise ValueError(f"{name}: zeros must be {rows} contiguous values on GPU {index}")
+    return t.data_ptr()
+
+
+def qz_i8_quantize(X, colf=None, sums=False, values=False):
+    """Rows of a matrix (bf16 or fp32, contiguous rows), times the column factors colf, to int8 with a
+    scale each: (codes int8 [rows x pitch], scales fp32 [rows]), then with sums=True the rows' sums of
+    codes (int32), and with values=True the numbers the codes stand for in X's dtype."""
+    torch = _torch()
+    ld = _matrix(X, "X")
+    xt = _dtype_code(X)
+    rows, cols = X.shape
+    if not 1 <= cols <= QZ_I8_MAX_COLS:
+        raise ValueError(f"X must have 1 to {QZ_I8_MAX_COLS} columns")
+    index = X.device.index
+    codes = X.new_empty((rows, (cols + 127) & ~127), dtype=torch.int8)
+    scales = X.new_empty((rows,), dtype=torch.float32)
+    total = X.new_empty((rows,), dtype=torch.int32) if sums else None
+    out = X.new_empty((rows, cols)) if values else None
+    _run(index, lib().qz_i8_quantize, X.data_ptr(), xt, rows, cols, ld, _vector(colf, cols, "colf", index),
+         codes.data_ptr(), scales.data_ptr(), total.data_ptr() if sums else None,
+         out.data_ptr() if values else None)
+    return (codes, scales) + ((total,) if sums else ()) + ((out,) if values else ())
+
+
+def qz_i8_pack(codes):
+    """The solvers' codes (uint8 [rows x cols]) as int8 codes less 128, in padded rows."""
+    torch = _torch()
+    _dev(codes, "codes")
+    if codes.dtype is not torch.uint8 or codes.dim() != 2:
+        raise TypeError("codes must be a uint8 matrix")
+    rows, cols = codes.shape
+    if not 1 <= cols <= QZ_I8_MAX_COLS:
+        raise ValueError(f"codes must have 1 to {QZ_I8_MAX_COLS} columns")
+    out = codes.new_empty((rows, (cols + 127) & ~127), dtype=torch.int8)
+    _run(codes.device.index, lib().qz_i8_pack, codes.data_ptr(), rows, cols, out.data_ptr())
+    return out
+
+
+def qz_i8_unpack(codes, cols):
+    """The int8 codes' uint8 form (code + 128), [rows x cols]."""
+    torch = _torch()
+    _dev(codes, "codes")
+    if codes.dtype is not torch.int8 or codes.dim() != 2:
+        raise TypeError("codes must be an int8 matrix")
+    if not 1 <= cols <= QZ_I8_MAX_COLS or codes.shape[1] != (cols + 127) & ~127:
+        raise ValueError(f"rows of {cols} columns do not have {codes.shape[1]} codes")
+    out = codes.new_empty((codes.shape[0], cols), dtype=torch.uint8)
+    _run(codes.device.index, lib().qz_i8_unpack, codes.data_ptr(), codes.shape[0], cols, out.data_ptr())
+    return out
+
+
+def qz_i8_matmul_workspace(n, d_o, d_i) -> int:
+    return lib().qz_i8_matmul_workspace(n, d_o, d_i)
+
+
+def qz_i8_matmul(xcodes, xscales, codes, scales, d_i, zeros=None, xsums=None, bias=None,
+                 out_dtype=None, out=None, ws=None):
+    """Y = X W^T + bias with X [n x d_i] and W [d_o x d_i] both as int8 rows.  zeros (the solvers'
+    zero points of W, uint8 [d_o]) needs xsums, the row sums of X.  Y is out_dtype (bf16 or fp32;
+    default bf16), or `out` is written."""
+    L = lib()
+    _dev(xcodes, "X codes")
+    n, d_o, dev = xcodes.shape[0], codes.shape[0], xcodes.device
+    index = dev.index
+    _i8_rows(xcodes, xscales, n, d_i, "X", index)
+    _i8_rows(codes, scales, d_o, d_i, "W", index)
+    zp = _i8_zeros(zeros, d_o, "W", index)
+    if xsums is not None:
+        if xsums.dtype is not _torch().int32:
+            raise TypeError("xsums must be int32")
+        if xsums.get_device() != index or xsums.shape != (n,) or not xsums.is_contiguous():
+            raise ValueError(f"xsums must be {n} contiguous values on GPU {index}")
+    elif zp is not None:
+        raise ValueError("zeros need xsums, the row sums of X")
+    out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
+    wp, wn, ws = _scratch(ws, L.qz_i8_matmul_workspace(n, d_o, d_i), dev)
+    _run(index, L.qz_i8_matmul, xcodes.data_ptr(), xscales.data_ptr(),
+         None if xsums is None else xsums.data_ptr(), n, codes.data_ptr(), scales.data_ptr(), zp, d_o,
+         d_i, _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy, wp, wn)
+    return out
+
+
+def qz_i8_linear_workspace(n, d_o, d_i) -> int:
+    return lib().qz_i8_linear_workspace(n, d_o, d_i)
+
+
+def qz_i8_linear(X, codes, scales, zeros=None, colf=None, bias=None, out_dtype=None, out=None, ws=None):
+    """Y = Q(X) W^T + bias: X (bf16 or fp32 [n x d_i], contiguous rows), times the column factors
+    colf, is quantized per row in the same call; W [d_o x d_i] as int8 rows with zeros or without."""
+    L = lib()
+    ldx = _matrix(X, "X")
+    xt = _dtype_code(X)
+    (n, d_i), d_o, dev = X.shape, codes.shape[0], X.device
+    index = dev.index
+    _i8_rows(codes, scales, d_o, d_i, "W", index)
+    out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
+    wp, wn, ws = _scratch(ws, L.qz_i8_linear_workspace(n, d_o, d_i), dev)
+    _run(index, L.qz_i8_linear, X.data_ptr(), xt, n, ldx, _vector(colf, d_i, "colf", index),
+         codes.data_ptr(), scales.data_ptr(), _i8_zeros(zeros, d_o, "W", index), d_o, d_i,
+         _vector(bias, d_o, "bias", index), out.data_ptr(), yt, ldy, wp, wn)
+    return out
+
+
+def _int32(v, name):
+    v = int(v)
+    if not -2 ** 31 <= v < 2 ** 31:      # ctypes would cut it to 32 bits
+        raise ValueError(f"{name} must fit 32 bits")
+    return v
+
+
+def qz_route(logits, top_k, scores="softmax", bias=None, groups=1, top_groups=1, group_best=1,
+             renorm=True, scale=1.0):
+    """(ids int32, weights fp32) [n x top_k]: the experts of each token from the router's logits (bf16
+    or fp32 [n x E], contiguous rows).  scores "softmax" or "sigmoid"; bias fp32 [E] moves the choice
+    alone; of `groups` groups the best top_groups stay, each counted by the sum of its group_best
+    (1 or 2) largest choices; weights divided by their sum with renorm, times scale."""
+    torch = _torch()
+    ld = _matrix(logits, "logits")
+    lt = _dtype_code(logits)
+    n, E = logits.shape
+    if scores not in ("softmax", "sigmoid"):
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
+    k, index = _int32(top_k, "top_k"), logits.device.index
+    p = QzRouter(C.sizeof(QzRouter), _int32(E, "the number of experts"), k, _int32(groups, "groups"),
+                 _int32(top_groups, "top_groups"), _int32(group_best, "group_best"),
+                 (_lib.QZ_ROUTE_SIGMOID if scores == "sigmoid" else 0) | (_lib.QZ_ROUTE_RENORM if renorm else 0),
+                 scale)
+    ids = logits.new_empty((n, max(k, 0)), dtype=torch.int32)
+    w = logits.new_empty((n, max(k, 0)), dtype=torch.float32)
+    _run(index, lib().qz_route, logits.data_ptr(), lt, n, ld, C.byref(p), _vector(bias, E, "bias", index),
+         ids.data_ptr(), w.data_ptr())
+    return ids, w
+
+
+def qz_i8_moe_workspace(n, d, f, n_experts, top_k) -> int:
+    return lib().qz_i8_moe_workspace(n, d, f, _int32(n_experts, "the number of experts"), _int32(top_k, "top_k"))
+
+
+def qz_i8_moe(X, ids, weights, gu_codes, gu_scales, dn_codes, dn_scales, gu_zeros=None, dn_zeros=None,
+              ws=None):
+    """The routed expert layer on int8 weights: X (bf16 or fp32 [n x d]), ids (int32) and weights (fp32)
+    [n x top_k] as qz_route returns them, gate and up weights [E x 2f x d] and down weights [E x d x f]
+    as int8 rows with zeros or without.  Returns Y bf16 [n x d]; ids outside [0, E) are skipped."""
+    torch, L = _torch(), lib()
+    ldx = _matrix(X, "X")
+    xt = _dtype_code(X)
+    (n, d), dev = X.shape, X.device
+    index = dev.index
+    if gu_scales.dim() != 2 or gu_scales.shape[1] % 2 or dn_scales.dim() != 2:
+        raise ValueError("the scales must be [E x 2f] and [E x d]")
+    E, f = gu_scales.shape[0], gu_scales.shape[1] // 2
+    if dn_scales.shape != (E, d):
+        raise ValueError("the down weights must be [E x d x f]")
+    _i8_rows(gu_codes, gu_scales, E * 2 * f, d, "gate and up weights", index)
+    _i8_rows(dn_codes, dn_scales, E * d, f, "down weights", index)
+    if ids.dtype is not torch.int32 or weights.dtype is not torch.float32:
+        raise TypeError("ids must be int32 and weights fp32")
+    if ids.dim() != 2 or ids.shape[0] != n or weights.shape != ids.shape:
+        raise ValueError(f"ids and weights must be [{n} x top_k]")
+    if ids.get_device() != index or weights.get_device() != index \
+            or not (ids.is_contiguous() and weights.is_contiguous()):
+        raise ValueError(f"ids and weights must be contiguous and on GPU {index}")
+    k = ids.shape[1]
+    wp, wn, ws = _scratch(ws, L.qz_i8_moe_workspace(n, d, f, E, k), dev)
+    y = X.new_empty((n, d), dtype=torch.bfloat16)
+    _run(index, L.qz_i8_moe, X.data_ptr(), xt, n, ldx, d, f, E, k, ids.data_ptr(), weights.data_ptr(),
+         gu_codes.data_ptr(), gu_scales.data_ptr(), _i8_zeros(gu_zeros, E * 2 * f, "gate and up weights", index),
+         dn_codes.data_ptr(), dn_scales.data_ptr(), _i8_zeros(dn_zeros, E * d, "down weights", index),
+         y.data_ptr(), wp, wn)
+    return y
 
 
 def qz_timing_enable(on=True):

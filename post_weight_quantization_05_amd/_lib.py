@@ -21,6 +21,8 @@ QZ_ORDER_ACT = 1
 QZ_ORDER_MIN_PIVOT = 2
 QZ_MX4_FLOOR, QZ_MX4_LEAST = 0, 1
 QZ_MOE_RENORM = 0x1
+QZ_ROUTE_SIGMOID, QZ_ROUTE_RENORM = 0x1, 0x2
+QZ_I8_MAX_COLS = 65536
 
 STATUS_NAMES = {0: "QZ_OK", -1: "QZ_EINVAL", -2: "QZ_ENOTPD", -3: "QZ_ENONFINITE", -4: "QZ_EHIP",
                 -5: "QZ_ESOLVER", -6: "QZ_EWORKSPACE"}
@@ -39,6 +41,9 @@ EXPORTS = ("qz_hessian_workspace", "qz_build_hessian", "qz_rtn_workspace", "qz_r
            "qz_mx4_blocks", "qz_mx4_quantize", "qz_mx4_unpack", "qz_mx4_linear_workspace",
            "qz_mx4_linear", "qz_mx4_matmul_workspace", "qz_mx4_matmul", "qz_mx4_moe_workspace",
            "qz_mx4_moe",
+           "qz_i8_pitch", "qz_i8_quantize", "qz_i8_pack", "qz_i8_unpack", "qz_i8_matmul_workspace",
+           "qz_i8_matmul", "qz_i8_linear_workspace", "qz_i8_linear", "qz_route",
+           "qz_i8_moe_workspace", "qz_i8_moe",
            "qz_timing_enable", "qz_timing_read", "qz_timing_kind_name",
            "qz_last_error", "qz_abi_version")
 
@@ -57,6 +62,12 @@ class QzAdmm(C.Structure):
 class QzMoe(C.Structure):
     _fields_ = [("struct_size", C.c_uint32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
                 ("flags", C.c_uint32)]
+
+
+class QzRouter(C.Structure):
+    _fields_ = [("struct_size", C.c_uint32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
+                ("n_groups", C.c_int32), ("top_groups", C.c_int32), ("group_best", C.c_int32),
+                ("flags", C.c_uint32), ("scale", C.c_float)]
 
 
 P = C.c_void_p
@@ -104,6 +115,17 @@ _SIGS = {
     "qz_mx4_moe_workspace": (SZ, [I64, I64, I64, C.POINTER(QzMoe)]),
     "qz_mx4_moe": (C.c_int, [P, I32, I64, I64, I64, I64, C.POINTER(QzMoe), P, I32, P, P, P, P, P, P,
                              P, P, SZ, P]),
+    "qz_i8_pitch": (I64, [I64]),
+    "qz_i8_quantize": (C.c_int, [P, I32, I64, I64, I64, P, P, P, P, P, P]),
+    "qz_i8_pack": (C.c_int, [P, I64, I64, P, P]),
+    "qz_i8_unpack": (C.c_int, [P, I64, I64, P, P]),
+    "qz_i8_matmul_workspace": (SZ, [I64, I64, I64]),
+    "qz_i8_matmul": (C.c_int, [P, P, P, I64, P, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),
+    "qz_i8_linear_workspace": (SZ, [I64, I64, I64]),
+    "qz_i8_linear": (C.c_int, [P, I32, I64, I64, P, P, P, P, I64, I64, P, P, I32, I64, P, SZ, P]),
+    "qz_route": (C.c_int, [P, I32, I64, I64, C.POINTER(QzRouter), P, P, P, P]),
+    "qz_i8_moe_workspace": (SZ, [I64, I64, I64, I32, I32]),
+    "qz_i8_moe": (C.c_int, [P, I32, I64, I64, I64, I64, I32, I32, P, P, P, P, P, P, P, P, P, P, SZ, P]),
     "qz_timing_enable": (C.c_int, [C.c_int]),
     "qz_timing_read": (C.c_int, [C.POINTER(C.c_int64), C.POINTER(C.c_double), C.c_int, C.c_int]),
     "qz_timing_kind_name": (C.c_char_p, [C.c_int]),

@@ -63,6 +63,10 @@ enum KernelKind : int {
   K_MX4_QUANTIZE,
   K_MX4_PRODUCT,
   K_MX4_MOE,
+  K_I8_QUANTIZE,
+  K_I8_PRODUCT,
+  K_ROUTE,
+  K_I8_MOE,
   K_KIND_COUNT
 };
 // Records an event pair around the enclosed launches when timing is enabled.
@@ -298,6 +302,41 @@ struct MoeArgs {
 };
 int moe_slots(int64_t n, int E, int k);
 int launch_moe(const MoeArgs& a, int router_type, hipStream_t s);
+
+// 8-bit integer storage, products, routing and expert layer (k_i8.hip, k_i8_gemm.hip, k_route.hip,
+// k_i8_moe.hip)
+__host__ __device__ inline int64_t i8_pitch(int64_t cols) { return round_up(cols, 128); }
+int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx,
+                       const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
+                       hipStream_t s);
+int launch_i8_pack(const uint8_t* codes, int64_t rows, int64_t cols, int8_t* out, hipStream_t s);
+int launch_i8_unpack(const int8_t* codes, int64_t rows, int64_t cols, uint8_t* out, hipStream_t s);
+// Rows of X against rows of W: every row (plain), or the slots of an expert layer: pairs (token, r)
+// sorted by expert, slot i holding pair order[i], expert e's slots being offsets[e] .. offsets[e+1].
+struct I8Product {
+  int64_t n, d_o;                               // rows of X (slots at most), rows of W (of an expert)
+  int64_t P;                                    // pitch of the rows of X and W, bytes
+  const int8_t* X; const float* sx; const int32_t* xsum;
+  const int8_t* W; const float* sw; const uint8_t* zeros;   // zeros null: 128
+  const float* bias;                            // [d_o] or null
+  void* Y; int yt; int64_t ldy;
+  int32_t* partial;                             // split sums, or null
+  const int32_t* offsets; const int32_t* order; // of an expert layer
+  const float* pair_weight;                     // [pairs]
+  int E, k;
+};
+size_t i8_product_ws(int64_t n, int64_t d_o, int64_t P);
+int launch_i8_product(const I8Product& p, hipStream_t s);
+// h[slot] = silu(gate) up, fp32 [slots x ldy]; rows d_o of W are gate rows, the next d_o up rows
+int launch_i8_gate_up(const I8Product& p, hipStream_t s);
+// Y[pair] = pair_weight[pair] * product, fp32 [pairs x ldy]
+int launch_i8_down(const I8Product& p, hipStream_t s);
+int launch_i8_group(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* order,
+                    hipStream_t s);
+int launch_i8_sum(const float* y_pairs, int64_t ldp, const int32_t* ids, int64_t n, int64_t d,
+                  int k, int E, uint16_t* Y, hipStream_t s);
+int launch_route(const void* logits, int lt, int64_t n, int64_t ldl, const qz_router& r,
+                 const float* bias, int32_t* ids, float* weights, hipStream_t s);
 
 // eigendecomposition of Sigma H Sigma (k_eig.hip): workspace bytes (asks the solver library
 // for its scratch size once per size), and the decomposition in the caller's workspace

@@ -1,0 +1,571 @@
+"""GPU: the 8-bit integer operators and the router against their definitions in 64 bits.
+
+Quantisation, packing, and the experts that the router chooses are compared for equality.  Products:
+the integer sums are exact, so with scales that are powers of two, a sum below 2^24 and a whole bias
+the result is the one rounding to the output type; on ordinary values the sum's conversion, the
+product with sx and the fused step round once each, at most half a step of 2^-23 of what they round:
+    |error| <= 2^-24 (3 |sx sw a| + 2 |bias|) (1 + 2^-20), and 2^-8 |y| (1 + 2^-8) more in bf16."""
+import numpy as np
+import pytest
+
+from gpu_util import qz, to_dev, to_host
+from oracle import i8
+
+pytestmark = pytest.mark.gpu
+
+
+def _t():
+    import torch
+    return torch
+
+
+def _dtype(name):
+    return {"bf16": _t().bfloat16, "f32": _t().float32}[name]
+
+
+def _host(t):
+    return t.double().cpu().numpy() if t.is_floating_point() else to_host(t)
+
+
+def _rounded(a, dtype):
+    """Values (64 bits) rounded to 32 bits and then to dtype, and the device tensor."""
+    t = _t().from_numpy(np.ascontiguousarray(a, np.float32)).to(_dtype(dtype))
+    return t.float().numpy(), t.cuda()
+
+
+def _same(got, want):
+    np.testing.assert_array_equal(to_host(got) if not hasattr(got, "dtype") or not got.is_floating_point()
+                                  else got.float().cpu().numpy(), want)
+
+
+# ------------------------------------------------------------------------------ quantisation
+def _check_quantize(x, xd, colf, cols):
+    q = qz()
+    c, s, total, v = q.qz_i8_quantize(xd, colf=None if colf is None else to_dev(colf), sums=True, values=True)
+    c_ref, s_ref = i8.quantize(x, colf)
+    _same(s, s_ref)
+    _same(c, i8.padded(c_ref))
+    _same(total, c_ref.astype(np.int64).sum(1))
+    assert v.dtype == xd.dtype
+    with np.errstate(all="ignore"):
+        want = _t().from_numpy(c_ref.astype(np.float32) * s_ref[:, None]).to(xd.dtype).float().numpy()
+    _same(v, want)
+    c2, s2 = q.qz_i8_quantize(xd, colf=None if colf is None else to_dev(colf))
+    assert _t().equal(c, c2) and (_t().equal(s, s2) or np.isnan(s_ref).any())
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 31), (2, 128), (5, 129), (70, 200), (33, 1056), (9, 2048), (7, 2050),
+                                       (64, 4096), (300, 520), (5, 8192), (4, 8200), (3, 12288), (2, 16385),
+                                       (1, 25600), (2, 65536)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factors", [False, True])
+def test_quantize_exact(rows, cols, dtype, factors):
+    rng = np.random.default_rng([rows, cols])
+    w = rng.standard_normal((rows, cols)) * np.exp(rng.standard_normal((rows, 1)))
+    w[rng.random((rows, cols)) < 0.1] = 0.0
+    tied = rng.random(rows) < 0.5      # rows of halves under a scale of 2^-5
+    w[tied] = np.clip(np.round(w[tied] * 64), -250, 250) / 64
+    w[tied, 0] = 127 / 32
+    x, xd = _rounded(w, dtype)
+    colf = np.exp(0.5 * rng.standard_normal(cols)).astype(np.float32) if factors else None
+    _check_quantize(x, xd, colf, cols)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_quantize_special_rows(dtype):
+    top = float(_t().finfo(_dtype(dtype)).max)
+    rows = [[0.0] * 40, [-0.0] * 40, [2.0 ** -126] * 40, [2.0 ** -133, -(2.0 ** -130)] * 20, [2.0 ** -133] + [0.0] * 39,
+            [190 * 2.0 ** -149, -(127 * 2.0 ** -149)] * 20, [top, -top] * 20, [1.0] * 32 + [float("nan")] + [2.0] * 7,
+            [float("inf")] + [1.0] * 39, [-float("inf"), float("nan")] * 20, [1e-30, 1e30] * 20,
+            [127.0, 0.5, -1.5, 2.5] * 10, [254.0, 1.0, -3.0, 253.0] * 10, [1e-38, -3e-39, 5e-38, 0.0] * 10]
+    x, xd = _rounded(rows, dtype)
+    _check_quantize(x, xd, None, 40)
+
+
+def test_quantize_every_quotient_near_a_half():
+    """Rows whose values lie next to (k + 1/2) s, one last bit to either side and on it."""
+    rng = np.random.default_rng(8)
+    rows = []
+    for _ in range(64):
+        top = np.float32(np.exp(3 * rng.standard_normal()))
+        s = np.float64(np.float32(top / np.float32(127)))
+        mid = ((np.arange(-126, 126) + 0.5) * s).astype(np.float32)
+        rows.append(np.concatenate([[top], mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(-np.inf))]))
+    x = np.stack(rows).astype(np.float32)
+    _check_quantize(x, to_dev(x), None, x.shape[1])
+
+
+def test_quantize_strided_and_unaligned_rows():
+    torch = _t()
+    base = torch.randn((37, 300), device="cuda")
+    wide = torch.randn((9, 9000), device="cuda")
+    for x in (base[:, 5:205], base[:, 4:132], base[::2, 1:97], base[3:4, 7:39], base.to(torch.bfloat16)[:, 3:131],
+              base.to(torch.bfloat16)[:, 8:200], wide[:, 3:8600], wide.to(torch.bfloat16)[:, 8:8200]):
+        _check_quantize(x.float().cpu().numpy(), x, None, x.shape[1])
+    q = qz()
+    c, s = q.qz_i8_quantize(torch.empty((0, 40), device="cuda"))
+    assert c.shape == (0, 128) and s.shape == (0,)
+
+
+def test_pack_and_unpack():
+    q = qz()
+    rng = np.random.default_rng(1)
+    for rows, cols in ((1, 1), (5, 127), (8, 128), (17, 300)):
+        u = rng.integers(0, 256, (rows, cols)).astype(np.uint8)
+        c = q.qz_i8_pack(to_dev(u))
+        _same(c, i8.padded((u.astype(np.int64) - 128).astype(np.int8)))
+        _same(q.qz_i8_unpack(c, cols), u)
+
+
+# ---------------------------------------------------------------------------------- products
+NS = [1, 2, 5, 15, 16, 17, 31, 33, 64, 65, 128, 129, 200, 257, 300, 513]
+SHAPES = [(32, 16), (1, 1), (31, 7), (128, 15), (64, 17), (96, 100), (200, 33), (512, 64), (640, 130), (1024, 257),
+          (1056, 40), (2080, 520), (4100, 260)]
+
+
+def _cases():
+    """Every n with some shape and every shape with some n, and the corners of both."""
+    out = [(n, *SHAPES[i % len(SHAPES)]) for i, n in enumerate(NS)]
+    out += [(NS[(5 * i + 3) % len(NS)], *s) for i, s in enumerate(SHAPES)]
+    return sorted(set(out + [(513, 2080, 520), (1, 2080, 520), (257, 1, 1), (130, 96, 1030), (1, 12800, 70)]))
+
+
+def _stored(rng, rows, cols, lo=-127, hi=127):
+    return rng.integers(lo, hi + 1, (rows, cols)).astype(np.int8)
+
+
+def _powers(rng, n):
+    return np.ldexp(1.0, rng.integers(-3, 4, n)).astype(np.float32)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", _cases())
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_matmul_exact(n, d_i, d_o, out):
+    """Codes small enough that sums stay below 2^24: exact in fp32, with zero points or without."""
+    q = qz()
+    rng = np.random.default_rng([n, d_i, d_o])
+    top = int(min(127, np.sqrt(2.0 ** 23 / d_i / 4)))
+    zeros = rng.integers(128 - top, 129 + top, d_o).astype(np.uint8) if (n + d_i) % 2 else None
+    xq, wq = _stored(rng, n, d_i, -top, top), _stored(rng, d_o, d_i, -top, top)
+    sx, sw = _powers(rng, n), _powers(rng, d_o)
+    bias = rng.integers(-50, 50, d_o).astype(np.float32) if (n + d_o) % 2 else None
+    y = i8.product(xq, sx, wq, sw, zeros, None if bias is None else bias.astype(np.float64))
+    sums = xq.astype(np.int64).sum(1).astype(np.int32)
+    got = q.qz_i8_matmul(to_dev(i8.padded(xq)), to_dev(sx), to_dev(i8.padded(wq)), to_dev(sw), d_i,
+                         zeros=None if zeros is None else to_dev(zeros), xsums=to_dev(sums),
+                         bias=None if bias is None else to_dev(bias), out_dtype=_dtype(out))
+    assert got.dtype == _dtype(out)
+    _same(got, _t().from_numpy(y).float().to(_dtype(out)).float().numpy())
+
+
+def test_matmul_of_the_largest_sums():
+    """65536 columns of extreme codes: sums up to 65536 * 128 * 255 = 2^31 - 2^23, in integers."""
+    q = qz()
+    d_i = 65536
+    xq = np.stack([np.full(d_i, -128), np.full(d_i, 127), np.resize([127, -128], d_i)]).astype(np.int8)
+    wq = np.stack([np.full(d_i, -128), np.full(d_i, 127), np.full(d_i, 127), np.resize([-128, 127], d_i)]).astype(np.int8)
+    zeros = np.array([255, 0, 128, 3], np.uint8)
+    one = np.ones(4, np.float32)
+    a = xq.astype(np.int64) @ i8.levels(wq, zeros).T
+    assert np.abs(a).max() == 65536 * 128 * 255
+    for rows in (1, 3):
+        got = q.qz_i8_matmul(to_dev(xq[:rows]), to_dev(one[:rows]), to_dev(wq), to_dev(one), d_i, zeros=to_dev(zeros),
+                             xsums=to_dev(xq[:rows].astype(np.int64).sum(1).astype(np.int32)), out_dtype=_t().float32)
+        _same(got, a[:rows].astype(np.float32))
+
+
+def _bound(xq, sx, wq, sw, zeros, bias, out, y):
+    main = np.abs(i8.product(xq, sx, wq, sw, zeros))
+    e = 2.0 ** -24 * (3 * main + 2 * (0 if bias is None else np.abs(bias))) * (1 + 2.0 ** -20)
+    return e + (2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(y) if out == "bf16" else 0)
+
+
+ORDINARY = [(1, 4096, 512), (13, 5120, 300), (100, 1408, 256), (515, 2048, 384), (700, 4096, 1100), (260, 12288, 256)]
+
+
+@pytest.mark.parametrize("n,d_i,d_o", ORDINARY)
+@pytest.mark.parametrize("zeroed", [False, True])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_linear_of_ordinary_values(n, d_i, d_o, zeroed, out):
+    q = qz()
+    rng = np.random.default_rng([n, d_i])
+    x, xd = _rounded(rng.standard_t(4, (n, d_i)), "bf16" if n % 2 else "f32")
+    colf = np.exp(0.5 * rng.standard_normal(d_i)).astype(np.float32) if d_o % 3 else None
+    bias = rng.standard_normal(d_o).astype(np.float32) if zeroed else None
+    zeros = rng.integers(0, 256, d_o).astype(np.uint8) if zeroed else None
+    wq = _stored(rng, d_o, d_i, -128, 127)
+    sw = np.exp(rng.standard_normal(d_o)).astype(np.float32) * np.float32(1e-3)
+    xq, sx = i8.quantize(x, colf)
+    y = i8.product(xq, sx, wq, sw, zeros, None if bias is None else bias.astype(np.float64))
+    args = dict(zeros=None if zeros is None else to_dev(zeros), bias=None if bias is None else to_dev(bias),
+                out_dtype=_dtype(out))
+    factors = None if colf is None else to_dev(colf)
+    got = q.qz_i8_linear(xd, to_dev(i8.padded(wq)), to_dev(sw), colf=factors, **args)
+    assert (np.abs(_host(got) - y) <= _bound(xq, sx, wq, sw, zeros, bias, out, y)).all()
+    c, s, total = q.qz_i8_quantize(xd, colf=factors, sums=True)
+    two = q.qz_i8_matmul(c, s, to_dev(i8.padded(wq)), to_dev(sw), d_i, xsums=total, **args)
+    assert _t().equal(got, two)                            # the same bytes as the two calls
+
+
+@pytest.mark.parametrize("n", [1, 3, 20, 90, 300])
+def test_linear_special_rows(n):
+    """A row with a NaN or an infinity gives a row of NaN, a zero row the bias, and neither reaches others."""
+    q = qz()
+    rng = np.random.default_rng(n)
+    w = rng.standard_normal((n, 300))
+    for bad in (None, np.nan, np.inf):
+        x = w.copy()
+        at = n // 2
+        x[at] = 0
+        if bad is not None:
+            x[at, 7] = bad
+        x, xd = _rounded(x, "f32")
+        wq, sw = _stored(rng, 50, 300), np.ones(50, np.float32)
+        bias = np.arange(50, dtype=np.float32)
+        got = _host(q.qz_i8_linear(xd, to_dev(i8.padded(wq)), to_dev(sw), bias=to_dev(bias), out_dtype=_t().float32))
+        if bad is None:
+            np.testing.assert_array_equal(got[at], bias)
+        else:
+            assert np.isnan(got[at]).all()
+        rest = np.arange(n) != at
+        xq, sx = i8.quantize(x[rest])
+        y = i8.product(xq, sx, wq, sw, None, bias.astype(np.float64))
+        assert (np.abs(got[rest] - y) <= _bound(xq, sx, wq, sw, None, bias, "f32", y)).all()
+
+
+@pytest.mark.parametrize("n", [1, 9, 40, 129, 300])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_outputs_inside_a_wider_matrix(n, out):
+    """Row strides and addresses of X and Y that no vector access fits; what lies between is left alone."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(n)
+    wq, sw = _stored(rng, 131, 200), _powers(rng, 131)
+    big = torch.randn((n, 211), device="cuda")
+    for off in (0, 3):
+        x = big[:, off:off + 200]
+        xq, sx = i8.quantize(x.cpu().numpy())
+        y = i8.product(xq, sx, wq, sw)
+        hold = torch.full((n, 140), 7.0, device="cuda", dtype=_dtype(out))
+        got = q.qz_i8_linear(x, to_dev(i8.padded(wq)), to_dev(sw), out=hold[:, off:off + 131])
+        assert (np.abs(_host(got) - y) <= _bound(xq, sx, wq, sw, None, None, out, y)).all()
+        assert (hold[:, :off] == 7).all() and (hold[:, off + 131:] == 7).all()
+
+
+# ----------------------------------------------------------------------------------- routing
+ROUTES = [  # E, k, scores, bias, groups, top_groups, best, renorm
+    (1, 1, "softmax", False, 1, 1, 1, True), (4, 4, "softmax", True, 1, 1, 1, False),
+    (8, 2, "softmax", False, 1, 1, 1, True), (60, 4, "sigmoid", False, 1, 1, 1, True),
+    (64, 6, "softmax", False, 8, 3, 1, False), (65, 5, "sigmoid", True, 5, 2, 2, True),
+    (128, 8, "softmax", False, 1, 1, 1, True), (160, 6, "softmax", True, 8, 3, 1, False),
+    (256, 8, "sigmoid", True, 8, 4, 2, True), (257, 3, "sigmoid", True, 1, 1, 2, False),
+    (384, 8, "sigmoid", True, 1, 1, 1, True), (512, 16, "sigmoid", True, 64, 9, 2, True),
+    (512, 16, "softmax", False, 2, 2, 1, True), (16, 4, "sigmoid", True, 16, 4, 2, True),
+    (64, 1, "sigmoid", False, 4, 1, 2, True)]
+
+
+def _check_route(x, xd, k, **kw):
+    q = qz()
+    bias = kw.pop("bias", None)
+    want_ids, want_w = i8.route(x, k, bias=bias, **kw)
+    ids, w = q.qz_route(xd, k, bias=None if bias is None else to_dev(bias), **kw)
+    _same(ids, want_ids)
+    assert ids.dtype == _t().int32 and w.dtype == _t().float32
+    # one rounding to 32 bits; what 64 bits lose is far below the 2^-40 allowed for it
+    assert (np.abs(_host(w) - want_w) <= 2.0 ** -24 * (1 + 2.0 ** -16) * np.abs(want_w) + 2.0 ** -150).all()
+
+
+@pytest.mark.parametrize("E,k,scores,biased,groups,top_groups,best,renorm", ROUTES)
+@pytest.mark.parametrize("n,dtype", [(1, "bf16"), (7, "f32"), (50, "bf16"), (131, "f32")])
+def test_route(E, k, scores, biased, groups, top_groups, best, renorm, n, dtype):
+    rng = np.random.default_rng([E, k, n])
+    x, xd = _rounded(1.5 * rng.standard_normal((n, E)), dtype)      # bf16: ties among them
+    bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if biased else None
+    _check_route(x, xd, k, scores=scores, bias=bias, groups=groups, top_groups=top_groups, group_best=best,
+                 renorm=renorm, scale=2.5 if renorm else 1.0)
+
+
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top_groups", [(1, 1), (4, 2)])
+def test_route_masks_and_ties(scores, groups, top_groups):
+    inf, nan = np.inf, np.nan
+    rng = np.random.default_rng(3)
+    E = 96
+    x = rng.standard_normal((12, E))
+    x[0] = -inf                                  # nothing left
+    x[1] = nan
+    x[2] = 0.0                                   # all tied
+    x[3, 5:] = -inf                              # fewer than k left
+    x[4, ::2] = nan
+    x[5, 10], x[5, 50] = inf, inf
+    x[6] = np.where(np.arange(E) == 77, 0.0, np.finfo(np.float32).min)
+    x[7] = -700.0 - np.arange(E) / 8             # far down: scores of subnormal size under sigmoid
+    x[8] = np.repeat([1.0, 2.0], E // 2)
+    x[9] = 800.0
+    x[10, 24:] = -inf                            # whole groups masked
+    x, xd = _rounded(x, "f32")
+    for bias in (None, np.where(np.arange(E) % 3 == 0, 0.25, 0.0).astype(np.float32),
+                 np.where(np.arange(E) % 5 == 0, -inf, 0.0).astype(np.float32),
+                 np.where(np.arange(E) == 9, nan, np.where(np.arange(E) == 11, inf, 0.0)).astype(np.float32)):
+        for renorm in (False, True):
+            _check_route(x, xd, 6, scores=scores, bias=bias, groups=groups, top_groups=top_groups, group_best=2,
+                         renorm=renorm)
+
+
+def test_route_strided_logits_and_nothing():
+    torch, q = _t(), qz()
+    base = torch.randn((30, 100), device="cuda")
+    for x in (base[:, 3:67], base[::2, 1:98], base.to(torch.bfloat16)[:, 5:69], base[4:5, :64]):
+        _check_route(x.float().cpu().numpy(), x, 4)
+    ids, w = q.qz_route(torch.empty((0, 64), device="cuda"), 4)
+    assert ids.shape == (0, 4) and w.shape == (0, 4)
+    big = torch.randn((40000, 8), device="cuda")           # more tokens than a grid's second dimension
+    _check_route(big.cpu().numpy(), big, 2)
+
+
+# ------------------------------------------------------------------------------- expert layer
+def _layer(rng, E, d, f, zeroed):
+    def rows(n, cols):
+        z = rng.integers(100, 156, (E, n)).astype(np.uint8) if zeroed else None
+        q = np.clip(np.rint(40 * rng.standard_normal((E, n, cols))), -128, 127).astype(np.int8)
+        return q, (np.exp(0.3 * rng.standard_normal((E, n))) * 0.02 / np.sqrt(cols)).astype(np.float32), z
+    return rows(2 * f, d), rows(d, f)
+
+
+def _on_device(m):
+    q, s, z = m
+    E, n, cols = q.shape
+    return to_dev(i8.padded(q.reshape(E * n, cols)).reshape(E, n, -1)), to_dev(s), None if z is None else to_dev(z)
+
+
+def _run_layer(xd, ids, w, gu, dn, **kw):
+    (gc, gs, gz), (dc, ds, dz) = _on_device(gu), _on_device(dn)
+    return qz().qz_i8_moe(xd, ids, w, gc, gs, dc, ds, gu_zeros=gz, dn_zeros=dz, **kw)
+
+
+def _check_layer(x, xd, ids, w, gu, dn, f):
+    y, slack = i8.moe(x, ids, w, gu, dn, f)
+    got = _run_layer(xd, to_dev(ids), to_dev(w), gu, dn)
+    assert got.dtype == _t().bfloat16
+    # slack: hidden codes next to a half and the roundings of h; the sum in 32 bits over k terms of
+    # three roundings each; the rounding to bf16
+    e = 2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(y) + slack * (1 + 2.0 ** -8)
+    bad = np.abs(_host(got) - y) > e
+    assert not bad.any(), (np.argwhere(bad)[:4], _host(got)[bad][:4], y[bad][:4], e[bad][:4])
+    return got
+
+
+LAYERS = [  # n, E, k, d, f, zeroed
+    (1, 8, 2, 64, 32, False), (1, 128, 8, 512, 96, False), (3, 4, 4, 200, 70, True), (7, 8, 2, 256, 520, True),
+    (48, 64, 6, 512, 176, False), (17, 1, 1, 128, 128, False), (40, 5, 3, 96, 33, True), (130, 8, 2, 256, 256, False),
+    (300, 4, 2, 128, 160, True), (33, 60, 4, 1, 1, False), (5, 512, 16, 128, 64, False), (600, 3, 1, 320, 200, False),
+    (2, 16, 16, 4096, 300, False), (4, 8, 2, 640, 2100, True)]
+
+
+@pytest.mark.parametrize("n,E,k,d,f,zeroed", LAYERS)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_moe(n, E, k, d, f, zeroed, dtype):
+    rng = np.random.default_rng([n, E, k])
+    x, xd = _rounded(rng.standard_normal((n, d)), dtype)
+    gu, dn = _layer(rng, E, d, f, zeroed)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(n)]).astype(np.int32)
+    w = rng.random((n, k)).astype(np.float32)
+    _check_layer(x, xd, ids, w, gu, dn, f)
+
+
+@pytest.mark.parametrize("n", [1, 6, 90, 400])
+def test_moe_ids_skipped_repeated_and_crowded(n):
+    rng = np.random.default_rng(n)
+    E, k, d, f = 6, 4, 256, 96
+    x, xd = _rounded(rng.standard_normal((n, d)), "bf16")
+    gu, dn = _layer(rng, E, d, f, n == 6)
+    w = rng.standard_normal((n, k)).astype(np.float32)
+    for ids in (np.full((n, k), 3), rng.integers(-2, E + 3, (n, k)), np.full((n, k), -1), np.full((n, k), 2 ** 31 - 1),
+                np.where(np.arange(n)[:, None] % 3 == 0, E, rng.integers(0, E, (n, k)))):
+        got = _check_layer(x, xd, ids.astype(np.int32), w, gu, dn, f)
+        none = ((ids < 0) | (ids >= E)).all(1)
+        assert not _host(got)[none].any()
+
+
+@pytest.mark.parametrize("n", [2, 70])
+def test_moe_special_rows(n):
+    """A token with a NaN gives NaN, a zero token zeros, and the others are as without them."""
+    rng = np.random.default_rng(n)
+    E, k, d, f = 5, 2, 128, 64
+    x = rng.standard_normal((n, d))
+    gu, dn = _layer(rng, E, d, f, False)
+    ids = rng.integers(0, E, (n, k)).astype(np.int32)
+    w = rng.random((n, k)).astype(np.float32)
+    clean = _host(_run_layer(_rounded(x, "f32")[1], to_dev(ids), to_dev(w), gu, dn))
+    x[0], x[1] = 0, np.nan
+    got = _host(_run_layer(_rounded(x, "f32")[1], to_dev(ids), to_dev(w), gu, dn))
+    assert not got[0].any() and np.isnan(got[1]).all()
+    np.testing.assert_array_equal(got[2:], clean[2:])
+
+
+def test_moe_of_no_tokens():
+    rng = np.random.default_rng(0)
+    gu, dn = _layer(rng, 2, 64, 32, False)
+    t = _t()
+    y = _run_layer(t.empty((0, 64), device="cuda"), t.empty((0, 2), dtype=t.int32, device="cuda"),
+                   t.empty((0, 2), device="cuda"), gu, dn)
+    assert y.shape == (0, 64)
+
+
+# ---------------------------------------------------------------------------- used together
+def test_solvers_codes_through_the_products():
+    """8-bit codes of the solvers, one grid a channel, as they are: pack, multiply, and back."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(4)
+    W = (0.02 * rng.standard_normal((96, 256))).astype(np.float32)
+    X = rng.standard_normal((600, 256)).astype(np.float32)
+    Wd, Xd = to_dev(W), to_dev(X)
+    codes, scales, zeros = q.qz_rtn(Wd, 8, 256)
+    packed = q.qz_i8_pack(codes)
+    assert torch.equal(q.qz_i8_unpack(packed, 256), codes)
+    value = to_host(scales).astype(np.float64) * (to_host(codes).astype(np.float64) - to_host(zeros).astype(np.float64))
+    xq, sx = i8.quantize(X)
+    y = (xq.astype(np.float64) * sx[:, None]) @ value.T
+    got = q.qz_i8_linear(Xd, packed, scales[:, 0], zeros=zeros[:, 0], out_dtype=torch.float32)
+    e = _bound(xq, sx, (to_host(codes).astype(np.int64) - 128).astype(np.int8), to_host(scales)[:, 0],
+               to_host(zeros)[:, 0], None, "f32", y)
+    # this reference multiplies values, not integers: each of 256 products and sums rounds in 64 bits, so
+    # where the integers cancel to zero it is off by up to 512 of 2^-53 of the products' sizes
+    e += 2.0 ** -44 * (np.abs(xq * sx[:, None].astype(np.float64)) @ np.abs(value).T)
+    assert (np.abs(_host(got) - y) <= e).all()
+    # a symmetric matrix judged by the layer objective: f = 1/2 sum (q - w) H (q - w)
+    H = (X.T.astype(np.float64) @ X + 10 * np.eye(256)).astype(np.float32)
+    c, s, v = q.qz_i8_quantize(Wd, values=True)
+    f = q.qz_objective(to_dev(H), Wd, q.qz_i8_unpack(c, 256), s[:, None].contiguous(),
+                       torch.full((96, 1), 128, dtype=torch.uint8, device="cuda"), 256)
+    D = _host(v) - W
+    want = 0.5 * np.einsum("ri,ij,rj->", D, H.astype(np.float64), D)
+    assert abs(float(f) - want) <= 1e-4 * want
+
+
+def test_a_block_of_them():
+    """One quantisation for two projections, and logits, routing and the expert layer behind them."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(5)
+    n, d, E, k, f = 37, 256, 16, 4, 96
+    x, xd = _rounded(rng.standard_normal((n, d)), "bf16")
+    c, s, total = q.qz_i8_quantize(xd, sums=True)
+    xq, sx = i8.quantize(x)
+    for d_o, zeroed in ((d, False), (64, True)):
+        wq, sw = _stored(rng, d_o, d), np.full(d_o, 0.001, np.float32)
+        z = rng.integers(0, 256, d_o).astype(np.uint8) if zeroed else None
+        y = q.qz_i8_matmul(c, s, to_dev(i8.padded(wq)), to_dev(sw), d, zeros=None if z is None else to_dev(z),
+                           xsums=total, out_dtype=torch.float32)
+        want = i8.product(xq, sx, wq, sw, z)
+        assert (np.abs(_host(y) - want) <= _bound(xq, sx, wq, sw, z, None, "f32", want)).all()
+    router = to_dev((rng.standard_normal((E, d)) / 16).astype(np.float32))
+    logits = xd.float() @ router.T
+    ids, w = q.qz_route(logits, k, scores="sigmoid", groups=4, top_groups=2, group_best=2, scale=2.5)
+    want_ids, want_w = i8.route(logits.cpu().numpy(), k, "sigmoid", None, 4, 2, 2, True, 2.5)
+    _same(ids, want_ids)
+    gu, dn = _layer(rng, E, d, f, False)
+    got = _run_layer(xd, ids, w, gu, dn)
+    y, slack = i8.moe(x, want_ids, want_w.astype(np.float32), gu, dn, f)
+    assert (np.abs(_host(got) - y) <= 2.0 ** -8 * (1 + 2.0 ** -8) * np.abs(y) + slack * (1 + 2.0 ** -8)).all()
+
+
+# ------------------------------------------------------------------- streams, graphs, workspaces
+def _program(n, seed):
+    """A run of the operators on inputs of its own: (callable, its outputs' expected values by an eager run)."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(seed)
+    d, E, k, f = 384, 8, 2, 160
+    xd = _rounded(rng.standard_normal((n, d)), "bf16")[1]
+    wq, sw = to_dev(i8.padded(_stored(rng, 200, d))), to_dev(np.full(200, 0.01, np.float32))
+    z = to_dev(rng.integers(0, 256, 200).astype(np.uint8))
+    logits = to_dev(rng.standard_normal((n, E)).astype(np.float32))
+    (gc, gs, _), (dc, ds, _) = (_on_device(m) for m in _layer(rng, E, d, f, False))
+
+    def run():
+        ids, w = q.qz_route(logits, k)
+        c, s, t, v = q.qz_i8_quantize(xd, sums=True, values=True)
+        return [ids, w, c, s, t, v, q.qz_i8_linear(xd, wq, sw, zeros=z),
+                q.qz_i8_matmul(c, s, wq, sw, d, zeros=z, xsums=t, out_dtype=torch.float32),
+                q.qz_i8_moe(xd, ids, w, gc, gs, dc, ds)]
+    return run, xd, logits
+
+
+@pytest.mark.parametrize("n", [1, 20, 300])
+def test_graph_replays(n):
+    """Two captured runs of the operators, replayed in turn on new inputs with eager calls between."""
+    torch = _t()
+    both = [_program(n, seed) for seed in (1, 2)]
+    graphs = []
+    for run, _, _ in both:
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = run()
+        graphs.append((g, held))
+    for turn in range(3):
+        for (run, xd, logits), (g, held) in zip(both, graphs):
+            xd.copy_(torch.randn(xd.shape, device="cuda"))
+            logits.copy_(torch.randn(logits.shape, device="cuda"))
+            want = [t.clone() for t in run()]
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(held, want):
+                assert torch.equal(a, b), turn
+            run()
+
+
+@pytest.mark.parametrize("n", [1, 20, 300])
+def test_two_streams_and_repeated_calls(n):
+    torch = _t()
+    (a, _, _), (b, _, _) = _program(n, 3), _program(n, 4)
+    want_a, want_b = a(), b()
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            got_a = a()
+        with torch.cuda.stream(s2):
+            got_b = b()
+        torch.cuda.synchronize()
+        for x, y in zip(got_a + got_b, want_a + want_b):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("n,d_i,d_o", [(1, 200, 40), (13, 2048, 96), (70, 640, 300), (300, 4096, 128), (520, 512, 520)])
+def test_workspaces_of_exactly_the_queried_size(n, d_i, d_o):
+    """Any bytes in the workspace, guards around it and around the results."""
+    q, torch = qz(), _t()
+    rng = np.random.default_rng(n)
+    xd = _rounded(rng.standard_normal((n, d_i)), "bf16")[1]
+    wq, sw = to_dev(i8.padded(_stored(rng, d_o, d_i))), to_dev(np.full(d_o, 0.01, np.float32))
+    gu, dn = _layer(rng, 4, d_i, 72, False)
+    (gc, gs, _), (dc, ds, _) = _on_device(gu), _on_device(dn)
+    ids = to_dev(rng.integers(0, 4, (n, 2)).astype(np.int32))
+    w = to_dev(rng.random((n, 2)).astype(np.float32))
+    c, s = q.qz_i8_quantize(xd)
+    calls = [(q.qz_i8_linear_workspace(n, d_o, d_i), lambda ws, y: q.qz_i8_linear(xd, wq, sw, out=y, ws=ws)),
+             (q.qz_i8_matmul_workspace(n, d_o, d_i), lambda ws, y: q.qz_i8_matmul(c, s, wq, sw, d_i, out=y, ws=ws)),
+             (q.qz_i8_moe_workspace(n, d_i, 72, 4, 2), lambda ws, y: q.qz_i8_moe(xd, ids, w, gc, gs, dc, ds, ws=ws))]
+    for need, call in calls:
+        want = call(None, torch.empty((n, d_o), device="cuda"))
+        for fill in (0, 255, 0x7f):
+            hold = torch.full((need + 1024,), fill, dtype=torch.uint8, device="cuda")
+            hold[:512] = 0x5a
+            hold[512 + need:] = 0x5a
+            ys = torch.full((n + 2, d_o), 3.0, device="cuda")
+            got = call(hold[512:512 + need] if need else None, ys[1:n + 1])
+            assert torch.equal(got, want)
+            assert (hold[:512] == 0x5a).all() and (hold[512 + need:] == 0x5a).all()
+            assert (ys[0] == 3).all() and (ys[n + 1] == 3).all()
+
+
+def test_timing_kinds():
+    q = qz()
+    q.qz_timing_enable(True)
+    try:
+        _program(3, 9)[0]()
+        _t().cuda.synchronize()
+        got = q.qz_timing_read()
+    finally:
+        q.qz_timing_enable(False)
+    assert {"i8_quantize", "i8_product", "route", "i8_moe"} <= set(got)
