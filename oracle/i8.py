@@ -24,7 +24,7 @@ def quantize(x, colf=None):
     with np.errstate(all="ignore"):
         if colf is not None:
             v = v * np.asarray(colf, np.float32)
-        s = (np.abs(v).max(1) / np.float32(127)).astype(np.float32)
+        s = np.abs(v).max(1) * (np.float32(1) / np.float32(127))
         # 24-bit quotients are 2^-25 or more from a half that they do not equal: 64 bits decide
         q = v.astype(np.float64) / s.astype(np.float64)[:, None]
     finite = np.isfinite(v).all(1)

@@ -1,0 +1,70 @@
+// Products of 8-bit integer rows, shared by the tile kernels and the few-token kernels: where a
+// workgroup's rows lie, and how an integer sum becomes a result.
+#pragma once
+
+#include "qz_internal.h"
+
+namespace qz {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+enum Form { kPlain, kGateUp, kDown };
+
+// An integer sum with its zero point, scales and bias.
+__device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, float sw, float bias) {
+  return fmaf(static_cast<float>(a - shift * xsum) * sx, sw, bias);
+}
+
+__device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(a)) |
+         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
+}
+
+// Expert and slots of the token tile `index` of `bn` slots, the experts' tiles in their order; false
+// past the last one.  Every lane of a wavefront has eight neighbouring experts.
+__device__ __forceinline__ bool find_tile(const I8Product& p, int index, int bn, int* expert, int* first,
+                                          int* end) {
+  const int lane = threadIdx.x & 63;
+  int at[9], tiles = 0;
+#pragma unroll
+  for (int i = 0; i <= 8; ++i) {
+    const int e = 8 * lane + i;
+    at[i] = p.offsets[e < p.E ? e : p.E];
+    if (i) tiles += (at[i] - at[i - 1] + bn - 1) / bn;
+  }
+  int upto = tiles;
+  for (int o = 1; o < 64; o *= 2) {
+    const int v = __shfl_up(upto, o);
+    if (lane >= o) upto += v;
+  }
+  const uint64_t who = __ballot(index < upto);
+  if (!who) return false;
+  const int src = __builtin_ctzll(who);
+  int left = index - (upto - tiles), e = 0, a = 0, b = 0;
+#pragma unroll
+  for (int i = 1; i <= 8; ++i) {
+    const int n = (at[i] - at[i - 1] + bn - 1) / bn;
+    if (left >= 0 && left < n) {
+      e = 8 * lane + i - 1;
+      a = at[i - 1] + left * bn;
+      b = at[i];
+    }
+    left -= n;
+  }
+  *expert = __builtin_amdgcn_readlane(e, src);
+  *first = __builtin_amdgcn_readlane(a, src);
+  const int stop = __builtin_amdgcn_readlane(b, src);
+  *end = *first + bn < stop ? *first + bn : stop;
+  return true;
+}
+
+// Token tiles of an expert layer, at most.
+inline int64_t most_tiles(const I8Product& p, int bn) {
+  return p.n / bn + (p.n < p.E ? p.n : p.E);
+}
+
+}  // namespace qz

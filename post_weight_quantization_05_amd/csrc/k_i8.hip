@@ -41,7 +41,7 @@ __global__ __launch_bounds__(256) void i8_quantize_kernel(
   __syncthreads();
   top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
   const bool finite = top < 0x7f800000u;
-  const float s = finite ? __uint_as_float(top) / 127.f : __uint_as_float(0x7fc00000u);
+  const float s = finite ? __uint_as_float(top) * (1.f / 127.f) : __uint_as_float(0x7fc00000u);
   // small rows are moved up by a power of two, exactly, so that 1 / s is a number
   const float up = s < 0x1p-60f ? 0x1p80f : 1.f, su = s * up, r = 1.f / su;
   int sum = 0;

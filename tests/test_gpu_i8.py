@@ -88,7 +88,7 @@ def test_quantize_every_quotient_near_a_half():
     rows = []
     for _ in range(64):
         top = np.float32(np.exp(3 * rng.standard_normal()))
-        s = np.float64(np.float32(top / np.float32(127)))
+        s = np.float64(top * (np.float32(1) / np.float32(127)))
         mid = ((np.arange(-126, 126) + 0.5) * s).astype(np.float32)
         rows.append(np.concatenate([[top], mid, np.nextafter(mid, np.float32(np.inf)), np.nextafter(mid, np.float32(-np.inf))]))
     x = np.stack(rows).astype(np.float32)
