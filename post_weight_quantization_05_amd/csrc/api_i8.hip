@@ -54,6 +54,14 @@ int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i, const in
   return QZ_OK;
 }
 
+// Few tokens: one launch that quantizes them itself and needs no workspace.
+bool i8_by_rows(int64_t n, int64_t P) { return n <= 4 && i8_rows_fits(n, P); }
+
+// Few pairs of an expert layer, each with its expert's rows alone.
+bool moe_by_rows(int64_t n, int64_t d, int64_t f, int k) {
+  return n * k <= 64 && i8_rows_fits(1, i8_pitch(d)) && i8_rows_fits(k, i8_pitch(f));
+}
+
 // X quantized, and the product's own workspace.
 struct LinearWs {
   int8_t* codes;
@@ -64,7 +72,8 @@ struct LinearWs {
 };
 LinearWs linear_ws(void* base, int64_t n, int64_t d_o, int64_t d_i) {
   Carver c(base);
-  LinearWs w;
+  LinearWs w{};
+  if (i8_by_rows(n, i8_pitch(d_i))) return w;
   w.codes = c.take<int8_t>(static_cast<size_t>(n) * i8_pitch(d_i));
   w.scales = c.take<float>(n);
   w.sums = c.take<int32_t>(n);
@@ -82,14 +91,18 @@ struct MoeWs {
 };
 MoeWs moe_ws(void* base, int64_t n, int64_t d, int64_t f, int E, int k) {
   Carver c(base);
-  MoeWs w;
+  MoeWs w{};
   const size_t pairs = static_cast<size_t>(n) * k;
+  w.h = c.take<float>(pairs * round_up(f, 4));
+  if (moe_by_rows(n, d, f, k)) {
+    w.bytes = c.used;
+    return w;
+  }
   w.xcodes = c.take<int8_t>(static_cast<size_t>(n) * i8_pitch(d));
   w.xscales = c.take<float>(n);
   w.xsums = c.take<int32_t>(n);
   w.offsets = c.take<int32_t>(E + 1);
   w.order = c.take<int32_t>(pairs);
-  w.h = c.take<float>(pairs * f);
   w.hcodes = c.take<int8_t>(pairs * i8_pitch(f));
   w.hscales = c.take<float>(pairs);
   w.hsums = c.take<int32_t>(pairs);
@@ -184,7 +197,7 @@ int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsum
   p.yt = yt;
   p.ldy = ldy;
   p.partial = static_cast<int32_t*>(ws);
-  return launch_i8_product(p, stream);
+  return i8_by_rows(n, p.P) ? launch_i8_rows(p, stream) : launch_i8_product(p, stream);
 }
 
 size_t qz_i8_linear_workspace(int64_t n, int64_t d_o, int64_t d_i) {
@@ -206,7 +219,6 @@ int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float*
   QZ_TRY(check_ws("i8_linear", ws, ws_bytes, w.bytes));
   set_error("");
   ScopedTimer tm(K_I8_PRODUCT, stream);
-  QZ_TRY(launch_i8_quantize(X, xt, n, d_i, ldx, colf, w.codes, w.scales, zeros ? w.sums : nullptr, nullptr, stream));
   I8Product p{};
   p.n = n;
   p.d_o = d_o;
@@ -222,6 +234,15 @@ int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float*
   p.yt = yt;
   p.ldy = ldy;
   p.partial = reinterpret_cast<int32_t*>(w.product);
+  if (i8_by_rows(n, p.P)) {
+    p.raw = X;
+    p.rt = xt;
+    p.ldraw = ldx;
+    p.cols = d_i;
+    p.colf = colf;
+    return launch_i8_rows(p, stream);
+  }
+  QZ_TRY(launch_i8_quantize(X, xt, n, d_i, ldx, colf, w.codes, w.scales, zeros ? w.sums : nullptr, nullptr, stream));
   return launch_i8_product(p, stream);
 }
 
@@ -276,8 +297,6 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   set_error("");
   ScopedTimer tm(K_I8_MOE, stream);
   const int64_t pairs = n * top_k;
-  QZ_TRY(launch_i8_quantize(X, xt, n, d, ldx, nullptr, w.xcodes, w.xscales, w.xsums, nullptr, stream));
-  QZ_TRY(launch_i8_group(ids, pairs, n_experts, w.offsets, w.order, stream));
   I8Product p{};
   p.n = pairs;
   p.offsets = w.offsets;
@@ -285,7 +304,6 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   p.pair_weight = weights;
   p.E = n_experts;
   p.k = top_k;
-  p.yt = QZ_F32;
   p.d_o = f;
   p.P = i8_pitch(d);
   p.X = w.xcodes;
@@ -295,9 +313,25 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   p.sw = gu_scales;
   p.zeros = gu_zeros;
   p.Y = w.h;
-  p.ldy = f;
-  QZ_TRY(launch_i8_gate_up(p, stream));
-  QZ_TRY(launch_i8_quantize(w.h, QZ_F32, pairs, f, f, nullptr, w.hcodes, w.hscales, w.hsums, nullptr, stream));
+  p.yt = QZ_F32;
+  p.ldy = round_up(f, 4);
+  if (moe_by_rows(n, d, f, top_k)) {
+    p.ids = ids;
+    p.raw = X;
+    p.rt = xt;
+    p.ldraw = ldx;
+    p.cols = d;
+    QZ_TRY(launch_i8_rows_gate_up(p, stream));
+    p.raw = w.h;
+    p.rt = QZ_F32;
+    p.ldraw = p.ldy;
+    p.cols = f;
+  } else {
+    QZ_TRY(launch_i8_quantize(X, xt, n, d, ldx, nullptr, w.xcodes, w.xscales, w.xsums, nullptr, stream));
+    QZ_TRY(launch_i8_group(ids, pairs, n_experts, w.offsets, w.order, stream));
+    QZ_TRY(launch_i8_gate_up(p, stream));
+    QZ_TRY(launch_i8_quantize(w.h, QZ_F32, pairs, f, p.ldy, nullptr, w.hcodes, w.hscales, w.hsums, nullptr, stream));
+  }
   p.d_o = d;
   p.P = i8_pitch(f);
   p.X = w.hcodes;
@@ -306,6 +340,11 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   p.W = dn_codes;
   p.sw = dn_scales;
   p.zeros = dn_zeros;
+  if (moe_by_rows(n, d, f, top_k)) {
+    p.Y = Y;
+    p.ldy = d;
+    return launch_i8_rows_down(p, n, stream);
+  }
   p.Y = w.y;
   p.ldy = d;
   QZ_TRY(launch_i8_down(p, stream));

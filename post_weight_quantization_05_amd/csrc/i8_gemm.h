@@ -2,7 +2,7 @@
 // workgroup's rows lie, and how an integer sum becomes a result.
 #pragma once
 
-#include "qz_internal.h"
+#include "i8_quant.h"
 
 namespace qz {
 
@@ -18,11 +18,6 @@ __device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, fl
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
-
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(a)) |
-         static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(b))) << 16;
-}
 
 // Expert and slots of the token tile `index` of `bn` slots, the experts' tiles in their order; false
 // past the last one.  Every lane of a wavefront has eight neighbouring experts.

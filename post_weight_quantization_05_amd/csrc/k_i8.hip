@@ -2,67 +2,92 @@
 // to and from it.
 #include <type_traits>
 
-#include "qz_internal.h"
+#include "i8_quant.h"
 
 namespace qz {
 
 namespace {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-// The whole number nearest to v / s (the quotient itself), ties to the even one, within +-127;
-// r = 1 / s to 32 bits, so q is off by one at most.  q s - v is exact in one fused step: it is a
-// multiple of both numbers' last bits' smaller one and at most s / 2 or so.
-__device__ __forceinline__ float nearest_code(float v, float s, float r) {
-  float q = fminf(fmaxf(__builtin_rintf(v * r), -127.f), 127.f);
-  const float rest = fmaf(-q, s, v), half = 0.5f * s;
-  if (fabsf(rest) > half || (fabsf(rest) == half && (static_cast<int>(q) & 1)))
-    q += rest > 0.f ? 1.f : -1.f;
-  return fminf(fmaxf(q, -127.f), 127.f);
-}
-
-template <int WT>
-__global__ __launch_bounds__(256) void i8_quantize_kernel(
-    const void* __restrict__ X, int64_t cols, int64_t ldx, const float* __restrict__ colf,
-    int8_t* __restrict__ codes, float* __restrict__ scales, int32_t* __restrict__ sums,
-    void* __restrict__ values) {
-  __shared__ uint32_t tops[4];
-  __shared__ int parts[4];
-  const int64_t row = blockIdx.x, P = i8_pitch(cols);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  auto value = [&](int64_t c) {
-    const float x = load_w<WT>(X, row * ldx + c);
-    return colf ? x * colf[c] : x;
-  };
-  uint32_t top = 0;   // magnitudes compare as integers, and a NaN is above every number
-  for (int64_t c = threadIdx.x; c < cols; c += 256) top = max(top, __float_as_uint(value(c)) & 0x7fffffffu);
-  for (int o = 32; o; o >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(top, o)));
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
-  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
-  const bool finite = top < 0x7f800000u;
-  const float s = finite ? __uint_as_float(top) * (1.f / 127.f) : __uint_as_float(0x7fc00000u);
-  // small rows are moved up by a power of two, exactly, so that 1 / s is a number
-  const float up = s < 0x1p-60f ? 0x1p80f : 1.f, su = s * up, r = 1.f / su;
+// TPR threads a row, CH chunks of eight elements each, which stay in registers between the row's
+// maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier.
+//
+// Bound by HBM.
+template <int WT, bool VEC, int TPR, int CH>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
+    const void* __restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
+    const float* __restrict__ colf, int8_t* __restrict__ codes, float* __restrict__ scales,
+    int32_t* __restrict__ sums, void* __restrict__ values) {
+  constexpr int kWaves = TPR / 64;
+  __shared__ uint32_t tops[kWaves];
+  __shared__ int parts[kWaves];
+  const int64_t row = TPR == 64 ? blockIdx.x * (int64_t)4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (TPR == 64 && row >= rows) return;
+  const int t = threadIdx.x % TPR, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t P = i8_pitch(cols);
+  float v[CH][8];
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) load8<WT, VEC>(X, row * ldx + (c * TPR + t) * 8, cols - (c * TPR + t) * 8, v[c]);
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    if (colf) {
+      float f[8];
+      load8<QZ_F32, VEC>(colf, (c * TPR + t) * 8, cols - (c * TPR + t) * 8, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[c][i] *= f[i];
+    }
+    top = top8(v[c], top);
+  }
+  top = wave_top(top);
+  if constexpr (kWaves > 1) {
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
+    top = wave_top(lane < kWaves ? tops[lane] : 0u);
+  }
+  const RowScale sc = row_scale(top);
   int sum = 0;
-  for (int64_t c = threadIdx.x; c < P; c += 256) {
-    const float q = finite && s > 0.f && c < cols ? nearest_code(value(c) * up, su, r) : 0.f;
-    codes[row * P + c] = static_cast<int8_t>(static_cast<int>(q));
-    sum += static_cast<int>(q);
-    if (values && c < cols) {
-      if constexpr (WT == QZ_BF16)
-        static_cast<uint16_t*>(values)[row * cols + c] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(q * s));
-      else
-        static_cast<float*>(values)[row * cols + c] = q * s;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int64_t at = (c * TPR + t) * 8;
+    if (at >= P) continue;
+    float q[8];
+    const uint2 w = codes8(v[c], sc, q);
+    *reinterpret_cast<uint2*>(codes + row * P + at) = w;
+    sum = add_codes(w.x, add_codes(w.y, sum));
+    if (!values || at >= cols) continue;
+    const int64_t o = row * cols + at;
+    if constexpr (VEC) {
+      if constexpr (WT == QZ_BF16) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[i] = bf16_pair(q[2 * i] * sc.s, q[2 * i + 1] * sc.s);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(values) + o) = make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(values) + o);
+        f[0] = make_float4(q[0] * sc.s, q[1] * sc.s, q[2] * sc.s, q[3] * sc.s);
+        f[1] = make_float4(q[4] * sc.s, q[5] * sc.s, q[6] * sc.s, q[7] * sc.s);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (at + i < cols) {
+          if constexpr (WT == QZ_BF16)
+            static_cast<uint16_t*>(values)[o + i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(q[i] * sc.s));
+          else
+            static_cast<float*>(values)[o + i] = q[i] * sc.s;
+        }
     }
   }
-  for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-  if (lane == 0) parts[wave] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    scales[row] = s;
-    if (sums) sums[row] = parts[0] + parts[1] + parts[2] + parts[3];
+  if (sums) {
+    sum = wave_sum(sum);
+    if constexpr (kWaves > 1) {
+      if (lane == 0) parts[wave] = sum;
+      __syncthreads();
+      sum = wave_sum(lane < kWaves ? parts[lane] : 0);
+    }
+    if (t == 0) sums[row] = sum;
   }
+  if (t == 0) scales[row] = sc.s;
 }
 
 __global__ __launch_bounds__(256) void i8_pack_kernel(const uint8_t* __restrict__ in, int64_t rows,
@@ -94,12 +119,33 @@ int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_
                        const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
                        hipStream_t s) {
   if (rows == 0) return QZ_OK;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, X, cols, ldx, colf,
-                       codes, scales, sums, values);
+  auto go = [&](auto kernel, int tpr) {
+    const int64_t groups = tpr == 64 ? ceil_div(rows, 4) : rows;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(tpr < 256 ? 256 : tpr), 0, s, X, rows,
+                       cols, ldx, colf, codes, scales, sums, values);
     return check_launch("i8_quantize");
   };
-  return xt == QZ_BF16 ? go(i8_quantize_kernel<QZ_BF16>) : go(i8_quantize_kernel<QZ_F32>);
+  auto by_size = [&](auto type, auto vec) {
+    constexpr int WT = decltype(type)::value;
+    constexpr bool VEC = decltype(vec)::value;
+    if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, 64, 1>, 64);
+    if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, 64, 2>, 64);
+    if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, 64, 4>, 64);
+    if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, 256, 2>, 256);
+    if (cols <= 8192) return go(i8_quantize_kernel<WT, VEC, 256, 4>, 256);
+    if (cols <= 16384) return go(i8_quantize_kernel<WT, VEC, 1024, 2>, 1024);
+    if (cols <= 32768) return go(i8_quantize_kernel<WT, VEC, 1024, 4>, 1024);
+    return go(i8_quantize_kernel<WT, VEC, 1024, 8>, 1024);
+  };
+  auto by_type = [&](auto type) {
+    const size_t size = decltype(type)::value == QZ_BF16 ? 2 : 4;
+    auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    return cols % 8 == 0 && ldx * size % 16 == 0 && on16(X) && on16(values) && on16(colf)
+               ? by_size(type, std::true_type{})
+               : by_size(type, std::false_type{});
+  };
+  return xt == QZ_BF16 ? by_type(std::integral_constant<int, QZ_BF16>{})
+                       : by_type(std::integral_constant<int, QZ_F32>{});
 }
 
 int launch_i8_pack(const uint8_t* codes, int64_t rows, int64_t cols, int8_t* out, hipStream_t s) {

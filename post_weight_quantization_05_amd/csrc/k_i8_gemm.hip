@@ -458,8 +458,8 @@ int launch(const I8Product& p, hipStream_t s) {
                        dim3(64), 0, s, p);
     return check_launch("i8_product");
   }
-  if (FORM == kPlain && p.n <= 512) return launch_tile<FORM, TileI8<2, 2, 2, 2>>(p, 1, s);
-  return launch_tile<FORM, TileI8<2, 2, 4, 4>>(p, 1, s);
+  if (FORM != kPlain || p.n <= 2048) return launch_tile<FORM, TileI8<2, 2, 2, 2>>(p, 1, s);
+  return launch_tile<FORM, TileI8<2, 4, 4, 2>>(p, 1, s);
 }
 
 }  // namespace

@@ -324,6 +324,10 @@ struct I8Product {
   const int32_t* offsets; const int32_t* order; // of an expert layer
   const float* pair_weight;                     // [pairs]
   int E, k;
+  // Few-token kernels (k_i8_rows.hip): X as numbers, quantized on the way (raw; else null and X as
+  // codes), and the pairs' experts in place of slots.
+  const void* raw; int rt; int64_t ldraw, cols; const float* colf;
+  const int32_t* ids;
 };
 size_t i8_product_ws(int64_t n, int64_t d_o, int64_t P);
 int launch_i8_product(const I8Product& p, hipStream_t s);
@@ -331,6 +335,14 @@ int launch_i8_product(const I8Product& p, hipStream_t s);
 int launch_i8_gate_up(const I8Product& p, hipStream_t s);
 // Y[pair] = pair_weight[pair] * product, fp32 [pairs x ldy]
 int launch_i8_down(const I8Product& p, hipStream_t s);
+// rows of X that the few-token kernels can hold at once
+bool i8_rows_fits(int64_t rows, int64_t P);
+// Y = X W^T for n <= 4
+int launch_i8_rows(const I8Product& p, hipStream_t s);
+// h[pair] = silu(gate) up for n pairs (those whose id is an expert), X by token
+int launch_i8_rows_gate_up(const I8Product& p, hipStream_t s);
+// Y[token] bf16 = the weighted sum over its pairs, X by pair
+int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s);
 int launch_i8_group(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* order,
                     hipStream_t s);
 int launch_i8_sum(const float* y_pairs, int64_t ldp, const int32_t* ids, int64_t n, int64_t d,
