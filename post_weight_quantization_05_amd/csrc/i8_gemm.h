@@ -2,6 +2,8 @@
 // workgroup's rows lie, and how an integer sum becomes a result.
 #pragma once
 
+#include <atomic>
+
 #include "i8_quant.h"
 
 namespace qz {
@@ -56,6 +58,23 @@ __device__ __forceinline__ bool find_tile(const I8Product& p, int index, int bn,
   *end = *first + bn < stop ? *first + bn : stop;
   return true;
 }
+
+// Lets a kernel use its dynamic LDS, once a device.
+class LdsAllowance {
+ public:
+  int ask(const void* kernel, int bytes) {
+    int dev = 0;
+    QZ_HIP(hipGetDevice(&dev));
+    if (dev > 63 || !(allowed_.load(std::memory_order_relaxed) >> dev & 1)) {
+      QZ_HIP(hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+      if (dev <= 63) allowed_.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
+    }
+    return QZ_OK;
+  }
+
+ private:
+  std::atomic<uint64_t> allowed_{0};
+};
 
 // Token tiles of an expert layer, at most.
 inline int64_t most_tiles(const I8Product& p, int bn) {

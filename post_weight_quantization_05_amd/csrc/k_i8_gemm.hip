@@ -1,6 +1,5 @@
 // Products of 8-bit integer rows: Y = X W^T with a scale per row of X and of W, plain or grouped by
 // expert.
-#include <atomic>
 #include <type_traits>
 
 #include "i8_gemm.h"
@@ -378,14 +377,8 @@ __global__ __launch_bounds__(256) void i8_join_kernel(const I8Product p, int spl
 template <Form FORM, class T>
 int launch_tile(const I8Product& p, int splits, hipStream_t s) {
   const auto kernel = i8_tile_kernel<FORM, T>;
-  static std::atomic<uint64_t> allowed{0};   // devices on which the kernel may use its LDS
-  int dev = 0;
-  QZ_HIP(hipGetDevice(&dev));
-  if (dev > 63 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
-    QZ_HIP(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                               hipFuncAttributeMaxDynamicSharedMemorySize, T::kShared));
-    if (dev <= 63) allowed.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
-  }
+  static LdsAllowance allowed;
+  QZ_TRY(allowed.ask(reinterpret_cast<const void*>(kernel), T::kShared));
   const int64_t tw = ceil_div(p.d_o, FORM == kGateUp ? T::BM / 2 : T::BM);
   const int64_t tx = FORM == kPlain ? ceil_div(p.n, T::BN) : most_tiles(p, T::BN);
   if (tw * tx > 0x7fffffff) return fail(QZ_EINVAL, "i8_product: too many tiles");
@@ -402,62 +395,9 @@ int launch_tile(const I8Product& p, int splits, hipStream_t s) {
   return check_launch("i8_join");
 }
 
-// A wavefront per 16 rows of W by 16 rows of X, operands straight from memory.
-template <Form FORM>
-__global__ __launch_bounds__(64) void i8_product_kernel(const I8Product p) {
-  const int lane = threadIdx.x, m = lane & 15, q = lane >> 4;
-  int expert = 0, slot0 = 0, slot_end = 0;
-  if constexpr (FORM != kPlain)
-    if (!find_tile(p, blockIdx.y, 16, &expert, &slot0, &slot_end)) return;
-  const int64_t first = FORM == kPlain ? blockIdx.y * (int64_t)16 : slot0, end = FORM == kPlain ? p.n : slot_end;
-  const int64_t r0 = blockIdx.x * (int64_t)16;
-  const int64_t w_rows = (FORM == kGateUp ? 2 : 1) * p.d_o, base = expert * w_rows;
-  const int64_t wr = r0 + m < p.d_o ? r0 + m : p.d_o - 1;
-  const int64_t slot = first + m < end ? first + m : end - 1;
-  const int64_t pair = FORM == kPlain ? slot : p.order[slot];
-  const int64_t xr = FORM == kGateUp ? pair / p.k : slot;
-  const int8_t* w = p.W + (base + wr) * p.P + 16 * q;
-  const int8_t* u = FORM == kGateUp ? w + p.d_o * p.P : w;
-  const int8_t* x = p.X + xr * p.P + 16 * q;
-  i32x4 acc = {0, 0, 0, 0}, acu = {0, 0, 0, 0};
-  for (int64_t c = 0; c < p.P; c += 64) {
-    const i32x4 xv = *reinterpret_cast<const i32x4*>(x + c);
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4*>(w + c), xv, acc, 0, 0, 0);
-    if constexpr (FORM == kGateUp)
-      acu = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4*>(u + c), xv, acu, 0, 0, 0);
-  }
-  if (first + m >= end) return;
-  const float sx = p.sx[xr];
-  const int xsum = p.zeros ? p.xsum[xr] : 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + 4 * q + i;
-    if (r >= p.d_o) continue;
-    const int shift = p.zeros ? p.zeros[base + r] - 128 : 0;
-    const float v = scaled(acc[i], shift, xsum, sx, p.sw[base + r], FORM == kPlain && p.bias ? p.bias[r] : 0.f);
-    if constexpr (FORM == kPlain) {
-      if (p.yt == QZ_BF16)
-        static_cast<uint16_t*>(p.Y)[slot * p.ldy + r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
-      else
-        static_cast<float*>(p.Y)[slot * p.ldy + r] = v;
-    } else if constexpr (FORM == kGateUp) {
-      const int64_t ru = base + p.d_o + r;
-      const float up = scaled(acu[i], p.zeros ? p.zeros[ru] - 128 : 0, xsum, sx, p.sw[ru], 0.f);
-      static_cast<float*>(p.Y)[slot * p.ldy + r] = silu(v) * up;
-    } else {
-      static_cast<float*>(p.Y)[pair * p.ldy + r] = v * p.pair_weight[pair];
-    }
-  }
-}
-
 template <Form FORM>
 int launch(const I8Product& p, hipStream_t s) {
-  if (p.n <= 64) {
-    const int64_t tiles = FORM == kPlain ? ceil_div(p.n, 16) : most_tiles(p, 16);
-    hipLaunchKernelGGL((i8_product_kernel<FORM>), dim3(static_cast<unsigned>(ceil_div(p.d_o, 16)), static_cast<unsigned>(tiles)),
-                       dim3(64), 0, s, p);
-    return check_launch("i8_product");
-  }
+  if (p.n <= 64) return FORM == kPlain ? launch_i8_few(p, s) : FORM == kGateUp ? launch_i8_few_gate_up(p, s) : launch_i8_few_down(p, s);
   if (FORM != kPlain || p.n <= 2048) return launch_tile<FORM, TileI8<2, 2, 2, 2>>(p, 1, s);
   return launch_tile<FORM, TileI8<2, 4, 4, 2>>(p, 1, s);
 }
