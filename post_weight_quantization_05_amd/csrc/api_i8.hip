@@ -196,7 +196,6 @@ int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsum
   p.Y = Y;
   p.yt = yt;
   p.ldy = ldy;
-  p.partial = static_cast<int32_t*>(ws);
   return i8_by_rows(n, p.P) ? launch_i8_rows(p, stream) : launch_i8_product(p, stream);
 }
 
@@ -233,7 +232,6 @@ int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float*
   p.Y = Y;
   p.yt = yt;
   p.ldy = ldy;
-  p.partial = reinterpret_cast<int32_t*>(w.product);
   if (i8_by_rows(n, p.P)) {
     p.raw = X;
     p.rt = xt;

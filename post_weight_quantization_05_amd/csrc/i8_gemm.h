@@ -14,9 +14,13 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 enum Form { kPlain, kGateUp, kDown };
 
-// An integer sum with its zero point, scales and bias.
+enum class I8Kind;
+int launch_i8_few(I8Kind kind, int form, const I8Product& p, hipStream_t s);
+
+// An integer sum with its zero point, scales and bias.  shift: the zero point less 128; |xsum| < 2^23, so
+// the product takes the 24-bit multiplier.
 __device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, float sw, float bias) {
-  return fmaf(static_cast<float>(a - shift * xsum) * sx, sw, bias);
+  return fmaf(static_cast<float>(a - __mul24(shift, xsum)) * sx, sw, bias);
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }

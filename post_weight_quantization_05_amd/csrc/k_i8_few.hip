@@ -3,6 +3,7 @@
 #include <type_traits>
 
 #include "i8_gemm.h"
+#include "i8_plan.h"
 #include "lds_copy.h"
 
 namespace qz {
@@ -195,13 +196,21 @@ static int launch_few(const I8Product& p, hipStream_t s) {
 }
 
 #ifndef QZ_NO_ENTRY
-int launch_i8_few(const I8Product& p, hipStream_t s) {
-  if (p.n <= 16) return p.d_o <= 8192 ? launch_few<kPlain, FewI8<1, 1, 8, 160>>(p, s) : launch_few<kPlain, FewI8<2, 1, 4, 80>>(p, s);
-  if (p.n <= 32) return p.d_o <= 8192 ? launch_few<kPlain, FewI8<1, 2, 8, 160>>(p, s) : launch_few<kPlain, FewI8<2, 2, 4, 160>>(p, s);
-  return launch_few<kPlain, FewI8<2, 4, 4, 160>>(p, s);
+template <Form FORM>
+static int by_kind(I8Kind kind, const I8Product& p, hipStream_t s) {
+  switch (kind) {
+    case I8Kind::kFew11: if constexpr (FORM != kGateUp) return launch_few<FORM, FewI8<1, 1, 4, 80>>(p, s); break;
+    case I8Kind::kFew21: return launch_few<FORM, FewI8<2, 1, 4, 80>>(p, s);
+    case I8Kind::kFew22: return launch_few<FORM, FewI8<2, 2, 4, 160>>(p, s);
+    case I8Kind::kFew24: return launch_few<FORM, FewI8<2, 4, 4, 160>>(p, s);
+    default: break;
+  }
+  return fail(QZ_EHIP, "i8_few: no kernel");
 }
-int launch_i8_few_gate_up(const I8Product& p, hipStream_t s) { return launch_few<kGateUp, FewI8<2, 1, 4, 80>>(p, s); }
-int launch_i8_few_down(const I8Product& p, hipStream_t s) { return launch_few<kDown, FewI8<2, 1, 4, 80>>(p, s); }
+
+int launch_i8_few(I8Kind kind, int form, const I8Product& p, hipStream_t s) {
+  return form == kPlain ? by_kind<kPlain>(kind, p, s) : form == kGateUp ? by_kind<kGateUp>(kind, p, s) : by_kind<kDown>(kind, p, s);
+}
 #endif
 
 }  // namespace qz

@@ -320,7 +320,6 @@ struct I8Product {
   const int8_t* W; const float* sw; const uint8_t* zeros;   // zeros null: 128
   const float* bias;                            // [d_o] or null
   void* Y; int yt; int64_t ldy;
-  int32_t* partial;                             // split sums, or null
   const int32_t* offsets; const int32_t* order; // of an expert layer
   const float* pair_weight;                     // [pairs]
   int E, k;
@@ -335,10 +334,6 @@ int launch_i8_product(const I8Product& p, hipStream_t s);
 int launch_i8_gate_up(const I8Product& p, hipStream_t s);
 // Y[pair] = pair_weight[pair] * product, fp32 [pairs x ldy]
 int launch_i8_down(const I8Product& p, hipStream_t s);
-// the same for few tokens (k_i8_few.hip)
-int launch_i8_few(const I8Product& p, hipStream_t s);
-int launch_i8_few_gate_up(const I8Product& p, hipStream_t s);
-int launch_i8_few_down(const I8Product& p, hipStream_t s);
 // rows of X that the few-token kernels can hold at once
 bool i8_rows_fits(int64_t rows, int64_t P);
 // Y = X W^T for n <= 4
