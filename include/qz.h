@@ -506,7 +506,7 @@ int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float*
 /* qz_route: the experts of each token and their weights, from the router's logits, in 64 bits.
  *   score = softmax over the row, or with QZ_ROUTE_SIGMOID 1 / (1 + exp(-logit)).
  *   choice = score + bias (bias [n_experts] fp32, nullable: moves the choice, not the weight).
- *   A logit of -inf or NaN (or a choice that is NaN) makes the expert's choice -inf and its score 0.
+ *   A logit of -inf or NaN gives a score of 0 and a choice of -inf; a choice that is NaN counts as -inf.
  *   n_groups groups of n_experts / n_groups neighbours: a group counts as the sum of its group_best
  *     (1 or 2) largest choices above -inf; the top_groups best groups stay.
  *   ids: the top_k experts of those by descending choice; weights: their scores, with
