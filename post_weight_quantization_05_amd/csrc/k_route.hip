@@ -38,10 +38,45 @@ __device__ __forceinline__ double row_sum(double v) {
 constexpr double kLast = -1.7e308;
 __device__ __forceinline__ double gone() { return __builtin_bit_cast(double, uint64_t{0xfff8000000000000}); }
 
-__device__ __forceinline__ double score_of(double x, bool sigmoid, double top, double sum) {
-  if (!(x > -__builtin_inf())) return 0.;
-  if (sigmoid) return 1. / (1. + exp(-x));
-  return sum > 0. ? (x == top ? 1. : exp(x - top)) / sum : 0.;
+// a b + c with c in scalar registers: the compiler's accumulating form would first copy c.
+__device__ __forceinline__ double fma_const(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
+
+// e^v: v = n ln 2 + r with |r| <= ln 2 / 2, and the power series of e^r up to r^13 / 13! (the next term
+// is below 2^-57).  Off by a last bit or two; 0 and infinity where 64 bits end.
+__device__ __forceinline__ double exp64(double v) {
+  v = fmin(fmax(v, -1000.), 1000.);
+  const double n = __builtin_rint(v * 1.4426950408889634074);
+  // ln 2 in two parts, the first of 32 bits, so that n times it is exact
+  double r = fma(-n, 0x1.62e42feep-1, v);
+  r = fma(-n, 0x1.a39ef35793c76p-33, r);
+  double e = fma_const(r, 1. / 6227020800., 1. / 479001600.);
+  e = fma_const(e, r, 1. / 39916800.);
+  e = fma_const(e, r, 1. / 3628800.);
+  e = fma_const(e, r, 1. / 362880.);
+  e = fma_const(e, r, 1. / 40320.);
+  e = fma_const(e, r, 1. / 5040.);
+  e = fma_const(e, r, 1. / 720.);
+  e = fma_const(e, r, 1. / 120.);
+  e = fma_const(e, r, 1. / 24.);
+  e = fma_const(e, r, 1. / 6.);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.);
+  e = fma(e, r, 1.);
+  return __builtin_ldexp(e, static_cast<int>(n));
+}
+
+// Scores: 0 for a logit of -inf or NaN.
+__device__ __forceinline__ double sigmoid64(double x) {
+  const double s = 1. / (1. + exp64(-x));
+  return x > -__builtin_inf() ? s : 0.;
+}
+__device__ __forceinline__ double softmax64(double x, double top) {   // before it is divided by the sum
+  const double e = exp64(x - top);
+  return x > -__builtin_inf() ? (x == top ? 1. : e) : 0.;
 }
 
 // Sixteen lanes a token, PER neighbouring experts a lane: of equal choices the lowest lane's first one
@@ -105,8 +140,7 @@ __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const
     top = row_max(top);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const double v = x[i];
-      pick[i] = v > none ? (v == top ? 1. : exp(v - top)) : 0.;
+      pick[i] = softmax64(x[i], top);
       sum += pick[i];
     }
     sum = row_sum(sum);
@@ -116,7 +150,7 @@ __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) pick[i] = score_of(x[i], true, 0., 0.);
+    for (int i = 0; i < PER; ++i) pick[i] = sigmoid64(x[i]);
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -125,15 +159,40 @@ __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const
     if (e0 + i >= E) pick[i] = gone();
   }
 
-  if (p.top_groups < p.n_groups) {   // the same for all
+  const int G = p.n_groups, size = E / G, span = size / PER;   // lanes of a group, where they are whole
+  if (p.top_groups < G && size % PER == 0 && (span & (span - 1)) == 0) {   // the same for all
+    // A lane's experts are of one group, and so are `span` neighbouring lanes: all in registers.  (Lanes
+    // past the experts have no group and are not asked.)
+    double first = kLast, second = kLast;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      second = fmax(second, fmin(first, pick[i]));
+      first = fmax(first, pick[i]);
+    }
+    for (int o = 1; o < span; o *= 2) {
+      const double f = __shfl_xor(first, o), c = __shfl_xor(second, o);
+      second = fmax(fmax(second, c), fmin(first, f));
+      first = fmax(first, f);
+    }
+    const double v = p.group_best == 2 && second > kLast ? first + second : first;
+    const int g = l / span;
+    int better = 0;
+    for (int h = 0; h < G; ++h) {
+      const double o = __shfl(v, h * span, kLanes);
+      better += o > v || (o == v && h < g);
+    }
+    if (better >= p.top_groups)
+#pragma unroll
+      for (int i = 0; i < PER; ++i) pick[i] = gone();
+  } else if (p.top_groups < G) {
     double* const mine = choices + slot * E;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (e0 + i < E) mine[e0 + i] = pick[i];
     __syncthreads();
-    const int G = p.n_groups, size = E / G;
     for (int g = l; g < G; g += kLanes) {   // best and second best, the ones below every number left out
       double first = kLast, second = kLast;
+#pragma unroll 4
       for (int i = 0; i < size; ++i) {
         const double c = mine[g * size + i];
         second = fmax(second, fmin(first, c));
@@ -165,9 +224,13 @@ __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const
     }
   }
 
-  double best = pick[0];
+  auto largest = [&] {   // in four chains
+    double m[4] = {pick[0], gone(), gone(), gone()};
 #pragma unroll
-  for (int i = 1; i < PER; ++i) best = fmax(best, pick[i]);
+    for (int i = 1; i < PER; ++i) m[i % 4] = fmax(m[i % 4], pick[i]);
+    return PER > 2 ? fmax(fmax(m[0], m[1]), fmax(m[2], m[3])) : fmax(m[0], m[1]);
+  };
+  double best = largest();
   int my_id = 0;
   for (int k = 0; k < p.top_k; ++k) {
     const double m = row_max(best);
@@ -175,23 +238,26 @@ __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const
     const int lane = __builtin_ctz(static_cast<uint32_t>(who) | 1u << kLanes);
     int id = 0;
     if (l == lane) {
-      bool found = false;
-      best = gone();
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const bool hit = !found && pick[i] == m;
-        found = found || hit;
-        id = hit ? e0 + i : id;
-        pick[i] = hit ? gone() : pick[i];
-        best = fmax(best, pick[i]);
+      for (int i = PER - 1; i >= 0; --i) id = pick[i] == m ? i : id;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {   // the high word makes it a NaN
+        const uint64_t u = __builtin_bit_cast(uint64_t, pick[i]);
+        const uint32_t hi = i == id ? 0xfff80000u : static_cast<uint32_t>(u >> 32);
+        pick[i] = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | static_cast<uint32_t>(u));
       }
+      best = largest();
+      id += e0;
     }
     id = __shfl(id, lane & (kLanes - 1), kLanes);
     if (l == k) my_id = id;
   }
   // lane k has the k-th expert: its score once more
   double w = 0.;
-  if (l < p.top_k) w = score_of(load_w<LT>(logits, row + my_id), sigmoid, top, sum);
+  if (l < p.top_k) {
+    const double v = load_w<LT>(logits, row + my_id);
+    w = sigmoid ? sigmoid64(v) : sum > 0. ? softmax64(v, top) / sum : 0.;
+  }
   if (p.flags & QZ_ROUTE_RENORM) {
     const double total = row_sum(w);
     w = total > 0. ? w / total : 0.;
