@@ -106,7 +106,7 @@ MoeWs moe_ws(void* base, int64_t n, int64_t d, int64_t f, int E, int k) {
   w.hcodes = c.take<int8_t>(pairs * i8_pitch(f));
   w.hscales = c.take<float>(pairs);
   w.hsums = c.take<int32_t>(pairs);
-  w.y = c.take<float>(pairs * d);
+  w.y = c.take<float>(pairs * round_up(d, 4));
   w.bytes = c.used;
   return w;
 }
@@ -344,9 +344,9 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
     return launch_i8_rows_down(p, n, stream);
   }
   p.Y = w.y;
-  p.ldy = d;
+  p.ldy = round_up(d, 4);
   QZ_TRY(launch_i8_down(p, stream));
-  return launch_i8_sum(w.y, d, ids, n, d, top_k, n_experts, static_cast<uint16_t*>(Y), stream);
+  return launch_i8_sum(w.y, p.ldy, ids, n, d, top_k, n_experts, static_cast<uint16_t*>(Y), stream);
 }
 
 }  // extern "C"

@@ -25,43 +25,47 @@ __device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, fl
 
 __device__ __forceinline__ float silu(float g) { return g / (1.f + expf(-g)); }
 
-// Expert and slots of the token tile `index` of `bn` slots, the experts' tiles in their order; false
-// past the last one.  Every lane of a wavefront has eight neighbouring experts.
-__device__ __forceinline__ bool find_tile(const I8Product& p, int index, int bn, int* expert, int* first,
-                                          int* end) {
-  const int lane = threadIdx.x & 63;
-  int at[9], tiles = 0;
+// The token tiles of `bn` slots of an expert layer, the experts' tiles in their order.  Every lane of a
+// wavefront has eight neighbouring experts.
+struct Tiles {
+  int at[9], upto, tiles;   // the lane's experts' slots; tiles up to and of the lane
+  int total;
+  __device__ __forceinline__ Tiles(const I8Product& p, int bn) {
+    const int lane = threadIdx.x & 63;
+    tiles = 0;
 #pragma unroll
-  for (int i = 0; i <= 8; ++i) {
-    const int e = 8 * lane + i;
-    at[i] = p.offsets[e < p.E ? e : p.E];
-    if (i) tiles += (at[i] - at[i - 1] + bn - 1) / bn;
-  }
-  int upto = tiles;
-  for (int o = 1; o < 64; o *= 2) {
-    const int v = __shfl_up(upto, o);
-    if (lane >= o) upto += v;
-  }
-  const uint64_t who = __ballot(index < upto);
-  if (!who) return false;
-  const int src = __builtin_ctzll(who);
-  int left = index - (upto - tiles), e = 0, a = 0, b = 0;
-#pragma unroll
-  for (int i = 1; i <= 8; ++i) {
-    const int n = (at[i] - at[i - 1] + bn - 1) / bn;
-    if (left >= 0 && left < n) {
-      e = 8 * lane + i - 1;
-      a = at[i - 1] + left * bn;
-      b = at[i];
+    for (int i = 0; i <= 8; ++i) {
+      const int e = 8 * lane + i;
+      at[i] = p.offsets[e < p.E ? e : p.E];
+      if (i) tiles += (at[i] - at[i - 1] + bn - 1) / bn;
     }
-    left -= n;
+    upto = tiles;
+    for (int o = 1; o < 64; o *= 2) {
+      const int v = __shfl_up(upto, o);
+      if (lane >= o) upto += v;
+    }
+    total = __builtin_amdgcn_readlane(upto, 63);
   }
-  *expert = __builtin_amdgcn_readlane(e, src);
-  *first = __builtin_amdgcn_readlane(a, src);
-  const int stop = __builtin_amdgcn_readlane(b, src);
-  *end = *first + bn < stop ? *first + bn : stop;
-  return true;
-}
+  // Expert and slots of tile `index` < total.
+  __device__ __forceinline__ void find(int index, int bn, int* expert, int* first, int* end) const {
+    const int src = __builtin_ctzll(__ballot(index < upto));
+    int left = index - (upto - tiles), e = 0, a = 0, b = 0;
+#pragma unroll
+    for (int i = 1; i <= 8; ++i) {
+      const int n = (at[i] - at[i - 1] + bn - 1) / bn;
+      if (left >= 0 && left < n) {
+        e = 8 * static_cast<int>(threadIdx.x & 63) + i - 1;
+        a = at[i - 1] + left * bn;
+        b = at[i];
+      }
+      left -= n;
+    }
+    *expert = __builtin_amdgcn_readlane(e, src);
+    *first = __builtin_amdgcn_readlane(a, src);
+    const int stop = __builtin_amdgcn_readlane(b, src);
+    *end = *first + bn < stop ? *first + bn : stop;
+  }
+};
 
 // Lets a kernel use its dynamic LDS, once a device.
 class LdsAllowance {

@@ -25,19 +25,12 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   return c;
 }
 
-// The whole number nearest to v / s (the quotient itself), ties to the even one, within +-127.
-// v r is off by less than 2^-14 of a code (127 codes, three roundings), so only a quotient that near
-// to a half needs the remainder v - q s, which one fused step gives exactly: it is a multiple of the
-// smaller of both numbers' last bits, and at most s / 2 or so.
-__device__ __forceinline__ float nearest_code(float v, const RowScale& c) {
-  v *= c.up;
-  const float t = v * c.r;
-  float q = __builtin_rintf(t);
-  if (fabsf(t - q) > 0.5f - 0x1p-13f) {
-    const float rest = fmaf(-q, c.su, v), half = 0.5f * c.su;
-    if (fabsf(rest) > half || (fabsf(rest) == half && (static_cast<int>(q) & 1)))
-      q += rest > 0.f ? 1.f : -1.f;
-  }
+// Code of v: the whole number nearest to v / s (the quotient itself), ties to the even one, within
+// +-127, from the remainder v - q s, which one fused step gives exactly: it is a multiple of the smaller
+// of both numbers' last bits, and at most s / 2 or so.  q: at most one off.
+__device__ __forceinline__ float settled_code(float v, float q, const RowScale& c) {
+  const float rest = fmaf(-q, c.su, v), half = 0.5f * c.su;
+  if (fabsf(rest) > half || (fabsf(rest) == half && (static_cast<int>(q) & 1))) q += rest > 0.f ? 1.f : -1.f;
   return fminf(fmaxf(q, -127.f), 127.f);
 }
 
@@ -79,17 +72,42 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8], uint32_t top) {
 }
 
 // Codes of eight elements (two words), and their values' whole numbers.
+//
+// v r is off by less than 2^-14 of a code (127 codes, two roundings), so only quotients that near to a
+// half need their remainder.  Adding 1.5 2^23 rounds to a whole number, nearest even, and leaves its low
+// byte in the sum's.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& c, float (&q)[8]) {
+  constexpr float kWhole = 12582912.f;
+  float u[8], m[8];
+  bool near = c.up != 1.f;   // small rows: all by their remainders
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    u[i] = v[i] * c.r;
+    m[i] = u[i] + kWhole;
+    q[i] = m[i] - kWhole;
+    near = near || fabsf(u[i] - q[i]) > 0.5f - 0x1p-13f;
+  }
+  if (near) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float w = v[i] * c.up;
+      q[i] = settled_code(w, fminf(fmaxf(__builtin_rintf(w * c.r), -127.f), 127.f), c);
+      m[i] = q[i] + kWhole;
+    }
+  }
+  if (!c.codes) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = 0.f;
+      m[i] = kWhole;
+    }
+  }
   uint32_t w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[4 * h + i] = c.codes ? nearest_code(v[4 * h + i], c) : 0.f;
-      b[i] = static_cast<uint32_t>(static_cast<int>(q[4 * h + i])) & 255u;
-    }
-    w[h] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(m[4 * h + 1]), __float_as_uint(m[4 * h]), 0x0c0c0400);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(m[4 * h + 3]), __float_as_uint(m[4 * h + 2]), 0x04000c0c);
+    w[h] = lo | hi;
   }
   return make_uint2(w[0], w[1]);
 }

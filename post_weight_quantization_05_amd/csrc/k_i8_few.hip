@@ -39,8 +39,11 @@ __global__ __launch_bounds__(64 * T::kWaves) void i8_few_kernel(const I8Product 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   lds_u8* const lds = (lds_u8*)smem + wave * D * T::kStage;
   int expert = 0, slot0 = 0, slot_end = 0;
-  if constexpr (FORM != kPlain)
-    if (!find_tile(p, blockIdx.y, 16 * NT, &expert, &slot0, &slot_end)) return;
+  if constexpr (FORM != kPlain) {
+    const Tiles tiles(p, 16 * NT);
+    if (static_cast<int>(blockIdx.y) >= tiles.total) return;
+    tiles.find(blockIdx.y, 16 * NT, &expert, &slot0, &slot_end);
+  }
   const int64_t t0 = FORM == kPlain ? blockIdx.y * (int64_t)(16 * NT) : slot0;
   const int64_t t_end = FORM == kPlain ? p.n : slot_end;
   constexpr int kRows = FORM == kGateUp ? 8 * RT : 16 * RT;   // output rows

@@ -57,22 +57,33 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
   // The hardware deals workgroups to the 8 XCDs in turn.  Each XCD gets a run of consecutive tiles,
   // and runs go through 8 rows of W tiles by all X tiles, so the tiles that are resident on an XCD
   // share panels in its L2.
-  int pid = blockIdx.x;
-  {
-    const int nb = gridDim.x, per = nb / 8, extra = nb % 8, x = pid % 8;
-    pid = x * per + (x < extra ? x : extra) + pid / 8;
+  const auto mapped = [&](int nb) {
+    const int per = nb / 8, extra = nb % 8, x = blockIdx.x % 8;
+    return x * per + (x < extra ? x : extra) + static_cast<int>(blockIdx.x) / 8;
+  };
+  int pid, expert = 0, slot0 = 0, slot_end = 0, tw, tx;
+  const auto place = [&] {
+    constexpr int kGroup = 8;
+    const int in_group = kGroup * tiles_x;
+    const int g0 = pid / in_group * kGroup;
+    const int gh = tiles_w - g0 < kGroup ? tiles_w - g0 : kGroup;
+    tw = __builtin_amdgcn_readfirstlane(g0 + pid % in_group % gh);
+    tx = __builtin_amdgcn_readfirstlane(pid % in_group / gh);
+  };
+  if constexpr (FORM == kPlain) {
+    pid = mapped(gridDim.x);
+    place();
+  } else {
+    // the launch has room for the most tiles there can be; those there are go evenly to the XCDs
+    const Tiles tiles(p, BN);
+    tiles_x = tiles.total;
+    if (static_cast<int>(blockIdx.x) >= tiles_w * tiles_x) return;
+    pid = mapped(tiles_w * tiles_x);
+    place();
+    tiles.find(tx, BN, &expert, &slot0, &slot_end);
   }
-  constexpr int kGroup = 8;
-  const int in_group = kGroup * tiles_x;
-  const int g0 = pid / in_group * kGroup;
-  const int gh = tiles_w - g0 < kGroup ? tiles_w - g0 : kGroup;
-  const int tw = __builtin_amdgcn_readfirstlane(g0 + pid % in_group % gh);
-  const int tx = __builtin_amdgcn_readfirstlane(pid % in_group / gh);
   constexpr int kRows = FORM == kGateUp ? BM / 2 : BM;   // output rows of the tile
   const int64_t r0 = static_cast<int64_t>(tw) * kRows;
-  int expert = 0, slot0 = 0, slot_end = 0;
-  if constexpr (FORM != kPlain)
-    if (!find_tile(p, tx, BN, &expert, &slot0, &slot_end)) return;
   const int64_t t0 = FORM == kPlain ? static_cast<int64_t>(tx) * BN : slot0;
   const int64_t t_end = FORM == kPlain ? p.n : slot_end;
   // last rows inside the matrices, counted in the tile: rows past them read these again

@@ -1,6 +1,6 @@
 // The routed expert layer on 8-bit integer weights: pairs sorted by expert, and the sum over a
 // token's experts (the products are in k_i8_gemm.hip).
-#include "qz_internal.h"
+#include "i8_quant.h"
 
 namespace qz {
 
@@ -44,17 +44,33 @@ __global__ __launch_bounds__(256) void i8_group_kernel(const int32_t* __restrict
   }
 }
 
+// A token's results added in the order of its experts: a workgroup per 1024 columns of a token, four a
+// thread; rows of y are whole fours.
 __global__ __launch_bounds__(256) void i8_sum_kernel(const float* __restrict__ y, int64_t ldp,
-                                                     const int32_t* __restrict__ ids, int64_t n,
-                                                     int64_t d, int k, int E, uint16_t* __restrict__ Y) {
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n * d; i += (int64_t)gridDim.x * 256) {
-    const int64_t t = i / d, c = i % d;
-    float v = 0.f;
-    for (int r = 0; r < k; ++r) {
-      const int id = ids[t * k + r];
-      if (id >= 0 && id < E) v += y[(t * k + r) * ldp + c];
-    }
-    Y[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+                                                     const int32_t* __restrict__ ids, int64_t d,
+                                                     int blocks, int k, int E, uint16_t* __restrict__ Y) {
+  const int64_t t = blockIdx.x / static_cast<unsigned>(blocks);
+  const int64_t c = (blockIdx.x % static_cast<unsigned>(blocks)) * (int64_t)1024 + 4 * threadIdx.x;
+  if (c >= d) return;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = 0; r < k; ++r) {
+    const int id = ids[t * k + r];
+    if (id < 0 || id >= E) continue;
+    const float4 o = *reinterpret_cast<const float4*>(y + (t * k + r) * ldp + c);
+    v.x += o.x;
+    v.y += o.y;
+    v.z += o.z;
+    v.w += o.w;
+  }
+  const uint2 w = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+  uint16_t* const o = Y + t * d + c;
+  if (d % 4 == 0 && reinterpret_cast<uintptr_t>(Y) % 8 == 0) {
+    *reinterpret_cast<uint2*>(o) = w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (c + j < d) o[j] = static_cast<uint16_t>((j < 2 ? w.x : w.y) >> (16 * (j % 2)));
   }
 }
 
@@ -68,9 +84,9 @@ int launch_i8_group(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, 
 
 int launch_i8_sum(const float* y_pairs, int64_t ldp, const int32_t* ids, int64_t n, int64_t d,
                   int k, int E, uint16_t* Y, hipStream_t s) {
-  const int64_t b = ceil_div(n * d, 256);
-  hipLaunchKernelGGL(i8_sum_kernel, dim3(static_cast<unsigned>(b < 65536 ? b : 65536)), dim3(256), 0,
-                     s, y_pairs, ldp, ids, n, d, k, E, Y);
+  const int64_t blocks = ceil_div(d, 1024);
+  hipLaunchKernelGGL(i8_sum_kernel, dim3(static_cast<unsigned>(n * blocks)), dim3(256), 0, s, y_pairs, ldp, ids,
+                     d, static_cast<int>(blocks), k, E, Y);
   return check_launch("i8_sum");
 }
 
