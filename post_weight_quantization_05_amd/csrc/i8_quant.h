@@ -34,31 +34,50 @@ __device__ __forceinline__ float settled_code(float v, float q, const RowScale& 
   return fminf(fmaxf(q, -127.f), 127.f);
 }
 
-// Eight neighbouring elements of a row, columns past `left` as zeros.  VEC: all eight or none are
-// there, on a 16-byte boundary.
+// Eight neighbouring elements of a row as they lie in memory, and as numbers; columns past `left` are
+// zeros.  VEC: all eight or none are there, on a 16-byte boundary.
+template <int WT>
+struct Raw8 {
+  uint4 w[WT == QZ_BF16 ? 1 : 2];
+};
 template <int WT, bool VEC>
-__device__ __forceinline__ void load8(const void* p, int64_t at, int64_t left, float (&v)[8]) {
+__device__ __forceinline__ Raw8<WT> load8(const void* p, int64_t at, int64_t left) {
+  Raw8<WT> r;
   if constexpr (VEC) {
-    if (left <= 0) {
+    constexpr int n = WT == QZ_BF16 ? 1 : 2;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (2 * n));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    } else if constexpr (WT == QZ_BF16) {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    for (int i = 0; i < n; ++i) r.w[i] = left > 0 ? src[i] : make_uint4(0, 0, 0, 0);
+  } else if constexpr (WT == QZ_BF16) {
+    uint32_t w[4];
+    const uint16_t* src = static_cast<const uint16_t*>(p) + at;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-      const float4 a = f[0], b = f[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    for (int i = 0; i < 4; ++i)
+      w[i] = (2 * i < left ? static_cast<uint32_t>(src[2 * i]) : 0u) | (2 * i + 1 < left ? static_cast<uint32_t>(src[2 * i + 1]) << 16 : 0u);
+    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    uint32_t w[8];
+    const uint32_t* src = static_cast<const uint32_t*>(p) + at;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = i < left ? src[i] : 0u;
+    r.w[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    r.w[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  return r;
+}
+template <int WT>
+__device__ __forceinline__ void numbers8(const Raw8<WT>& r, float (&v)[8]) {
+  if constexpr (WT == QZ_BF16) {
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? load_w<WT>(p, at + i) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   }
 }
 
@@ -73,8 +92,8 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8], uint32_t top) {
 
 // Codes of eight elements (two words), and their values' whole numbers.
 //
-// v r is off by less than 2^-14 of a code (127 codes, two roundings), so only quotients that near to a
-// half need their remainder.  Adding 1.5 2^23 rounds to a whole number, nearest even, and leaves its low
+// v r is off by less than 2^-16 of a code (127 codes, two roundings of 2^-24 each), so only quotients that
+// near to a half need their remainder.  Adding 1.5 2^23 rounds to a whole number, nearest even, and leaves its low
 // byte in the sum's.
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& c, float (&q)[8]) {
   constexpr float kWhole = 12582912.f;
@@ -85,7 +104,7 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], const RowScale& c, 
     u[i] = v[i] * c.r;
     m[i] = u[i] + kWhole;
     q[i] = m[i] - kWhole;
-    near = near || fabsf(u[i] - q[i]) > 0.5f - 0x1p-13f;
+    near = near || fabsf(u[i] - q[i]) > 0.5f - 0x1p-15f;
   }
   if (near) {
 #pragma unroll

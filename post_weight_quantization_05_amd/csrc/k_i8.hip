@@ -10,84 +10,97 @@ namespace {
 
 // TPR threads a row, CH chunks of eight elements each, which stay in registers between the row's
 // maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier.
+// A workgroup goes through several rows: the next one is on its way while one is worked on, and the
+// column factors are loaded once.
 //
 // Bound by HBM.
-template <int WT, bool VEC, int TPR, int CH>
+template <int WT, bool VEC, bool FACTORS, int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
     const void* __restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
     const float* __restrict__ colf, int8_t* __restrict__ codes, float* __restrict__ scales,
     int32_t* __restrict__ sums, void* __restrict__ values) {
-  constexpr int kWaves = TPR / 64;
-  __shared__ uint32_t tops[kWaves];
-  __shared__ int parts[kWaves];
-  const int64_t row = TPR == 64 ? blockIdx.x * (int64_t)4 + (threadIdx.x >> 6) : blockIdx.x;
-  if (TPR == 64 && row >= rows) return;
+  constexpr int kWaves = TPR / 64, kRows = TPR == 64 ? 4 : 1;   // rows of a workgroup at a time
+  __shared__ uint32_t tops[2][kWaves];
+  __shared__ int parts[2][kWaves];
   const int t = threadIdx.x % TPR, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t P = i8_pitch(cols);
-  float v[CH][8];
-  uint32_t top = 0;
+  const int64_t P = i8_pitch(cols), step = static_cast<int64_t>(gridDim.x) * kRows;
+  int64_t row = blockIdx.x * (int64_t)kRows + (TPR == 64 ? wave : 0);
+  if (row >= rows) return;
+  float f[FACTORS ? CH : 1][8];
+  if constexpr (FACTORS) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) load8<WT, VEC>(X, row * ldx + (c * TPR + t) * 8, cols - (c * TPR + t) * 8, v[c]);
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    if (colf) {
-      float f[8];
-      load8<QZ_F32, VEC>(colf, (c * TPR + t) * 8, cols - (c * TPR + t) * 8, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] *= f[i];
-    }
-    top = top8(v[c], top);
+    for (int c = 0; c < CH; ++c) numbers8(load8<QZ_F32, VEC>(colf, (c * TPR + t) * 8, cols - (c * TPR + t) * 8), f[c]);
   }
-  top = wave_top(top);
-  if constexpr (kWaves > 1) {
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-    top = wave_top(lane < kWaves ? tops[lane] : 0u);
-  }
-  const RowScale sc = row_scale(top);
-  int sum = 0;
+  Raw8<WT> raw[CH];
+  auto load = [&](int64_t r) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int64_t at = (c * TPR + t) * 8;
-    if (at >= P) continue;
-    float q[8];
-    const uint2 w = codes8(v[c], sc, q);
-    *reinterpret_cast<uint2*>(codes + row * P + at) = w;
-    sum = add_codes(w.x, add_codes(w.y, sum));
-    if (!values || at >= cols) continue;
-    const int64_t o = row * cols + at;
-    if constexpr (VEC) {
-      if constexpr (WT == QZ_BF16) {
-        uint32_t u[4];
+    for (int c = 0; c < CH; ++c) raw[c] = load8<WT, VEC>(X, r * ldx + (c * TPR + t) * 8, cols - (c * TPR + t) * 8);
+  };
+  load(row);
+  for (int turn = 0; row < rows; row += step, turn ^= 1) {
+    float v[CH][8];
+    uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = bf16_pair(q[2 * i] * sc.s, q[2 * i + 1] * sc.s);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(values) + o) = make_uint4(u[0], u[1], u[2], u[3]);
-      } else {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(values) + o);
-        f[0] = make_float4(q[0] * sc.s, q[1] * sc.s, q[2] * sc.s, q[3] * sc.s);
-        f[1] = make_float4(q[4] * sc.s, q[5] * sc.s, q[6] * sc.s, q[7] * sc.s);
+    for (int c = 0; c < CH; ++c) {
+      numbers8(raw[c], v[c]);
+      if constexpr (FACTORS) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] *= f[c][i];
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (at + i < cols) {
-          if constexpr (WT == QZ_BF16)
-            static_cast<uint16_t*>(values)[o + i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(q[i] * sc.s));
-          else
-            static_cast<float*>(values)[o + i] = q[i] * sc.s;
-        }
+      top = top8(v[c], top);
     }
-  }
-  if (sums) {
-    sum = wave_sum(sum);
+    load(row + step < rows ? row + step : row);
+    top = wave_top(top);
     if constexpr (kWaves > 1) {
-      if (lane == 0) parts[wave] = sum;
-      __syncthreads();
-      sum = wave_sum(lane < kWaves ? parts[lane] : 0);
+      if (lane == 0) tops[turn][wave] = top;
+      __syncthreads();   // the other buffer is free when the next row's barrier is passed
+      top = wave_top(lane < kWaves ? tops[turn][lane] : 0u);
     }
-    if (t == 0) sums[row] = sum;
+    const RowScale sc = row_scale(top);
+    int sum = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int64_t at = (c * TPR + t) * 8;
+      if (at >= P) continue;
+      float q[8];
+      const uint2 w = codes8(v[c], sc, q);
+      *reinterpret_cast<uint2*>(codes + row * P + at) = w;
+      sum = add_codes(w.x, add_codes(w.y, sum));
+      if (!values || at >= cols) continue;
+      const int64_t o = row * cols + at;
+      if constexpr (VEC) {
+        if constexpr (WT == QZ_BF16) {
+          uint32_t u[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[i] = bf16_pair(q[2 * i] * sc.s, q[2 * i + 1] * sc.s);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(values) + o) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+          float4* d = reinterpret_cast<float4*>(static_cast<float*>(values) + o);
+          d[0] = make_float4(q[0] * sc.s, q[1] * sc.s, q[2] * sc.s, q[3] * sc.s);
+          d[1] = make_float4(q[4] * sc.s, q[5] * sc.s, q[6] * sc.s, q[7] * sc.s);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (at + i < cols) {
+            if constexpr (WT == QZ_BF16)
+              static_cast<uint16_t*>(values)[o + i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(q[i] * sc.s));
+            else
+              static_cast<float*>(values)[o + i] = q[i] * sc.s;
+          }
+      }
+    }
+    if (sums) {
+      sum = wave_sum(sum);
+      if constexpr (kWaves > 1) {
+        if (lane == 0) parts[turn][wave] = sum;
+        __syncthreads();
+        sum = wave_sum(lane < kWaves ? parts[turn][lane] : 0);
+      }
+      if (t == 0) sums[row] = sum;
+    }
+    if (t == 0) scales[row] = sc.s;
   }
-  if (t == 0) scales[row] = sc.s;
 }
 
 __global__ __launch_bounds__(256) void i8_pack_kernel(const uint8_t* __restrict__ in, int64_t rows,
@@ -119,30 +132,36 @@ int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_
                        const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
                        hipStream_t s) {
   if (rows == 0) return QZ_OK;
+  // With factors, or in bf16, where a row is few bytes a thread, workgroups that fill the chip once and go
+  // through the rows (8192 x 5120 bf16 with factors and values 41 us, a row each 52); else a row each
+  // (25600 x 5120 fp32 with values 208 us, going through the rows 230).
+  const bool through = colf || xt == QZ_BF16;
   auto go = [&](auto kernel, int tpr) {
     const int64_t groups = tpr == 64 ? ceil_div(rows, 4) : rows;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups)), dim3(tpr < 256 ? 256 : tpr), 0, s, X, rows,
-                       cols, ldx, colf, codes, scales, sums, values);
+    const int64_t most = through ? 256 * (tpr < 256 ? 8 : 2048 / tpr) : groups;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(tpr < 256 ? 256 : tpr), 0,
+                       s, X, rows, cols, ldx, colf, codes, scales, sums, values);
     return check_launch("i8_quantize");
   };
-  auto by_size = [&](auto type, auto vec) {
+  auto by_size = [&](auto type, auto vec, auto factors) {
     constexpr int WT = decltype(type)::value;
-    constexpr bool VEC = decltype(vec)::value;
-    if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, 64, 1>, 64);
-    if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, 64, 2>, 64);
-    if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, 64, 4>, 64);
-    if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, 256, 2>, 256);
-    if (cols <= 8192) return go(i8_quantize_kernel<WT, VEC, 256, 4>, 256);
-    if (cols <= 16384) return go(i8_quantize_kernel<WT, VEC, 1024, 2>, 1024);
-    if (cols <= 32768) return go(i8_quantize_kernel<WT, VEC, 1024, 4>, 1024);
-    return go(i8_quantize_kernel<WT, VEC, 1024, 8>, 1024);
+    constexpr bool VEC = decltype(vec)::value, F = decltype(factors)::value;
+    if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, F, 64, 1>, 64);
+    if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, F, 64, 2>, 64);
+    if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, F, 64, 4>, 64);
+    if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, F, 256, 2>, 256);
+    if (cols <= 6144) return go(i8_quantize_kernel<WT, VEC, F, 256, 3>, 256);
+    if (cols <= 8192) return go(i8_quantize_kernel<WT, VEC, F, 256, 4>, 256);
+    if (cols <= 16384) return go(i8_quantize_kernel<WT, VEC, F, 1024, 2>, 1024);
+    if (cols <= 32768) return go(i8_quantize_kernel<WT, VEC, F, 1024, 4>, 1024);
+    return go(i8_quantize_kernel<WT, VEC, F, 1024, 8>, 1024);
   };
   auto by_type = [&](auto type) {
     const size_t size = decltype(type)::value == QZ_BF16 ? 2 : 4;
     auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     return cols % 8 == 0 && ldx * size % 16 == 0 && on16(X) && on16(values) && on16(colf)
-               ? by_size(type, std::true_type{})
-               : by_size(type, std::false_type{});
+               ? (colf ? by_size(type, std::true_type{}, std::true_type{}) : by_size(type, std::true_type{}, std::false_type{}))
+               : (colf ? by_size(type, std::false_type{}, std::true_type{}) : by_size(type, std::false_type{}, std::false_type{}));
   };
   return xt == QZ_BF16 ? by_type(std::integral_constant<int, QZ_BF16>{})
                        : by_type(std::integral_constant<int, QZ_F32>{});

@@ -51,10 +51,10 @@ __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t top = 0;
   auto elements = [&](int c, float (&v)[8]) {
-    load8<QT, VEC>(p.raw, row * p.ldraw + c, p.cols - c, v);
+    numbers8(load8<QT, VEC>(p.raw, row * p.ldraw + c, p.cols - c), v);
     if (p.colf) {
       float f[8];
-      load8<QZ_F32, VEC>(p.colf, c, p.cols - c, f);
+      numbers8(load8<QZ_F32, VEC>(p.colf, c, p.cols - c), f);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] *= f[j];
     }
