@@ -26,7 +26,7 @@ class QzError(RuntimeError):
 
 
 def lib():
-    return _lib.load()
+    return _lib._lib or _lib.load()
 
 
 def _check(status: int):
@@ -34,9 +34,16 @@ def _check(status: int):
         raise QzError(status, lib().qz_last_error().decode(errors="replace"))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    """torch, imported on first use (the statement itself takes longer than a look at a name)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
@@ -472,6 +479,8 @@ def _product_out(out, like, n, d_o, dtype, device):
     torch = _torch()
     if out is None:
         if dtype is None or dtype is torch.bfloat16:
+            if like.dtype is torch.bfloat16:
+                return like.new_empty((n, d_o)), d_o, _lib.QZ_BF16
             return like.new_empty((n, d_o), dtype=torch.bfloat16), d_o, _lib.QZ_BF16
         if dtype is not torch.float32:
             raise TypeError(f"unsupported dtype {dtype} (bf16 or fp32)")
@@ -581,16 +590,14 @@ def _i8_rows(codes, scales, rows, cols, name, index):
     torch = _torch()
     if not 1 <= cols <= QZ_I8_MAX_COLS:
         raise ValueError(f"{name} must have 1 to {QZ_I8_MAX_COLS} columns")
-    pitch = (cols + 127) & ~127
     if codes.dtype is not torch.int8 or scales.dtype is not torch.float32:
         raise TypeError(f"{name}: codes must be int8 and scales fp32")
     if codes.get_device() != index or scales.get_device() != index:
         raise ValueError(f"{name}: codes and scales must be on GPU {index}")
     if not (codes.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{name}: codes and scales must be contiguous")
-    if codes.shape == (rows, pitch) and scales.shape == (rows,):
-        return
-    if codes.shape[-1] != pitch or codes.numel() != pitch * rows or scales.numel() != rows:
+    pitch = (cols + 127) & ~127
+    if codes.numel() != pitch * rows or scales.numel() != rows or codes.shape[-1] != pitch:
         raise ValueError(f"{name}: expected {rows} rows of {pitch} codes and {rows} scales")
 
 
@@ -616,7 +623,7 @@ def qz_i8_quantize(X, colf=None, sums=False, values=False):
         raise ValueError(f"X must have 1 to {QZ_I8_MAX_COLS} columns")
     index = X.device.index
     codes = X.new_empty((rows, (cols + 127) & ~127), dtype=torch.int8)
-    scales = X.new_empty((rows,), dtype=torch.float32)
+    scales = X.new_empty((rows,)) if xt == _lib.QZ_F32 else X.new_empty((rows,), dtype=torch.float32)
     total = X.new_empty((rows,), dtype=torch.int32) if sums else None
     out = X.new_empty((rows, cols)) if values else None
     _run(index, lib().qz_i8_quantize, X.data_ptr(), xt, rows, cols, ld, _vector(colf, cols, "colf", index),
@@ -696,7 +703,7 @@ def qz_i8_linear(X, codes, scales, zeros=None, colf=None, bias=None, out_dtype=N
     (n, d_i), d_o, dev = X.shape, codes.shape[0], X.device
     index = dev.index
     _i8_rows(codes, scales, d_o, d_i, "W", index)
-    out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
+    out, ldy, yt = _product_out(out, X if xt == _lib.QZ_BF16 else codes, n, d_o, out_dtype, dev)
     wp, wn, ws = _scratch(ws, L.qz_i8_linear_workspace(n, d_o, d_i), dev)
     _run(index, L.qz_i8_linear, X.data_ptr(), xt, n, ldx, _vector(colf, d_i, "colf", index),
          codes.data_ptr(), scales.data_ptr(), _i8_zeros(zeros, d_o, "W", index), d_o, d_i,
@@ -728,8 +735,8 @@ def qz_route(logits, top_k, scores="softmax", bias=None, groups=1, top_groups=1,
                  _int32(top_groups, "top_groups"), _int32(group_best, "group_best"),
                  (_lib.QZ_ROUTE_SIGMOID if scores == "sigmoid" else 0) | (_lib.QZ_ROUTE_RENORM if renorm else 0),
                  scale)
-    ids = logits.new_empty((n, max(k, 0)), dtype=torch.int32)
-    w = logits.new_empty((n, max(k, 0)), dtype=torch.float32)
+    ids = logits.new_empty((n, k if k > 0 else 0), dtype=torch.int32)
+    w = logits.new_empty(ids.shape, dtype=torch.float32)
     _run(index, lib().qz_route, logits.data_ptr(), lt, n, ld, C.byref(p), _vector(bias, E, "bias", index),
          ids.data_ptr(), w.data_ptr())
     return ids, w

@@ -113,7 +113,7 @@ __device__ __forceinline__ void stage_rows(const I8Product& p, int64_t first, in
       s.scale[tid] = p.sx[first + tid];
       s.sum[tid] = p.zeros ? p.xsum[first + tid] : 0;
     }
-  } else if (n < 4) {   // a barrier or two a row; otherwise a wavefront a row
+  } else if (n < 4) {   // a few barriers a row; otherwise a wavefront a row
     for (int i = 0; i < n; ++i) stage_row<QT, VEC, kRowsThreads>(p, first + i, i, tid, s, tops);
   } else {
     for (int i = tid / 64; i < n; i += kRowsThreads / 64) stage_row<QT, VEC, 64>(p, first + i, i, tid & 63, s, tops);
@@ -122,125 +122,92 @@ __device__ __forceinline__ void stage_rows(const I8Product& p, int64_t first, in
 }
 
 // A wavefront has R rows of W (kGateUp: R / 2 gate rows and their up rows); N tokens for kPlain.
-// Lane l has 16 bytes of every 1024 columns; blocks of U times 1024 columns of R rows are loaded one
-// ahead, the first one before the tokens are staged.
+// Lane l has 16 bytes of every 1024 columns; blocks of U times 1024 columns of R rows are loaded two
+// ahead, the first two before the tokens are staged.
 template <Form FORM, int QT, bool VEC, int N, int R>
 __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p) {
   constexpr int U = R >= 8 ? 1 : 8 / R;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float xscale[QZ_ROUTE_MAX_TOP_K];
-  __shared__ int xsums[QZ_ROUTE_MAX_TOP_K];
+  __shared__ float xscale[N];
+  __shared__ int xsums[N];
   __shared__ uint32_t tops[4];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   constexpr int kOut = FORM == kGateUp ? R / 2 : R;   // results of a wavefront (for each token)
   const int64_t r0 = (blockIdx.x * (int64_t)4 + wave) * kOut;
   const int pair = FORM == kGateUp ? blockIdx.y : 0;
-  const int token = FORM == kDown ? blockIdx.y : 0;
-  const int segments = FORM == kDown ? p.k : 1;
   const uint32_t P = static_cast<uint32_t>(p.P);
   const Staged s{smem, xscale, xsums, static_cast<int>(round_up(p.P, 1024))};
 
-  auto expert_of = [&](int at) {   // -1: not here
-    const int e = FORM == kPlain ? 0 : p.ids[at];
-    return FORM == kPlain || (e >= 0 && e < p.E) ? e : -1;
-  };
-  if (FORM == kGateUp && expert_of(pair) < 0) return;   // nobody reads its hidden row
-  const int64_t w_rows = (FORM == kGateUp ? 2 : 1) * p.d_o;
+  const int expert = FORM == kGateUp ? p.ids[pair] : 0;
+  if (FORM == kGateUp && (expert < 0 || expert >= p.E)) return;   // nobody reads its hidden row
+  const int64_t w_row0 = expert * (FORM == kGateUp ? 2 : 1) * p.d_o;
   auto row_of = [&](int i) {   // of the expert's
     const int64_t r = r0 + (FORM == kGateUp ? i % kOut : i);
     return (r < p.d_o ? r : p.d_o - 1) + (FORM == kGateUp && i >= kOut ? p.d_o : 0);
   };
-  const int per = (s.pitch / 1024 + U - 1) / U, blocks = segments * per;
+  const int blocks = (s.pitch / 1024 + U - 1) / U;
   auto load = [&](int b, i32x4 (&w)[R][U]) {
-    int e = FORM == kPlain ? 0 : expert_of(FORM == kGateUp ? pair : token * p.k + b / per);
-    if (e < 0) e = 0;
-    const int8_t* base = p.W + e * w_rows * p.P;
+    if (b >= blocks) return;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int8_t* row = base + row_of(i) * p.P;
+      const int8_t* row = p.W + (w_row0 + row_of(i)) * p.P;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const uint32_t c = static_cast<uint32_t>(b % per * U + u) * 1024 + 16 * lane;
+        const uint32_t c = static_cast<uint32_t>(b * U + u) * 1024 + 16 * lane;
         w[i][u] = *reinterpret_cast<const i32x4*>(row + (c < P ? c : 0));   // past the row: against zeros
       }
     }
   };
   int acc[R][N];
-  float y = 0.f;   // kDown: of row `lane`
-  auto clear = [&] {
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int t = 0; t < N; ++t) acc[i][t] = 0;
-  };
-  // Lane l's sum of [i][t], l = i N + t.
-  auto mine = [&] {
-    int v = 0;
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int t = 0; t < N; ++t) {
-        const int total = lanes_sum(acc[i][t]);
-        v = lane == i * N + t ? total : v;
-      }
-    return v;
-  };
+    for (int t = 0; t < N; ++t) acc[i][t] = 0;
   auto use = [&](int b, const i32x4 (&w)[R][U]) {
-    const int seg = b / per;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = (b % per * U + u) * 1024 + 16 * lane;
+      const int c = (b * U + u) * 1024 + 16 * lane;
       if (U > 1 && c >= s.pitch) continue;
 #pragma unroll
       for (int t = 0; t < N; ++t) {
-        const i32x4 x = *reinterpret_cast<const i32x4*>(s.codes + (seg + t) * s.pitch + c);
+        const i32x4 x = *reinterpret_cast<const i32x4*>(s.codes + t * s.pitch + c);
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[i][t] = __builtin_amdgcn_sdot4(w[i][u][j], x[j], acc[i][t], false);
       }
     }
-    if constexpr (FORM == kDown) {
-      if ((b + 1) % per == 0) {   // an expert's product, weighted
-        const int e = expert_of(token * p.k + seg);
-        const int a = mine();
-        const int64_t r = e * w_rows + (r0 + lane < p.d_o ? r0 + lane : p.d_o - 1);
-        if (lane < R && e >= 0)
-          y += p.pair_weight[token * p.k + seg] *
-               scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[seg], xscale[seg], p.sw[r], 0.f);
-        clear();
-      }
-    }
   };
   i32x4 even[R][U], odd[R][U];
   load(0, even);
-  stage_rows<QT, VEC>(p, FORM == kDown ? (int64_t)token * p.k : FORM == kGateUp ? pair / p.k : 0,
-                      FORM == kDown ? p.k : N, s, tops);
-  clear();
-  for (int b = 0;;) {
-    if (b + 1 < blocks) load(b + 1, odd);
+  load(1, odd);
+  stage_rows<QT, VEC>(p, FORM == kGateUp ? pair / p.k : 0, N, s, tops);
+  for (int b = 0; b < blocks; b += 2) {
     use(b, even);
-    if (++b >= blocks) break;
-    if (b + 1 < blocks) load(b + 1, even);
-    use(b, odd);
-    if (++b >= blocks) break;
+    load(b + 2, even);
+    if (b + 1 >= blocks) break;
+    use(b + 1, odd);
+    load(b + 3, odd);
   }
-  if constexpr (FORM == kDown) {
-    if (lane < R && r0 + lane < p.d_o)
-      static_cast<uint16_t*>(p.Y)[token * p.ldy + r0 + lane] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(y));
-  } else if constexpr (FORM == kGateUp) {
-    const int a = mine();
-    const int i = lane % kOut;
-    const int64_t r = expert_of(pair) * w_rows + row_of(lane < R ? lane : 0);
+  // Lane l's sum of row i and token t, l = i N + t.
+  int a = 0;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      const int total = lanes_sum(acc[i][t]);
+      a = lane == i * N + t ? total : a;
+    }
+  if constexpr (FORM == kGateUp) {
+    const int64_t r = w_row0 + row_of(lane < R ? lane : 0);
     float v = 0.f;
     if (lane < R) v = scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[0], xscale[0], p.sw[r], 0.f);
     const float up = __shfl(v, lane + kOut);
-    if (lane < kOut && r0 + i < p.d_o) static_cast<float*>(p.Y)[pair * p.ldy + r0 + i] = silu(v) * up;
+    if (lane < kOut && r0 + lane < p.d_o) static_cast<float*>(p.Y)[pair * p.ldy + r0 + lane] = silu(v) * up;
   } else {
-    const int a = mine();
-    const int i = lane / N, t = lane % N;
-    const int64_t r = r0 + i;
+    const int t = lane % N;
+    const int64_t r = r0 + lane / N;
     if (lane < R * N && r < p.d_o) {
       const float v = scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[t], xscale[t], p.sw[r], p.bias ? p.bias[r] : 0.f);
       if (p.yt == QZ_BF16)
@@ -251,18 +218,99 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
   }
 }
 
+// The down products of a token's pairs and their weighted sum.  SPLIT wavefronts share the pairs (wavefront
+// w has w % SPLIT, w % SPLIT + SPLIT, ...), and 4 / SPLIT of them the rows of W, R each; the first two
+// blocks of W are on their way before the hidden rows are staged.
+template <bool VEC, int SPLIT, int R>
+__global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Product p) {
+  constexpr int kOut = R * (4 / SPLIT);
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float xscale[QZ_ROUTE_MAX_TOP_K], part[QZ_ROUTE_MAX_TOP_K][kOut];
+  __shared__ int xsums[QZ_ROUTE_MAX_TOP_K];
+  __shared__ uint32_t tops[4];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), turn = wave % SPLIT;
+  const int64_t wg0 = blockIdx.x * (int64_t)kOut, r0 = wg0 + wave / SPLIT * R;
+  const int64_t pair0 = blockIdx.y * (int64_t)p.k;
+  const uint32_t P = static_cast<uint32_t>(p.P);
+  const Staged s{smem, xscale, xsums, static_cast<int>(round_up(p.P, 1024))};
+  const int per = s.pitch / 1024, mine = (p.k - turn + SPLIT - 1) / SPLIT, blocks = mine * per;   // of this wavefront
+  auto expert_of = [&](int at) {   // -1: not here
+    const int e = p.ids[pair0 + at];
+    return e >= 0 && e < p.E ? e : -1;
+  };
+  auto load = [&](int b, i32x4 (&w)[R]) {
+    if (b >= blocks) return;
+    int e = expert_of(turn + SPLIT * (b / per));
+    if (e < 0) e = 0;
+    const uint32_t c = static_cast<uint32_t>(b % per) * 1024 + 16 * lane, at = c < P ? c : 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = e * p.d_o + (r0 + i < p.d_o ? r0 + i : p.d_o - 1);
+      w[i] = *reinterpret_cast<const i32x4*>(p.W + r * p.P + at);
+    }
+  };
+  int acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) acc[i] = 0;
+  auto use = [&](int b, const i32x4 (&w)[R]) {
+    const int at = turn + SPLIT * (b / per);
+    const i32x4 x = *reinterpret_cast<const i32x4*>(s.codes + at * s.pitch + b % per * 1024 + 16 * lane);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i] = __builtin_amdgcn_sdot4(w[i][j], x[j], acc[i], false);
+    if ((b + 1) % per) return;
+    int a = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {   // a pair's product, weighted
+      const int total = lanes_sum(acc[i]);
+      a = lane == i ? total : a;
+      acc[i] = 0;
+    }
+    const int e = expert_of(at);
+    if (lane < R && e >= 0) {
+      const int64_t r = e * p.d_o + (r0 + lane < p.d_o ? r0 + lane : p.d_o - 1);
+      part[at][r0 - wg0 + lane] = p.pair_weight[pair0 + at] * scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[at], xscale[at], p.sw[r], 0.f);
+    }
+  };
+  i32x4 even[R], odd[R];
+  load(0, even);
+  load(1, odd);
+  if constexpr (SPLIT == 4) {   // each wavefront its own; its LDS accesses stay in order
+    for (int i = wave; i < p.k; i += 4) stage_row<QZ_F32, VEC, 64>(p, pair0 + i, i, lane, s, nullptr);
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    stage_rows<QZ_F32, VEC>(p, pair0, p.k, s, tops);
+  }
+  for (int b = 0; b < blocks; b += 2) {
+    use(b, even);
+    load(b + 2, even);
+    if (b + 1 >= blocks) break;
+    use(b + 1, odd);
+    load(b + 3, odd);
+  }
+  __syncthreads();
+  const int64_t r = wg0 + threadIdx.x;
+  if (threadIdx.x < kOut && r < p.d_o) {
+    float y = 0.f;
+    for (int i = 0; i < p.k; ++i)
+      if (expert_of(i) >= 0) y += part[i][threadIdx.x];
+    static_cast<uint16_t*>(p.Y)[blockIdx.y * p.ldy + r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(y));
+  }
+}
+
 template <Form FORM, int QT, bool VEC, int N, int R>
 int launch_rows(const I8Product& p, int64_t y, hipStream_t s) {
-  const int64_t rows = FORM == kDown ? p.k : N, lds = rows * round_up(p.P, 1024);
   constexpr int kOut = 4 * (FORM == kGateUp ? R / 2 : R);
   hipLaunchKernelGGL((i8_rows_kernel<FORM, QT, VEC, N, R>), dim3(static_cast<unsigned>(ceil_div(p.d_o, kOut)), static_cast<unsigned>(y)),
-                     dim3(kRowsThreads), static_cast<size_t>(lds), s, p);
+                     dim3(kRowsThreads), static_cast<size_t>(N * round_up(p.P, 1024)), s, p);
   return check_launch("i8_rows");
 }
 
 template <Form FORM, int QT, bool VEC>
 int by_tokens(const I8Product& p, int64_t y, hipStream_t s) {
-  if constexpr (FORM != kPlain) {
+  if constexpr (FORM == kGateUp) {
     return launch_rows<FORM, QT, VEC, 1, 8>(p, y, s);
   } else {
     // rows a wavefront: enough wavefronts for the chip first
@@ -281,30 +329,49 @@ int by_tokens(const I8Product& p, int64_t y, hipStream_t s) {
   }
 }
 
-template <Form FORM>
-int by_type(const I8Product& p, int64_t y, hipStream_t s) {
-  if (!p.raw) {
-    if constexpr (FORM != kGateUp) return by_tokens<FORM, kCodes, true>(p, y, s);
-    return fail(QZ_EHIP, "i8_rows: no kernel");
-  }
+// Whether the tokens' rows (and the factors) are whole chunks of eight on 16-byte boundaries.
+bool vector_rows(const I8Product& p) {
   const size_t size = p.rt == QZ_BF16 ? 2 : 4;
   auto on16 = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  const bool vec = p.cols % 8 == 0 && p.ldraw * size % 16 == 0 && on16(p.raw) && on16(p.colf);
-  if constexpr (FORM != kDown)
-    if (p.rt == QZ_BF16)
-      return vec ? by_tokens<FORM, QZ_BF16, true>(p, y, s) : by_tokens<FORM, QZ_BF16, false>(p, y, s);
+  return p.cols % 8 == 0 && p.ldraw * size % 16 == 0 && on16(p.raw) && on16(p.colf);
+}
+
+template <Form FORM>
+int by_type(const I8Product& p, int64_t y, hipStream_t s) {
+  if constexpr (FORM == kPlain)
+    if (!p.raw) return by_tokens<FORM, kCodes, true>(p, y, s);
+  const bool vec = vector_rows(p);
+  if (p.rt == QZ_BF16)
+    return vec ? by_tokens<FORM, QZ_BF16, true>(p, y, s) : by_tokens<FORM, QZ_BF16, false>(p, y, s);
   return vec ? by_tokens<FORM, QZ_F32, true>(p, y, s) : by_tokens<FORM, QZ_F32, false>(p, y, s);
 }
 
 }  // namespace
 
 // LDS of a workgroup for the tokens' codes.
-constexpr int64_t kRowsLds = 60 * 1024;
+constexpr int64_t kRowsLds = 56 * 1024;   // besides it, some for the sums
 
 bool i8_rows_fits(int64_t rows, int64_t P) { return rows * round_up(P, 1024) <= kRowsLds; }
 
 int launch_i8_rows(const I8Product& p, hipStream_t s) { return by_type<kPlain>(p, 1, s); }
 int launch_i8_rows_gate_up(const I8Product& p, hipStream_t s) { return by_type<kGateUp>(p, p.n, s); }
-int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s) { return by_type<kDown>(p, tokens, s); }
+int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s) {
+  auto go = [&](auto kernel, int rows) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(ceil_div(p.d_o, rows)), static_cast<unsigned>(tokens)),
+                       dim3(kRowsThreads), static_cast<size_t>(p.k * round_up(p.P, 1024)), s, p);
+    return check_launch("i8_rows_down");
+  };
+  // Few workgroups: as many wavefronts on a token's pairs as there are pairs for, so that there are more of
+  // them (1 token 8 of 128 x 1024, d 4096: 12.3 us, half as many 18.8); else more rows for each staging
+  // (4 tokens there: 28.8 us against 32.8; 7 tokens 2 of 8 x 2048: 17.2 against 20.9).
+  const bool many = tokens * ceil_div(p.d_o, 16) >= 512;
+  auto by_pairs = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    if (p.k >= 4) return many ? go(i8_rows_down_kernel<VEC, 2, 16>, 32) : go(i8_rows_down_kernel<VEC, 4, 16>, 16);
+    if (p.k >= 2 && !many) return go(i8_rows_down_kernel<VEC, 2, 8>, 16);
+    return many ? go(i8_rows_down_kernel<VEC, 1, 8>, 32) : go(i8_rows_down_kernel<VEC, 1, 4>, 16);
+  };
+  return vector_rows(p) ? by_pairs(std::true_type{}) : by_pairs(std::false_type{});
+}
 
 }  // namespace qz
