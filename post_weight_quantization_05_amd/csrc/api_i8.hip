@@ -331,10 +331,11 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
     p.ldraw = p.ldy;
     p.cols = f;
   } else {
-    QZ_TRY(launch_i8_quantize(X, xt, n, d, ldx, nullptr, w.xcodes, w.xscales, w.xsums, nullptr, stream));
-    QZ_TRY(launch_i8_group(ids, pairs, n_experts, w.offsets, w.order, stream));
+    QZ_TRY(launch_i8_quantize_group(X, xt, n, d, ldx, w.xcodes, w.xscales, gu_zeros ? w.xsums : nullptr, ids, top_k,
+                                    n_experts, w.offsets, w.order, stream));
     QZ_TRY(launch_i8_gate_up(p, stream));
-    QZ_TRY(launch_i8_quantize(w.h, QZ_F32, pairs, f, p.ldy, nullptr, w.hcodes, w.hscales, w.hsums, nullptr, stream));
+    QZ_TRY(launch_i8_quantize(w.h, QZ_F32, pairs, f, p.ldy, nullptr, w.hcodes, w.hscales, dn_zeros ? w.hsums : nullptr, nullptr,
+                              stream));
   }
   p.d_o = d;
   p.P = i8_pitch(f);

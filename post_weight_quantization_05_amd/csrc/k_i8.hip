@@ -2,7 +2,7 @@
 // to and from it.
 #include <type_traits>
 
-#include "i8_quant.h"
+#include "i8_group.h"
 
 namespace qz {
 
@@ -14,17 +14,25 @@ namespace {
 // column factors are loaded once.
 //
 // Bound by HBM.
-template <int WT, bool VEC, bool FACTORS, int TPR, int CH>
+// GROUP: the first g.E workgroups sort an expert layer's pairs beside it.
+template <int WT, bool VEC, bool FACTORS, bool GROUP, int TPR, int CH>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
     const void* __restrict__ X, int64_t rows, int64_t cols, int64_t ldx,
     const float* __restrict__ colf, int8_t* __restrict__ codes, float* __restrict__ scales,
-    int32_t* __restrict__ sums, void* __restrict__ values) {
+    int32_t* __restrict__ sums, void* __restrict__ values, const Grouping g) {
+  if constexpr (GROUP) {
+    if (static_cast<int>(blockIdx.x) < g.E) {
+      group_expert<(TPR < 256 ? 4 : TPR / 64)>(g, blockIdx.x);
+      return;
+    }
+  }
   constexpr int kWaves = TPR / 64, kRows = TPR == 64 ? 4 : 1;   // rows of a workgroup at a time
   __shared__ uint32_t tops[2][kWaves];
   __shared__ int parts[2][kWaves];
   const int t = threadIdx.x % TPR, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t P = i8_pitch(cols), step = static_cast<int64_t>(gridDim.x) * kRows;
-  int64_t row = blockIdx.x * (int64_t)kRows + (TPR == 64 ? wave : 0);
+  const int skip = GROUP ? g.E : 0;
+  const int64_t P = i8_pitch(cols), step = static_cast<int64_t>(gridDim.x - skip) * kRows;
+  int64_t row = (blockIdx.x - skip) * (int64_t)kRows + (TPR == 64 ? wave : 0);
   if (row >= rows) return;
   float f[FACTORS ? CH : 1][8];
   if constexpr (FACTORS) {
@@ -128,10 +136,11 @@ unsigned grid_for(int64_t items) {
 
 }  // namespace
 
-int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx,
-                       const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
-                       hipStream_t s) {
-  if (rows == 0) return QZ_OK;
+namespace {
+
+template <bool GROUP>
+int quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx, const float* colf, int8_t* codes,
+             float* scales, int32_t* sums, void* values, const Grouping& g, hipStream_t s) {
   // With factors, or in bf16, where a row is few bytes a thread, workgroups that fill the chip once and go
   // through the rows (8192 x 5120 bf16 with factors and values 41 us, a row each 52); else a row each
   // (25600 x 5120 fp32 with values 208 us, going through the rows 230).
@@ -139,32 +148,50 @@ int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_
   auto go = [&](auto kernel, int tpr) {
     const int64_t groups = tpr == 64 ? ceil_div(rows, 4) : rows;
     const int64_t most = through ? 256 * (tpr < 256 ? 8 : 2048 / tpr) : groups;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(tpr < 256 ? 256 : tpr), 0,
-                       s, X, rows, cols, ldx, colf, codes, scales, sums, values);
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((groups < most ? groups : most) + (GROUP ? g.E : 0))),
+                       dim3(tpr < 256 ? 256 : tpr), 0, s, X, rows, cols, ldx, colf, codes, scales, sums, values, g);
     return check_launch("i8_quantize");
   };
   auto by_size = [&](auto type, auto vec, auto factors) {
     constexpr int WT = decltype(type)::value;
     constexpr bool VEC = decltype(vec)::value, F = decltype(factors)::value;
-    if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, F, 64, 1>, 64);
-    if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, F, 64, 2>, 64);
-    if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, F, 64, 4>, 64);
-    if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, F, 256, 2>, 256);
-    if (cols <= 6144) return go(i8_quantize_kernel<WT, VEC, F, 256, 3>, 256);
-    if (cols <= 8192) return go(i8_quantize_kernel<WT, VEC, F, 256, 4>, 256);
-    if (cols <= 16384) return go(i8_quantize_kernel<WT, VEC, F, 1024, 2>, 1024);
-    if (cols <= 32768) return go(i8_quantize_kernel<WT, VEC, F, 1024, 4>, 1024);
-    return go(i8_quantize_kernel<WT, VEC, F, 1024, 8>, 1024);
+    if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 1>, 64);
+    if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 2>, 64);
+    if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 4>, 64);
+    if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 256, 2>, 256);
+    if (cols <= 6144) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 256, 3>, 256);
+    if (cols <= 8192) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 256, 4>, 256);
+    if (cols <= 16384) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 1024, 2>, 1024);
+    if (cols <= 32768) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 1024, 4>, 1024);
+    return go(i8_quantize_kernel<WT, VEC, F, GROUP, 1024, 8>, 1024);
   };
   auto by_type = [&](auto type) {
     const size_t size = decltype(type)::value == QZ_BF16 ? 2 : 4;
     auto on16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
-    return cols % 8 == 0 && ldx * size % 16 == 0 && on16(X) && on16(values) && on16(colf)
-               ? (colf ? by_size(type, std::true_type{}, std::true_type{}) : by_size(type, std::true_type{}, std::false_type{}))
-               : (colf ? by_size(type, std::false_type{}, std::true_type{}) : by_size(type, std::false_type{}, std::false_type{}));
+    const bool vec = cols % 8 == 0 && ldx * size % 16 == 0 && on16(X) && on16(values) && on16(colf);
+    if constexpr (!GROUP)
+      if (colf)
+        return vec ? by_size(type, std::true_type{}, std::true_type{}) : by_size(type, std::false_type{}, std::true_type{});
+    return vec ? by_size(type, std::true_type{}, std::false_type{}) : by_size(type, std::false_type{}, std::false_type{});
   };
   return xt == QZ_BF16 ? by_type(std::integral_constant<int, QZ_BF16>{})
                        : by_type(std::integral_constant<int, QZ_F32>{});
+}
+
+}  // namespace
+
+int launch_i8_quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx,
+                       const float* colf, int8_t* codes, float* scales, int32_t* sums, void* values,
+                       hipStream_t s) {
+  if (rows == 0) return QZ_OK;
+  return quantize<false>(X, xt, rows, cols, ldx, colf, codes, scales, sums, values, Grouping{}, s);
+}
+
+int launch_i8_quantize_group(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes,
+                             float* scales, int32_t* sums, const int32_t* ids, int k, int E, int32_t* offsets,
+                             int32_t* order, hipStream_t s) {
+  return quantize<true>(X, xt, rows, cols, ldx, nullptr, codes, scales, sums, nullptr,
+                        Grouping{ids, rows * k, E, offsets, order}, s);
 }
 
 int launch_i8_pack(const uint8_t* codes, int64_t rows, int64_t cols, int8_t* out, hipStream_t s) {

@@ -342,8 +342,10 @@ int launch_i8_rows(const I8Product& p, hipStream_t s);
 int launch_i8_rows_gate_up(const I8Product& p, hipStream_t s);
 // Y[token] bf16 = the weighted sum over its pairs, X by pair
 int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s);
-int launch_i8_group(const int32_t* ids, int64_t pairs, int E, int32_t* offsets, int32_t* order,
-                    hipStream_t s);
+// X quantized, and its rows' k pairs each sorted by expert (i8_group.h)
+int launch_i8_quantize_group(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx, int8_t* codes,
+                             float* scales, int32_t* sums, const int32_t* ids, int k, int E, int32_t* offsets,
+                             int32_t* order, hipStream_t s);
 int launch_i8_sum(const float* y_pairs, int64_t ldp, const int32_t* ids, int64_t n, int64_t d,
                   int k, int E, uint16_t* Y, hipStream_t s);
 int launch_route(const void* logits, int lt, int64_t n, int64_t ldl, const qz_router& r,
