@@ -581,6 +581,8 @@ def qz_mx4_moe(X, router, gu_codes, gu_scales, dn_codes, dn_scales, top_k, renor
 
 
 # ------------------------------------------------------------------ 8-bit integer products
+# The ordinary call goes through _lib.binding (csrc/binding.cpp), which returns None for one that it leaves
+# to the code here: another GPU, a caller's output or workspace, or an argument that has to be refused.
 def qz_i8_pitch(cols) -> int:
     return lib().qz_i8_pitch(cols)
 
@@ -615,6 +617,10 @@ def qz_i8_quantize(X, colf=None, sums=False, values=False):
     """Rows of a matrix (bf16 or fp32, contiguous rows), times the column factors colf, to int8 with a
     scale each: (codes int8 [rows x pitch], scales fp32 [rows]), then with sums=True the rows' sums of
     codes (int32), and with values=True the numbers the codes stand for in X's dtype."""
+    if _lib.binding is not None:
+        r = _lib.binding.quantize(X, colf, sums, values)
+        if r is not None:
+            return r
     torch = _torch()
     ld = _matrix(X, "X")
     xt = _dtype_code(X)
@@ -668,6 +674,10 @@ def qz_i8_matmul(xcodes, xscales, codes, scales, d_i, zeros=None, xsums=None, bi
     """Y = X W^T + bias with X [n x d_i] and W [d_o x d_i] both as int8 rows.  zeros (the solvers'
     zero points of W, uint8 [d_o]) needs xsums, the row sums of X.  Y is out_dtype (bf16 or fp32;
     default bf16), or `out` is written."""
+    if out is None and ws is None and _lib.binding is not None:
+        r = _lib.binding.matmul(xcodes, xscales, codes, scales, d_i, zeros, xsums, bias, out_dtype)
+        if r is not None:
+            return r
     L = lib()
     _dev(xcodes, "X codes")
     n, d_o, dev = xcodes.shape[0], codes.shape[0], xcodes.device
@@ -697,6 +707,10 @@ def qz_i8_linear_workspace(n, d_o, d_i) -> int:
 def qz_i8_linear(X, codes, scales, zeros=None, colf=None, bias=None, out_dtype=None, out=None, ws=None):
     """Y = Q(X) W^T + bias: X (bf16 or fp32 [n x d_i], contiguous rows), times the column factors
     colf, is quantized per row in the same call; W [d_o x d_i] as int8 rows with zeros or without."""
+    if out is None and ws is None and _lib.binding is not None:
+        r = _lib.binding.linear(X, codes, scales, zeros, colf, bias, out_dtype)
+        if r is not None:
+            return r
     L = lib()
     ldx = _matrix(X, "X")
     xt = _dtype_code(X)
@@ -724,17 +738,20 @@ def qz_route(logits, top_k, scores="softmax", bias=None, groups=1, top_groups=1,
     or fp32 [n x E], contiguous rows).  scores "softmax" or "sigmoid"; bias fp32 [E] moves the choice
     alone; of `groups` groups the best top_groups stay, each counted by the sum of its group_best
     (1 or 2) largest choices; weights divided by their sum with renorm, times scale."""
+    if scores not in ("softmax", "sigmoid"):
+        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
+    flags = (_lib.QZ_ROUTE_SIGMOID if scores == "sigmoid" else 0) | (_lib.QZ_ROUTE_RENORM if renorm else 0)
+    if _lib.binding is not None:
+        r = _lib.binding.route(logits, top_k, flags, bias, groups, top_groups, group_best, scale)
+        if r is not None:
+            return r
     torch = _torch()
     ld = _matrix(logits, "logits")
     lt = _dtype_code(logits)
     n, E = logits.shape
-    if scores not in ("softmax", "sigmoid"):
-        raise ValueError(f"scores must be 'softmax' or 'sigmoid', not {scores!r}")
     k, index = _int32(top_k, "top_k"), logits.device.index
     p = QzRouter(C.sizeof(QzRouter), _int32(E, "the number of experts"), k, _int32(groups, "groups"),
-                 _int32(top_groups, "top_groups"), _int32(group_best, "group_best"),
-                 (_lib.QZ_ROUTE_SIGMOID if scores == "sigmoid" else 0) | (_lib.QZ_ROUTE_RENORM if renorm else 0),
-                 scale)
+                 _int32(top_groups, "top_groups"), _int32(group_best, "group_best"), flags, scale)
     ids = logits.new_empty((n, k if k > 0 else 0), dtype=torch.int32)
     w = logits.new_empty(ids.shape, dtype=torch.float32)
     _run(index, lib().qz_route, logits.data_ptr(), lt, n, ld, C.byref(p), _vector(bias, E, "bias", index),
@@ -751,6 +768,10 @@ def qz_i8_moe(X, ids, weights, gu_codes, gu_scales, dn_codes, dn_scales, gu_zero
     """The routed expert layer on int8 weights: X (bf16 or fp32 [n x d]), ids (int32) and weights (fp32)
     [n x top_k] as qz_route returns them, gate and up weights [E x 2f x d] and down weights [E x d x f]
     as int8 rows with zeros or without.  Returns Y bf16 [n x d]; ids outside [0, E) are skipped."""
+    if ws is None and _lib.binding is not None:
+        r = _lib.binding.moe(X, ids, weights, gu_codes, gu_scales, dn_codes, dn_scales, gu_zeros, dn_zeros)
+        if r is not None:
+            return r
     torch, L = _torch(), lib()
     ldx = _matrix(X, "X")
     xt = _dtype_code(X)

@@ -134,11 +134,14 @@ _SIGS = {
 }
 
 _lib = None
+binding = None      # the native calls (csrc/binding.cpp); None: every call through ctypes, to the same library
+_BINDING_ORDER = ("qz_i8_quantize", "qz_i8_matmul_workspace", "qz_i8_matmul", "qz_i8_linear_workspace",
+                  "qz_i8_linear", "qz_route", "qz_i8_moe_workspace", "qz_i8_moe")
 
 
 def load(path: str = LIB_PATH):
     """Load libqz.so and declare its signatures.  Raises if it is not built."""
-    global _lib
+    global _lib, binding
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -154,5 +157,9 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    if os.path.exists(os.path.join(_HERE, "_binding.so")):
+        from . import _binding
+        _binding.init(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _BINDING_ORDER))
+        binding = _binding
     _lib = lib
     return lib

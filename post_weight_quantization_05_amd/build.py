@@ -4,6 +4,9 @@ Every translation unit in csrc/ is compiled to an object under _build/ (in
 parallel), then linked into post_weight_quantization_05_amd/libqz.so together with
 rocSOLVER/rocBLAS (used only for the one-time eigendecomposition).  Always rebuilds.
 
+csrc/binding.cpp, the native calls of the package's Python functions, becomes _binding.so beside it (host
+code: g++, against the installed PyTorch's headers).
+
     python -m post_weight_quantization_05_amd.build
 """
 from __future__ import annotations
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqz.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = os.environ.get("QZ_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -46,6 +50,26 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> str:
+    import sysconfig
+
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    inc = os.path.join(base, "include")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", "/opt/rocm/include", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-L", os.path.join(base, "lib"), "-lc10", "-lc10_hip",
+           "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
@@ -53,7 +77,9 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
         raise RuntimeError("no HIP sources found")
     jobs = jobs or min(len(srcs), max(1, (os.cpu_count() or 4)), 16)
     with cf.ThreadPoolExecutor(jobs) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(_compile, srcs))
+        binding.result()
     tmp = LIB + ".tmp"
     r = subprocess.run([HIPCC, *LDFLAGS, *objs, "-o", tmp], capture_output=True, text=True)
     if r.returncode != 0:

@@ -57,7 +57,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
       }
       top = top8(v[c], top);
     }
-    load(row + step < rows ? row + step : row);
+    if (row + step < rows) load(row + step);
     top = wave_top(top);
     if constexpr (kWaves > 1) {
       if (lane == 0) tops[turn][wave] = top;

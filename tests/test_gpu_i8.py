@@ -569,3 +569,76 @@ def test_timing_kinds():
     finally:
         q.qz_timing_enable(False)
     assert {"i8_quantize", "i8_product", "route", "i8_moe"} <= set(got)
+
+
+# --------------------------------------------------------------------------- the native calls
+def test_native_and_interpreted_calls_agree(monkeypatch):
+    """The native binding is there, makes the ordinary calls, and gives the bytes that the Python code gives."""
+    from post_weight_quantization_05_amd import _lib
+    qz()
+    assert _lib.binding is not None
+    for n in (1, 20, 300):
+        run, _, _ = _program(n, 6)
+        native = run()
+        monkeypatch.setattr(_lib, "binding", None)
+        plain = run()
+        monkeypatch.undo()
+        assert len(native) == len(plain)
+        for a, b in zip(native, plain):
+            assert a.dtype == b.dtype and a.shape == b.shape and _t().equal(a, b)
+
+
+def test_native_calls_leave_the_rest_to_python():
+    """Anything out of the ordinary comes back as None, and the Python code says what is wrong."""
+    from post_weight_quantization_05_amd import _lib
+    q, torch = qz(), _t()
+    b = _lib.binding
+    x = torch.randn((4, 64), device="cuda")
+    c, s = q.qz_i8_quantize(x)
+    lo = torch.randn((4, 8), device="cuda")
+    for r in (b.quantize(x.cpu(), None, False, False), b.quantize(x.T, None, False, False), b.quantize(x.half(), None, False, False),
+              b.quantize(None, None, False, False), b.quantize(x, x[0, :3], False, False), b.quantize(x, None, 1, False),
+              b.quantize(x[:, :0], None, False, False), b.quantize(x), b.linear(x, c, s, None, None, None, torch.float16),
+              b.linear(x[:, :40], c[:, :100], s, None, None, None, None), b.linear(x, c, s[:3], None, None, None, None),
+              b.matmul(c, s, c, s, 129, None, None, None, None), b.matmul(c, s, c, s, 64.0, None, None, None, None),
+              b.matmul(c, s, c, s, 64, torch.zeros(4, dtype=torch.uint8, device="cuda"), None, None, None),
+              b.route(lo, 9, 0, None, 1, 1, 1, 1.0), b.route(lo, 2, 4, None, 1, 1, 1, 1.0), b.route(lo, 2 ** 40, 0, None, 1, 1, 1, 1.0),
+              b.route(lo, 2, 0, None, 3, 1, 1, 1.0), b.route(lo, 2, 0, None, 1, 1, 1, float("nan")), b.route(lo, 2, 0, lo[0, :4], 1, 1, 1, 1.0)):
+        assert r is None
+    with pytest.raises(ValueError, match="GPU"):
+        q.qz_i8_quantize(x.cpu())
+    with pytest.raises(ValueError, match="contiguous rows"):
+        q.qz_i8_quantize(x.T)
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        q.qz_i8_quantize(x.half())
+    with pytest.raises(ValueError, match="columns"):
+        q.qz_i8_quantize(x[:, :0])
+    with pytest.raises(ValueError, match="expected 4 rows"):
+        q.qz_i8_linear(x, c, s[:3])
+    with pytest.raises(TypeError, match="unsupported dtype"):
+        q.qz_i8_linear(x, c, s, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="row sums"):
+        q.qz_i8_matmul(c, s, c, s, 64, zeros=torch.zeros(4, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(q.QzError, match="top_k"):
+        q.qz_route(lo, 9)
+    with pytest.raises(q.QzError, match="n_groups"):
+        q.qz_route(lo, 2, groups=3)
+    with pytest.raises(ValueError, match="scores"):
+        q.qz_route(lo, 2, scores="tanh")
+    gu, dn = _layer(np.random.default_rng(0), 2, 64, 32, False)
+    ids, w = torch.zeros((4, 2), dtype=torch.int32, device="cuda"), torch.zeros((4, 2), device="cuda")
+    with pytest.raises(TypeError, match="ids must be int32"):
+        _run_layer(x, ids.long(), w, gu, dn)
+    with pytest.raises(ValueError, match="top_k"):
+        _run_layer(x, ids[:3], w[:3], gu, dn)
+    with pytest.raises(ValueError, match="down weights"):
+        _run_layer(x, ids, w, gu, tuple(None if m is None else m[:1] for m in dn))
+
+
+def test_inputs_that_need_gradients_are_read_as_values():
+    q, torch = qz(), _t()
+    x = torch.randn((5, 64), device="cuda", requires_grad=True)
+    c, s = q.qz_i8_quantize(x)
+    c2, s2 = q.qz_i8_quantize(x.detach())
+    y = q.qz_i8_linear(x, c, s)
+    assert torch.equal(c, c2) and torch.equal(s, s2) and not s.requires_grad and not y.requires_grad
