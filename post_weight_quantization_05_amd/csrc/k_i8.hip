@@ -8,6 +8,9 @@ namespace qz {
 
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
 // TPR threads a row, CH chunks of eight elements each, which stay in registers between the row's
 // maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier.
 // A workgroup goes through several rows: the next one is on its way while one is worked on, and the
@@ -34,15 +37,37 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
   const int64_t P = i8_pitch(cols), step = static_cast<int64_t>(gridDim.x - skip) * kRows;
   int64_t row = (blockIdx.x - skip) * (int64_t)kRows + (TPR == 64 ? wave : 0);
   if (row >= rows) return;
+  // Chunk c of this thread: eight neighbours, or in fp32 (VEC) four of them and four 4 TPR further on, so that
+  // a wavefront's 16 bytes a lane are whole lines.
+  constexpr bool kApart = VEC && WT == QZ_F32;
+  constexpr int kSecond = kApart ? 4 * TPR : 4;
+  auto place = [&](int c) { return static_cast<int64_t>(c * TPR * 8 + (kApart ? 4 : 8) * t); };
+  auto load_f32 = [&](const void* p, int64_t at, int64_t c) {
+    Raw8<QZ_F32> r;
+    if constexpr (kApart) {
+      const uint4 *a = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at + c),
+                  *b = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at + c + kSecond);
+      r.w[0] = c < cols ? *a : make_uint4(0, 0, 0, 0);
+      r.w[1] = c + kSecond < cols ? *b : make_uint4(0, 0, 0, 0);
+    } else {
+      r = load8<QZ_F32, VEC>(p, at + c, cols - c);
+    }
+    return r;
+  };
   float f[FACTORS ? CH : 1][8];
   if constexpr (FACTORS) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) numbers8(load8<QZ_F32, VEC>(colf, (c * TPR + t) * 8, cols - (c * TPR + t) * 8), f[c]);
+    for (int c = 0; c < CH; ++c) numbers8(load_f32(colf, 0, place(c)), f[c]);
   }
   Raw8<WT> raw[CH];
   auto load = [&](int64_t r) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) raw[c] = load8<WT, VEC>(X, r * ldx + (c * TPR + t) * 8, cols - (c * TPR + t) * 8);
+    for (int c = 0; c < CH; ++c) {
+      if constexpr (WT == QZ_F32)
+        raw[c] = load_f32(X, r * ldx, place(c));
+      else
+        raw[c] = load8<WT, VEC>(X, r * ldx + place(c), cols - place(c));
+    }
   };
   load(row);
   for (int turn = 0; row < rows; row += step, turn ^= 1) {
@@ -68,24 +93,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
     int sum = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-      const int64_t at = (c * TPR + t) * 8;
+      const int64_t at = place(c);
       if (at >= P) continue;
       float q[8];
       const uint2 w = codes8(v[c], sc, q);
-      *reinterpret_cast<uint2*>(codes + row * P + at) = w;
-      sum = add_codes(w.x, add_codes(w.y, sum));
+      sum = add_codes(w.x, add_codes(w.y, sum));   // (zeros past the columns)
+      int8_t* const to = codes + row * P + at;
+      if constexpr (kApart) {
+        *reinterpret_cast<uint32_t*>(to) = w.x;
+        if (at + kSecond < P) *reinterpret_cast<uint32_t*>(to + kSecond) = w.y;
+      } else {
+        *reinterpret_cast<uint2*>(to) = w;
+      }
       if (!values || at >= cols) continue;
       const int64_t o = row * cols + at;
-      if constexpr (VEC) {
+      if constexpr (VEC) {   // written past the caches: nothing here reads them again
         if constexpr (WT == QZ_BF16) {
-          uint32_t u[4];
+          u32x4 u;
 #pragma unroll
           for (int i = 0; i < 4; ++i) u[i] = bf16_pair(q[2 * i] * sc.s, q[2 * i + 1] * sc.s);
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(values) + o) = make_uint4(u[0], u[1], u[2], u[3]);
+          __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(static_cast<uint16_t*>(values) + o));
         } else {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(values) + o);
-          d[0] = make_float4(q[0] * sc.s, q[1] * sc.s, q[2] * sc.s, q[3] * sc.s);
-          d[1] = make_float4(q[4] * sc.s, q[5] * sc.s, q[6] * sc.s, q[7] * sc.s);
+          float* const d = static_cast<float*>(values) + o;
+          __builtin_nontemporal_store(f32x4{q[0] * sc.s, q[1] * sc.s, q[2] * sc.s, q[3] * sc.s}, reinterpret_cast<f32x4*>(d));
+          if (at + kSecond < cols)
+            __builtin_nontemporal_store(f32x4{q[4] * sc.s, q[5] * sc.s, q[6] * sc.s, q[7] * sc.s}, reinterpret_cast<f32x4*>(d + kSecond));
         }
       } else {
 #pragma unroll
