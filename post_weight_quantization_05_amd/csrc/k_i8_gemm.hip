@@ -392,7 +392,10 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
         const i32x4 v = rd16(out + t * T::kOutPitch + 16 * k);
         uint8_t* const dst = ybase + (yr * p.ldy + wr0 + e0) * osize;
         if (lines && wr0 + e0 + 16 / osize <= p.d_o) {
-          *reinterpret_cast<i32x4*>(dst) = v;
+          if constexpr (FORM == kPlain)   // past the caches: the next launch reads hidden rows and pairs' results
+            __builtin_nontemporal_store(v, reinterpret_cast<i32x4*>(dst));
+          else
+            *reinterpret_cast<i32x4*>(dst) = v;
         } else if (osize == 4) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
