@@ -544,7 +544,8 @@ int qz_route(const void* logits, int32_t lt, int64_t n, int64_t ldl, const qz_ro
  *   gu_codes/gu_scales/gu_zeros: [n_experts x 2 f] rows of d columns, gate rows before up rows;
  *   dn_codes/dn_scales/dn_zeros: [n_experts x d] rows of f columns; zeros nullable.  Y [n x d] bf16,
  *   dense.  Must not overlap the inputs.
- *   1 <= n_experts <= 512, 1 <= top_k <= 16, n <= 2^20 and n pitch(d) < 2^31, d and f <= 65536.
+ *   1 <= n_experts <= 512, 1 <= top_k <= 16, n <= 2^20, d and f <= 65536, n pitch(d) < 2^31 and
+ *   f pitch(d) < 2^31.
  *   ws: qz_i8_moe_workspace(...) bytes, 256-byte aligned; calls that may overlap need different
  *   workspaces.  Asynchronous.                                                                 */
 size_t qz_i8_moe_workspace(int64_t n, int64_t d, int64_t f, int32_t n_experts, int32_t top_k);

@@ -95,23 +95,23 @@ def moe(x, ids, weights, gu, dn, f):
     qx, sx = quantize(x)
     pick = lambda m, e: (m[0][e], m[1][e], None if m[2] is None else m[2][e])  # noqa: E731
     y, slack = np.zeros((n, dn[0].shape[1])), np.zeros((n, dn[0].shape[1]))
-    for t in range(n):
-        for r in range(k):
-            e = int(ids[t, r])
-            if not 0 <= e < E:
-                continue
-            v = product(qx[t:t + 1], sx[t:t + 1], *pick(gu, e))[0]
-            g, u = v[:f], v[f:]
-            h = gated(g, u)
-            s = np.abs(h).max() / 127
-            q = h / s if s > 0 else h * 0
-            code = np.clip(np.rint(q), -127, 127)
-            off = 2 * (24 + 4 * np.abs(g).max()) * 2.0 ** -24 * np.abs(q)
-            near = np.abs(np.abs(q - np.trunc(q)) - 0.5) <= off
-            w = float(weights[t, r])
-            c, ws, z = pick(dn, e)
-            level = levels(c, z).astype(np.float64)
-            y[t] += w * ws * s * (level @ code)
-            slack[t] += abs(w) * ws * s * (np.abs(level) @ near)
-            slack[t] += abs(w) * ws * s * (off.max() / 127 + 2.0 ** -20) * np.abs(level @ code)
+    for e in range(E):
+        t, r = np.nonzero(ids == e)
+        if not len(t):
+            continue
+        v = product(qx[t], sx[t], *pick(gu, e))
+        g, u = v[:, :f], v[:, f:]
+        h = gated(g, u)
+        s = np.abs(h).max(1, keepdims=True) / 127
+        q = np.divide(h, s, out=np.zeros_like(h), where=s > 0)
+        code = np.clip(np.rint(q), -127, 127)
+        off = 2 * (24 + 4 * np.abs(g).max(1, keepdims=True)) * 2.0 ** -24 * np.abs(q)
+        near = np.abs(np.abs(q - np.trunc(q)) - 0.5) <= off
+        w = weights[t, r].astype(np.float64)[:, None]
+        c, ws, z = pick(dn, e)
+        level = levels(c, z).astype(np.float64).T
+        main = code @ level
+        np.add.at(y, t, w * ws * s * main)
+        np.add.at(slack, t, np.abs(w) * ws * s * (near @ np.abs(level)
+                                                  + (off.max(1, keepdims=True) / 127 + 2.0 ** -20) * np.abs(main)))
     return y, slack

@@ -4,6 +4,7 @@
 #include <cstdint>
 #include <string>
 
+#include "i8_plan.h"
 #include "qz_internal.h"
 
 using namespace qz;
@@ -12,7 +13,8 @@ namespace {
 
 constexpr int64_t kMaxRows = int64_t(1) << 24;     // of W
 constexpr int64_t kMaxTokens = int64_t(1) << 20;
-constexpr int64_t kMaxLayerBytes = int64_t(1) << 31;   // the codes of an expert layer's tokens
+// The codes of an expert layer's tokens, and of an expert's gate rows: 32-bit offsets reach the up rows.
+constexpr int64_t kMaxLayerBytes = int64_t(1) << 31;
 
 bool float_type(int t) { return t == QZ_BF16 || t == QZ_F32; }
 bool aligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -54,20 +56,6 @@ int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i, const in
   return QZ_OK;
 }
 
-// Few tokens: one launch that quantizes them itself and needs no workspace.
-bool i8_by_rows(int64_t n, int64_t P) { return n <= 4 && i8_rows_fits(n, P); }
-
-// Few pairs of an expert layer, each with its expert's rows alone, in two launches: where the weights that
-// several tokens ask for, read once for each, take less time (at 5.2 TB/s) than four more launches and what
-// they do (16 us).
-bool moe_by_rows(int64_t n, int64_t d, int64_t f, int E, int k) {
-  const int64_t pairs = n * k;
-  if (pairs > 256 || !i8_rows_fits(1, i8_pitch(d)) || !i8_rows_fits(k, i8_pitch(f))) return false;
-  const double part = k < E ? 1. - static_cast<double>(k) / E : 0.;
-  const double reached = E * (1. - std::pow(part, static_cast<double>(n)));   // experts, on average
-  return (pairs - reached) * 3. * d * f < 16. * 5.2e6;
-}
-
 // X quantized, and the product's own workspace.
 struct LinearWs {
   int8_t* codes;
@@ -100,7 +88,7 @@ MoeWs moe_ws(void* base, int64_t n, int64_t d, int64_t f, int E, int k) {
   MoeWs w{};
   const size_t pairs = static_cast<size_t>(n) * k;
   w.h = c.take<float>(pairs * round_up(f, 4));
-  if (moe_by_rows(n, d, f, E, k)) {
+  if (i8_moe_by_rows(n, d, f, E, k)) {
     w.bytes = c.used;
     return w;
   }
@@ -124,6 +112,7 @@ int check_moe(int64_t n, int64_t d, int64_t f, int32_t E, int32_t k) {
     return fail(QZ_EINVAL, "i8_moe: need 0 <= n <= 2^20, 1 <= d <= 65536, 1 <= f <= 65536");
   if (n * i8_pitch(d) >= kMaxLayerBytes)
     return fail(QZ_EINVAL, "i8_moe: n pitch(d) must be below 2^31 (more tokens: in parts)");
+  if (f * i8_pitch(d) >= kMaxLayerBytes) return fail(QZ_EINVAL, "i8_moe: f pitch(d) must be below 2^31");
   return QZ_OK;
 }
 
@@ -319,7 +308,7 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   p.Y = w.h;
   p.yt = QZ_F32;
   p.ldy = round_up(f, 4);
-  if (moe_by_rows(n, d, f, n_experts, top_k)) {
+  if (i8_moe_by_rows(n, d, f, n_experts, top_k)) {
     p.ids = ids;
     p.raw = X;
     p.rt = xt;
@@ -345,7 +334,7 @@ int qz_i8_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int6
   p.W = dn_codes;
   p.sw = dn_scales;
   p.zeros = dn_zeros;
-  if (moe_by_rows(n, d, f, n_experts, top_k)) {
+  if (i8_moe_by_rows(n, d, f, n_experts, top_k)) {
     p.Y = Y;
     p.ldy = d;
     return launch_i8_rows_down(p, n, stream);

@@ -1,11 +1,93 @@
-// Plan of a product of 8-bit integer rows: the choice of a kernel from the sizes.  Plain C++, so that
-// host programs can include it.
+// Plan of a product of 8-bit integer rows: the kernels' shapes, what their wavefronts wait for, and the
+// choice of a kernel from the sizes.  Plain C++, so that host programs can include it.
 #pragma once
 
+#include <cmath>
 #include <cstdint>
 
 namespace qz {
 
+// ------------------------------------------------------------------------------- tile kernels
+// Workgroup tile of BM rows of W by BN rows of X, BM = 32 MT WM, BN = 32 NT WN, in WM x WN wavefronts
+// of 32 MT x 32 NT each.  The contraction goes in stages of 128 columns: whole lines of both.
+template <int WM_, int WN_, int MT_, int NT_, int LDS_KB>
+struct TileI8 {
+  static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
+  static constexpr int kHalfW = BM / 2 * 128, kHalf = (BM + BN) / 2 * 128;   // bytes
+  static constexpr int kFit = LDS_KB * 1024 / kHalf, kRing = kFit < 16 ? kFit : 16;   // halves of a stage in LDS
+  static constexpr int kCopiesW = BM / 16 / kWaves, kCopiesX = BN / 16 / kWaves;   // of a half, a wavefront
+  static constexpr int kCopies = kCopiesW + kCopiesX;
+  static constexpr int kProducts = MT * NT, kReads = MT + NT;   // of a step of 32 columns
+  static constexpr int kSteps = MT * NT <= 4 ? 4 : 1;           // whose operands are read ahead
+  static_assert(BM % (16 * kWaves) == 0 && BN % (16 * kWaves) == 0 && kRing >= 5);
+  static constexpr int kOutPitch = 32 * MT * 4 + 16;
+  static constexpr int kOut = kWaves * 32 * kOutPitch;
+  static constexpr int kUsed = kRing * kHalf;
+  static constexpr int kShared = kUsed > kOut + 12 * BM ? kUsed : kOut + 12 * BM;
+  static_assert(kShared <= 160 * 1024);
+};
+using Tile256x256 = TileI8<2, 4, 4, 2, 160>;
+using Tile256x128 = TileI8<4, 2, 2, 2, 160>;
+using Tile128x128 = TileI8<2, 2, 2, 2, 80>;
+using Tile128x64 = TileI8<2, 2, 2, 1, 80>;
+using Tile64x64 = TileI8<2, 2, 1, 1, 80>;
+using Tile64x64By4 = TileI8<2, 2, 1, 1, 40>;
+
+// Half p of the stages (2 st and 2 st + 1 of stage st) lies at place p % kRing of LDS.  Halves
+// 0 .. kRing - 1 go out first; at the join of stage st its places are free, and halves 2 st + kRing and
+// 2 st + kRing + 1 go out behind it.  Copies land in the order of their issue, and stage st + 1 has to have
+// landed at the join: where both halves of every join so far were there to issue, the kRing - 4 halves
+// behind it may be in flight; towards the end nothing may.
+template <class T>
+constexpr int tile_in_flight(int st, int halves) {
+  return 2 * st + T::kRing + 1 < halves ? (T::kRing - 4) * T::kCopies : 0;
+}
+// Before the first stage: all halves but its own two.
+template <class T>
+constexpr int tile_in_flight_first(int halves) {
+  return T::kRing <= halves ? (T::kRing - 2) * T::kCopies : 0;
+}
+
+// ---------------------------------------------------------------- very few tokens (k_i8_rows.hip)
+// LDS of a workgroup for its tokens' codes, besides some for the sums.
+constexpr int64_t kI8RowsLds = 56 * 1024;
+inline bool i8_rows_fit(int64_t rows, int64_t pitch) { return rows * ((pitch + 1023) / 1024 * 1024) <= kI8RowsLds; }
+
+// A product of one to four tokens: one launch, which quantizes them itself and needs no workspace.
+inline bool i8_by_rows(int64_t n, int64_t pitch) { return n <= 4 && i8_rows_fit(n, pitch); }
+
+// Few pairs of an expert layer, each with its expert's rows alone, in two launches: where the weights that
+// several tokens ask for, read once for each, take less time (at 5.2 TB/s) than three more launches and what
+// they do (16 us).
+inline bool i8_moe_by_rows(int64_t n, int64_t d, int64_t f, int experts, int k) {
+  const int64_t pairs = n * k;
+  if (pairs > 256 || !i8_rows_fit(1, (d + 127) / 128 * 128) || !i8_rows_fit(k, (f + 127) / 128 * 128)) return false;
+  const double part = k < experts ? 1. - static_cast<double>(k) / experts : 0.;
+  const double reached = experts * (1. - std::pow(part, static_cast<double>(n)));   // on average
+  return (pairs - reached) * 3. * d * f < 16. * 5.2e6;
+}
+
+// -------------------------------------------------------------------------- few-token kernels
+// Each wavefront streams its part of the contraction through LDS of its own, 128 columns a stage,
+// kDepth stages deep: whole lines of both operands, no registers in flight and no barrier before the
+// sums are joined.  kGateUp: the first half of the rows are gate rows, the second their up rows.
+template <int RT_, int NT_, int WAVES_, int LDS_KB>
+struct FewI8 {
+  static constexpr int RT = RT_, NT = NT_, kWaves = WAVES_;
+  static constexpr int kCopies = 2 * (RT + NT);             // of a stage, 1024 bytes each
+  static constexpr int kStage = kCopies * 1024;
+  static constexpr int kFit = LDS_KB * 1024 / kWaves / kStage, kDepth = kFit < 8 ? kFit : 8;
+  static constexpr int kLds = kWaves * kDepth * kStage;
+  static_assert(kDepth >= 3 && kLds >= kWaves * RT * NT * 1024);
+};
+using Few11 = FewI8<1, 1, 4, 80>;
+using Few21 = FewI8<2, 1, 4, 80>;
+using Few22 = FewI8<2, 2, 4, 160>;
+using Few24 = FewI8<2, 4, 4, 160>;
+
+// ------------------------------------------------------------------------- choice of a kernel
 // kFewRN: 16 R rows of W by 16 N of X, four wavefronts that share the contraction (k_i8_few.hip);
 // kBMxBN: tiles (k_i8_gemm.hip); by4: with LDS for four workgroups a compute unit, not two.
 enum class I8Kind { kFew11, kFew21, kFew22, kFew24, k256x256, k256x128, k128x128, k128x64, k64x64, k64x64by4 };

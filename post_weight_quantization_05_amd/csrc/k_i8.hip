@@ -179,7 +179,7 @@ int quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx, con
   const bool through = colf || xt == QZ_BF16;
   auto go = [&](auto kernel, int tpr) {
     const int64_t groups = tpr == 64 ? ceil_div(rows, 4) : rows;
-    const int64_t most = through ? 256 * (tpr < 256 ? 8 : 2048 / tpr) : groups;
+    const int64_t most = through ? 256 * (tpr < 256 ? 8 : 2048 / tpr) : int64_t{1} << 20;   // a launch's limit
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((groups < most ? groups : most) + (GROUP ? g.E : 0))),
                        dim3(tpr < 256 ? 256 : tpr), 0, s, X, rows, cols, ldx, colf, codes, scales, sums, values, g);
     return check_launch("i8_quantize");

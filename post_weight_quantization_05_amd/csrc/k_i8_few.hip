@@ -10,19 +10,6 @@ namespace qz {
 
 namespace {
 
-// Each wavefront streams its part of the contraction through LDS of its own, 128 columns a stage,
-// kDepth stages deep: whole lines of both operands, no registers in flight and no barrier before the
-// sums are joined.  kGateUp: the first half of the rows are gate rows, the second their up rows.
-template <int RT_, int NT_, int WAVES_, int LDS_KB>
-struct FewI8 {
-  static constexpr int RT = RT_, NT = NT_, kWaves = WAVES_;
-  static constexpr int kCopies = 2 * (RT + NT);             // of a stage, 1024 bytes each
-  static constexpr int kStage = kCopies * 1024;
-  static constexpr int kFit = LDS_KB * 1024 / kWaves / kStage, kDepth = kFit < 8 ? kFit : 8;
-  static constexpr int kLds = kWaves * kDepth * kStage;
-  static_assert(kDepth >= 3 && kLds >= kWaves * RT * NT * 1024);
-};
-
 // Until at most N copies of this wavefront are in flight.
 template <int N>
 __device__ __forceinline__ void wait_copies() {
@@ -202,10 +189,10 @@ static int launch_few(const I8Product& p, hipStream_t s) {
 template <Form FORM>
 static int by_kind(I8Kind kind, const I8Product& p, hipStream_t s) {
   switch (kind) {
-    case I8Kind::kFew11: if constexpr (FORM != kGateUp) return launch_few<FORM, FewI8<1, 1, 4, 80>>(p, s); break;
-    case I8Kind::kFew21: return launch_few<FORM, FewI8<2, 1, 4, 80>>(p, s);
-    case I8Kind::kFew22: return launch_few<FORM, FewI8<2, 2, 4, 160>>(p, s);
-    case I8Kind::kFew24: return launch_few<FORM, FewI8<2, 4, 4, 160>>(p, s);
+    case I8Kind::kFew11: if constexpr (FORM != kGateUp) return launch_few<FORM, Few11>(p, s); break;
+    case I8Kind::kFew21: return launch_few<FORM, Few21>(p, s);
+    case I8Kind::kFew22: return launch_few<FORM, Few22>(p, s);
+    case I8Kind::kFew24: return launch_few<FORM, Few24>(p, s);
     default: break;
   }
   return fail(QZ_EHIP, "i8_few: no kernel");

@@ -22,28 +22,6 @@ __device__ __forceinline__ void each(F&& f) {
   each_of(f, std::make_integer_sequence<int, N>{});
 }
 
-// ---------------------------------------------------------------------------- large products
-// Workgroup tile of BM rows of W by BN rows of X, BM = 32 MT WM, BN = 32 NT WN, in WM x WN wavefronts
-// of 32 MT x 32 NT each.  The contraction goes in stages of 128 columns: whole lines of both.
-template <int WM_, int WN_, int MT_, int NT_, int LDS_KB>
-struct TileI8 {
-  static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
-  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  static constexpr int BM = 32 * MT * WM, BN = 32 * NT * WN;
-  static constexpr int kHalfW = BM / 2 * 128, kHalf = (BM + BN) / 2 * 128;   // bytes
-  static constexpr int kFit = LDS_KB * 1024 / kHalf, kRing = kFit < 16 ? kFit : 16;   // halves of a stage in LDS
-  static constexpr int kCopiesW = BM / 16 / kWaves, kCopiesX = BN / 16 / kWaves;   // of a half, a wavefront
-  static constexpr int kCopies = kCopiesW + kCopiesX;
-  static constexpr int kProducts = MT * NT, kReads = MT + NT;   // of a step of 32 columns
-  static constexpr int kSteps = MT * NT <= 4 ? 4 : 1;           // whose operands are read ahead
-  static_assert(BM % (16 * kWaves) == 0 && BN % (16 * kWaves) == 0 && kRing >= 5);
-  static constexpr int kOutPitch = 32 * MT * 4 + 16;
-  static constexpr int kOut = kWaves * 32 * kOutPitch;
-  static constexpr int kUsed = kRing * kHalf;
-  static constexpr int kShared = kUsed > kOut + 12 * BM ? kUsed : kOut + 12 * BM;
-  static_assert(kShared <= 160 * 1024);
-};
-
 template <Form FORM, class T>
 __global__ __launch_bounds__(T::kThreads, T::kWaves / 4 * (T::kShared <= 80 * 1024 ? 2 : 1))
 void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
@@ -223,8 +201,8 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
     constexpr int ii = decltype(i)::value;
     if (ii < halves) copy_half(integral_constant<int, ii % 2>{}, ii / 2, ii);
   });
-  if (H <= halves)
-    wait_and_join<(H - 2) * T::kCopies>();
+  if (tile_in_flight_first<T>(halves))
+    wait_and_join<tile_in_flight_first<T>(H)>();
   else
     wait_and_join<0>();
 
@@ -244,7 +222,7 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
     auto stage = [&](auto set, auto full) {   // full: with the copies of both halves
       constexpr bool kFull = decltype(full)::value;
       constexpr int s = decltype(set)::value;
-      wait_and_join<kFull ? (H - 4) * T::kCopies : 0>();
+      wait_and_join<kFull ? tile_in_flight<T>(0, H + 2) : 0>();   // what tile_in_flight says for st
       const int next = wrap(at + 2), at1 = wrap(at + 1), far = st + H / 2;
       lds_u8* const aw = lds + wrap(next + wh) * T::kHalf + in_w;
       lds_u8* const ax = lds + wrap(next + xh) * T::kHalf + in_x;
@@ -273,7 +251,7 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
       at = next;
       ++st;
     };
-    while (2 * st + H + 3 < halves) {   // two whole stages
+    while (tile_in_flight<T>(st + 1, halves)) {   // two whole stages
       stage(Set0{}, std::true_type{});
       stage(Set1{}, std::true_type{});
     }
@@ -297,9 +275,9 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
     step(Set1{}, aw, ax, chunk_at(2), std::true_type{}, nothing);
     step(Set0{}, aw, ax, chunk_at(3), std::true_type{}, nothing);
   };
-  for (; 2 * st + H + 1 < halves; ++st) {
+  for (; tile_in_flight<T>(st, halves); ++st) {
     first_steps(lds + wrap(at + wh) * T::kHalf + in_w, lds + wrap(at + xh) * T::kHalf + in_x);
-    wait_and_join<(H - 4) * T::kCopies>();
+    wait_and_join<tile_in_flight<T>(0, H + 2)>();   // what it says for st
     const int next = wrap(at + 2), at1 = wrap(at + 1);
     const int far = st + H / 2;   // stage of half 2 st + H
     step(Set1{}, lds + wrap(next + wh) * T::kHalf + in_w, lds + wrap(next + xh) * T::kHalf + in_x, chunk_at(0),
@@ -432,7 +410,7 @@ int launch_tile(const I8Product& p, hipStream_t s) {
   QZ_TRY(allowed.ask(reinterpret_cast<const void*>(kernel), T::kShared));
   const int64_t tw = ceil_div(p.d_o, FORM == kGateUp ? T::BM / 2 : T::BM);
   const int64_t tx = FORM == kPlain ? ceil_div(p.n, T::BN) : most_tiles(p, T::BN);
-  if (tw * tx > 0x7fffffff) return fail(QZ_EINVAL, "i8_product: too many tiles");
+  if (tw * tx > 0xffffffffll / T::kThreads) return fail(QZ_EINVAL, "i8_product: too many tiles");   // a launch's limit
   hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(tw * tx)), dim3(T::kThreads), T::kShared, s, p,
                      static_cast<int>(tw), static_cast<int>(tx));
   return check_launch("i8_tile");
@@ -442,12 +420,12 @@ template <Form FORM>
 int launch(const I8Product& p, hipStream_t s) {
   const I8Kind kind = i8_choose(p.n, p.d_o * (FORM == kGateUp ? 2 : 1), p.P / 128, FORM == kPlain ? 0 : p.E, FORM == kGateUp);
   switch (kind) {
-    case I8Kind::k256x256: return launch_tile<FORM, TileI8<2, 4, 4, 2, 160>>(p, s);
-    case I8Kind::k256x128: return launch_tile<FORM, TileI8<4, 2, 2, 2, 160>>(p, s);
-    case I8Kind::k128x128: return launch_tile<FORM, TileI8<2, 2, 2, 2, 80>>(p, s);
-    case I8Kind::k128x64: return launch_tile<FORM, TileI8<2, 2, 2, 1, 80>>(p, s);
-    case I8Kind::k64x64: if constexpr (FORM != kGateUp) return launch_tile<FORM, TileI8<2, 2, 1, 1, 80>>(p, s); break;
-    case I8Kind::k64x64by4: if constexpr (FORM != kGateUp) return launch_tile<FORM, TileI8<2, 2, 1, 1, 40>>(p, s); break;
+    case I8Kind::k256x256: return launch_tile<FORM, Tile256x256>(p, s);
+    case I8Kind::k256x128: return launch_tile<FORM, Tile256x128>(p, s);
+    case I8Kind::k128x128: return launch_tile<FORM, Tile128x128>(p, s);
+    case I8Kind::k128x64: return launch_tile<FORM, Tile128x64>(p, s);
+    case I8Kind::k64x64: if constexpr (FORM != kGateUp) return launch_tile<FORM, Tile64x64>(p, s); break;
+    case I8Kind::k64x64by4: if constexpr (FORM != kGateUp) return launch_tile<FORM, Tile64x64By4>(p, s); break;
     default: return launch_i8_few(kind, FORM, p, s);
   }
   return fail(QZ_EHIP, "i8_product: no kernel");

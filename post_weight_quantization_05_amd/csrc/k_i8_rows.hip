@@ -348,11 +348,6 @@ int by_type(const I8Product& p, int64_t y, hipStream_t s) {
 
 }  // namespace
 
-// LDS of a workgroup for the tokens' codes.
-constexpr int64_t kRowsLds = 56 * 1024;   // besides it, some for the sums
-
-bool i8_rows_fits(int64_t rows, int64_t P) { return rows * round_up(P, 1024) <= kRowsLds; }
-
 int launch_i8_rows(const I8Product& p, hipStream_t s) { return by_type<kPlain>(p, 1, s); }
 int launch_i8_rows_gate_up(const I8Product& p, hipStream_t s) { return by_type<kGateUp>(p, p.n, s); }
 int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s) {

@@ -334,8 +334,6 @@ int launch_i8_product(const I8Product& p, hipStream_t s);
 int launch_i8_gate_up(const I8Product& p, hipStream_t s);
 // Y[pair] = pair_weight[pair] * product, fp32 [pairs x ldy]
 int launch_i8_down(const I8Product& p, hipStream_t s);
-// rows of X that the few-token kernels can hold at once
-bool i8_rows_fits(int64_t rows, int64_t P);
 // Y = X W^T for n <= 4
 int launch_i8_rows(const I8Product& p, hipStream_t s);
 // h[pair] = silu(gate) up for n pairs (those whose id is an expert), X by token

@@ -158,6 +158,31 @@ def test_matmul_exact(n, d_i, d_o, out):
     _same(got, _t().from_numpy(y).float().to(_dtype(out)).float().numpy())
 
 
+# Sizes at which every kernel of the products is chosen (tests/test_i8_plan.py says which).
+REACH_PRODUCTS = [(5, 128, 64), (5, 128, 4100), (17, 128, 64), (17, 256, 4100), (33, 640, 4100), (100, 1024, 4100),
+                  (150, 1024, 6200), (400, 2048, 6200), (700, 640, 6200), (1300, 640, 6200)]
+
+
+@pytest.mark.parametrize("n,d_i,d_o", REACH_PRODUCTS)
+@pytest.mark.parametrize("zeroed,out", [(False, "bf16"), (False, "f32"), (True, "bf16"), (True, "f32")])
+def test_matmul_exact_by_every_kernel(n, d_i, d_o, zeroed, out):
+    q, torch = qz(), _t()
+    rng = np.random.default_rng([n, d_i, d_o])
+    top = int(np.sqrt(2.0 ** 23 / d_i / 4))
+    xq, wq = _stored(rng, n, d_i, -top, top), _stored(rng, d_o, d_i, -top, top)
+    zeros = rng.integers(128 - top, 129 + top, d_o).astype(np.uint8) if zeroed else None
+    bias = rng.integers(-50, 50, d_o).astype(np.float32) if zeroed else None
+    sx, sw = _powers(rng, n), _powers(rng, d_o)
+    xd, wd = to_dev(i8.padded(xq)), to_dev(i8.padded(wq))
+    # fp32 products of whole numbers below 2^24 are exact, whatever their order
+    level = wd[:, :d_i].float() + (0 if zeros is None else 128.0 - to_dev(zeros).float()[:, None])
+    want = xd[:, :d_i].float() @ level.T * to_dev(sx)[:, None] * to_dev(sw) + (0 if bias is None else to_dev(bias))
+    got = q.qz_i8_matmul(xd, to_dev(sx), wd, to_dev(sw), d_i, zeros=None if zeros is None else to_dev(zeros),
+                         xsums=to_dev(xq.astype(np.int64).sum(1).astype(np.int32)),
+                         bias=None if bias is None else to_dev(bias), out_dtype=_dtype(out))
+    assert torch.equal(got, want.to(_dtype(out)))
+
+
 def test_matmul_of_the_largest_sums():
     """65536 columns of extreme codes: sums up to 65536 * 128 * 255 = 2^31 - 2^23, in integers."""
     q = qz()
@@ -370,6 +395,24 @@ def test_moe(n, E, k, d, f, zeroed, dtype):
     ids = np.stack([rng.permutation(E)[:k] for _ in range(n)]).astype(np.int32)
     w = rng.random((n, k)).astype(np.float32)
     _check_layer(x, xd, ids, w, gu, dn, f)
+
+
+# (n, E, k, d, f) at which every kernel of the layer's products is chosen (tests/test_i8_plan.py).
+REACH_LAYERS = [(100, 4, 4, 64, 64), (100, 4, 4, 64, 520), (100, 16, 4, 64, 128), (130, 2, 2, 64, 520), (130, 64, 2, 128, 520),
+                (5, 4, 4, 4100, 1030), (33, 2, 2, 2050, 520), (64, 2, 2, 2050, 520), (100, 4, 4, 64, 2050),
+                (300, 4, 4, 64, 2050), (300, 16, 1, 640, 1030), (600, 4, 4, 64, 2050), (600, 4, 4, 4100, 64),
+                (1300, 4, 4, 640, 520), (1300, 16, 2, 2050, 64), (3, 8, 2, 200, 96), (2, 8, 1, 200, 96), (40, 64, 6, 128, 64)]
+
+
+@pytest.mark.parametrize("n,E,k,d,f", REACH_LAYERS)
+@pytest.mark.parametrize("zeroed", [False, True])
+def test_moe_by_every_kernel(n, E, k, d, f, zeroed):
+    rng = np.random.default_rng([n, E, k, d])
+    x, xd = _rounded(rng.standard_normal((n, d)), "bf16")
+    gu, dn = _layer(rng, E, d, f, zeroed)
+    ids = np.argsort(rng.random((n, E)), axis=1)[:, :k].astype(np.int32)
+    ids[rng.random((n, k)) < 0.05] = -1
+    _check_layer(x, xd, ids, rng.random((n, k)).astype(np.float32), gu, dn, f)
 
 
 @pytest.mark.parametrize("n", [1, 6, 90, 400])

@@ -205,7 +205,7 @@ MOE = [A, 0, 4, 16, 16, 32, 8, 2, A, A, A, A, A, A, A, A, A, A, 1 << 40]
 
 @pytest.mark.parametrize("change,what", [
     ({1: 2}, "dtype"), ({2: -1}, "need"), ({2: 2 ** 20 + 1}, "need"), ({3: 15}, "ldx"), ({4: 0}, "need"),
-    ({4: 65537}, "need"), ({5: 0}, "need"), ({5: 65537}, "need"), ({6: 0}, "n_experts"), ({6: 513}, "n_experts"),
+    ({4: 65537}, "need"), ({5: 0}, "need"), ({5: 65537}, "need"), ({3: 65536, 4: 65536, 5: 32768}, "f pitch"), ({6: 0}, "n_experts"), ({6: 513}, "n_experts"),
     ({7: 0}, "top_k"), ({7: 17}, "top_k"), ({2: 2 ** 20, 3: 4096, 4: 4096}, "in parts"), ({0: None}, "null"),
     ({8: None}, "null"), ({9: None}, "null"), ({10: None}, "null"), ({11: None}, "null"), ({13: None}, "null"),
     ({14: None}, "null"), ({16: None}, "null"), ({10: C.c_void_p(4104)}, "16-byte"), ({13: C.c_void_p(4104)}, "16-byte"),
