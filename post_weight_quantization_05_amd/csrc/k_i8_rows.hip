@@ -277,9 +277,11 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
   i32x4 even[R], odd[R];
   load(0, even);
   load(1, odd);
-  if constexpr (SPLIT == 4) {   // each wavefront its own; its LDS accesses stay in order
+  if constexpr (SPLIT == 4) {   // each wavefront its own: its LDS accesses stay in order, the compiler's too
     for (int i = wave; i < p.k; i += 4) stage_row<QZ_F32, VEC, 64>(p, pair0 + i, i, lane, s, nullptr);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   } else {
     stage_rows<QZ_F32, VEC>(p, pair0, p.k, s, tops);
   }

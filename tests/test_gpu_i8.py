@@ -685,3 +685,72 @@ def test_inputs_that_need_gradients_are_read_as_values():
     c2, s2 = q.qz_i8_quantize(x.detach())
     y = q.qz_i8_linear(x, c, s)
     assert torch.equal(c, c2) and torch.equal(s, s2) and not s.requires_grad and not y.requires_grad
+
+
+# ----------------------------------------------------------------- offsets past 32 bits
+def test_long_quantisation_rows_stand_alone():
+    """4.5 GB of rows, more than a launch has workgroups: the last rows as by themselves."""
+    q, torch = qz(), _t()
+    x = torch.randn(((1 << 20) + 1029, 1040), device="cuda", dtype=torch.float32)
+    for colf in (None, torch.rand(1040, device="cuda") + 0.5):
+        c, s, n, v = q.qz_i8_quantize(x, colf=colf, sums=True, values=True)
+        for part in (slice(0, 999), slice(1 << 20, None)):
+            for a, b in zip((c, s, n, v), q.qz_i8_quantize(x[part].contiguous(), colf=colf, sums=True, values=True)):
+                assert torch.equal(a[part], b)
+
+
+@pytest.mark.parametrize("n", [1, 4, 20, 300])
+def test_long_weights(n):
+    """W of 4.5 GB: its first and last rows as by themselves (every rounding is the same in every kernel)."""
+    q, torch = qz(), _t()
+    d, rows = 4096, (1 << 20) + 70000
+    w = torch.randint(-127, 128, (rows, d), device="cuda", dtype=torch.int8)
+    s = torch.rand(rows, device="cuda") + 0.5
+    z = torch.randint(0, 256, (rows,), device="cuda", dtype=torch.uint8)
+    x = torch.randn(n, d, device="cuda")
+    y = q.qz_i8_linear(x, w, s, zeros=z)
+    for part in (slice(0, 500), slice(rows - 70123, None)):
+        assert torch.equal(y[:, part], q.qz_i8_linear(x, w[part], s[part], zeros=z[part]))
+
+
+def test_many_tokens():
+    """X of 4.4 GB against few rows of W, and results past 2^32 bytes."""
+    q, torch = qz(), _t()
+    n = 1 << 20
+    x = torch.randint(-127, 128, (n, 4224), device="cuda", dtype=torch.int8)
+    sx, sums = torch.rand(n, device="cuda"), x.sum(1, dtype=torch.int32)
+    for d_o in (33, 1100):
+        w = torch.randint(-127, 128, (d_o, 4224), device="cuda", dtype=torch.int8)
+        sw, z = torch.rand(d_o, device="cuda"), torch.randint(0, 256, (d_o,), device="cuda", dtype=torch.uint8)
+        y = q.qz_i8_matmul(x, sx, w, sw, 4224, zeros=z, xsums=sums, out_dtype=torch.float32)
+        for part in (slice(0, 300), slice(n - 1111, None)):
+            assert torch.equal(y[part], q.qz_i8_matmul(x[part], sx[part], w, sw, 4224, zeros=z, xsums=sums[part],
+                                                       out_dtype=torch.float32))
+
+
+@pytest.mark.parametrize("n", [1, 30, 700])
+def test_long_experts(n):
+    """Experts of 8.6 and 4.4 GB in all: the last two as a layer of two."""
+    q, torch = qz(), _t()
+    E, d, f = 512, 4096, 2080
+    gu = torch.randint(-127, 128, (E, 2 * f, d), device="cuda", dtype=torch.int8)
+    dn = torch.zeros((E, d, q.qz_i8_pitch(f)), device="cuda", dtype=torch.int8)
+    dn[:, :, :f] = torch.randint(-127, 128, (E, d, f), device="cuda", dtype=torch.int8)
+    gs, ds = torch.rand(E, 2 * f, device="cuda") * 1e-4, torch.rand(E, d, device="cuda") * 1e-4
+    gz, dz = (torch.randint(100, 156, s.shape, device="cuda", dtype=torch.uint8) for s in (gs, ds))
+    x = torch.randn(n, d, device="cuda", dtype=torch.bfloat16)
+    ids = torch.stack([torch.randperm(2) for _ in range(n)]).to(torch.int32).cuda()
+    w = torch.rand(n, 2, device="cuda")
+    y = q.qz_i8_moe(x, ids + (E - 2), w, gu, gs, dn, ds, gu_zeros=gz, dn_zeros=dz)
+    want = q.qz_i8_moe(x, ids, w, gu[-2:], gs[-2:], dn[-2:], ds[-2:], gu_zeros=gz[-2:], dn_zeros=dz[-2:])
+    assert torch.equal(y, want) and want.float().abs().max() > 0
+
+
+def test_pack_of_long_codes():
+    q, torch = qz(), _t()
+    c = torch.randint(0, 256, ((1 << 20) + 5, 4100), device="cuda", dtype=torch.uint8)
+    p = q.qz_i8_pack(c)
+    assert p.shape[1] == 4224 and not p[:, 4100:].any()
+    for part in (slice(0, 100), slice(-100, None)):
+        assert torch.equal(p[part, :4100], (c[part].to(torch.int16) - 128).to(torch.int8))
+    assert torch.equal(q.qz_i8_unpack(p, 4100), c)
