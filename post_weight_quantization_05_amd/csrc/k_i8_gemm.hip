@@ -30,7 +30,8 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
   lds_u8* const lds = (lds_u8*)smem;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / T::WN, wn = wave % T::WN;
+  // Wavefronts of the same tokens on different SIMDs where a tile may have few (the hardware deals them in turn).
+  const int wm = FORM == kPlain ? wave / T::WN : wave % T::WM, wn = FORM == kPlain ? wave % T::WN : wave / T::WM;
 
   // The hardware deals workgroups to the 8 XCDs in turn.  Each XCD gets a run of consecutive tiles,
   // and runs go through 8 rows of W tiles by all X tiles, so the tiles that are resident on an XCD
@@ -208,6 +209,20 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
 
   int at = 0;   // place of the stage's first half
   const auto wrap = [](int v) { return v >= H ? v - H : v; };
+  // An expert's last tile may leave a wavefront without tokens: it copies and meets the others, no more.
+  const bool idle = FORM != kPlain && t0 + wn * 32 * NT >= t_end;
+  if (idle) {
+    for (int st = 0; st + 1 < nst; ++st) {
+      if (tile_in_flight<T>(st, halves))
+        wait_and_join<tile_in_flight<T>(0, H + 2)>();
+      else
+        wait_and_join<0>();
+      const int far = st + H / 2;
+      if (2 * st + H < halves) copy_half(integral_constant<int, H % 2>{}, far, at);
+      if (2 * st + H + 1 < halves) copy_half(integral_constant<int, (H + 1) % 2>{}, far + (H % 2 + 1) / 2, wrap(at + 1));
+      at = wrap(at + 2);
+    }
+  } else {
   each<S>([&](auto k) {
     each<kR>([&](auto i) {
       read(Set0{}, k, i, lds + wh * T::kHalf + in_w, lds + xh * T::kHalf + in_x, chunk_at(k));
@@ -306,6 +321,7 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
     step(Set1{}, lds, lds, 0, std::false_type{}, nothing);
   }
   }
+  }
 #undef QZ_FENCE
 
   // Register r of lane l: row 8 (r / 4) + 4 (l / 32) + r % 4 of a tile, token l % 32.  32 tokens at a
@@ -321,6 +337,7 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
     *(__attribute__((address_space(3))) float*)(par + 4 * (2 * BM + tid)) = my_bias;
   }
   __syncthreads();
+  if (idle) return;
   constexpr int kOutRows = FORM == kGateUp ? 16 * MT : 32 * MT;   // of a wavefront
   const int64_t wr0 = r0 + wm * kOutRows;
   auto results = [&](int a, int b, int r4, auto shifted) {
