@@ -7,7 +7,8 @@ namespace qz {
 
 // Workgroup e: expert e's first slot (the pairs with smaller ids), and its pairs in their order.  Ids
 // outside [0, E) get no slot.  Every workgroup reads all ids twice, four neighbours a lane, from L2: no
-// counts have to pass between workgroups, and nothing depends on their order.
+// counts have to pass between workgroups, and nothing depends on their order.  4096 tokens of 6 of 64
+// experts: 18.6 us together with the tokens' quantisation, whose launch it shares; with an id a lane 54 us.
 struct Grouping {
   const int32_t* ids;
   int64_t pairs;

@@ -1,5 +1,12 @@
 // Products of 8-bit integer rows with few tokens: workgroups of 16 RT rows of W by 16 NT tokens, whose
 // wavefronts share the contraction.
+//
+// With few tokens W is read once and little is computed on it, so what counts is how many bytes are on
+// their way.  There are too few tiles to fill the chip with a wavefront each, so the four wavefronts of a
+// workgroup split the contraction and add their sums in LDS at the end; each has a ring of stages of its
+// own, of 128 columns (whole lines), and waits for its own copies alone, without a barrier.  13 tokens
+// 12288 -> 4096: 49 MB of W in 10.6 us (4.9 TB/s with the launch), 256 workgroups, 20 KB of copies a
+// wavefront on their way; 64 tokens 4096 -> 4096 6.3 us, against 9.2 by tiles.
 #include <type_traits>
 
 #include "i8_gemm.h"

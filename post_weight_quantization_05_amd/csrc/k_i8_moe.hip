@@ -7,7 +7,9 @@ namespace qz {
 namespace {
 
 // A token's results added in the order of its experts: a workgroup per 1024 columns of a token, four a
-// thread; rows of y are whole fours.
+// thread; rows of y are whole fours.  Each result is added in 32 bits and rounded once.  Bound by HBM: 4096
+// tokens of 6 experts, 2048 columns, 203 MB read and 17 written, 34.5 us (6.4 TB/s: some of y is still in the
+// last-level cache).
 __global__ __launch_bounds__(256) void i8_sum_kernel(const float* __restrict__ y, int64_t ldp,
                                                      const int32_t* __restrict__ ids, int64_t d,
                                                      int blocks, int k, int E, uint16_t* __restrict__ Y) {

@@ -1,6 +1,12 @@
 // Products of 8-bit integer rows with very few tokens: rows of W against one to four tokens, or
 // against the experts' tokens one pair (token, r) at a time, by four-way dot products.  The tokens are
 // quantized in the same launch where they come as numbers.
+//
+// Bound by the reading of W and, on small layers, by the launch and one chain: load a token, its maximum,
+// codes, products, sums.  Every workgroup quantizes the tokens again (from L2; a second launch would cost
+// 3 us more), while its first two blocks of W are on their way.  W goes straight to registers: no
+// wavefront shares a row.  One token: 4096 -> 1024 4.4 us; 8 of 128 experts of 1024, d 4096, gate and up (67 MB)
+// 17.3 us (3.9 TB/s with the launch), down (34 MB) 12.4.
 #include <type_traits>
 
 #include "i8_gemm.h"
