@@ -62,7 +62,7 @@ def _build_binding() -> str:
            "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I", "/opt/rocm/include", "-I", sysconfig.get_paths()["include"],
            os.path.join(CSRC, "binding.cpp"), "-L", os.path.join(base, "lib"), "-lc10", "-lc10_hip",
-           "-ltorch_cpu", "-ltorch_python", "-o", tmp]
+           "-ltorch_cpu", "-ltorch_hip", "-ltorch_python", "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")

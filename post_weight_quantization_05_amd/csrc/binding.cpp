@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -107,8 +108,9 @@ at::ScalarType out_type(PyObject* o) {
   return t;
 }
 
+// (straight from the device's allocator: the dispatcher takes as long again)
 at::Tensor make(at::IntArrayRef size, at::ScalarType type, int64_t index) {
-  return at::empty(size, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(index)));
+  return at::Tensor(at::detail::empty_cuda(size, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt));
 }
 
 hipStream_t stream_of(int64_t index) {
