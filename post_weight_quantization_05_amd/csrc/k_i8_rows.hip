@@ -188,6 +188,12 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
   i32x4 even[R][U], odd[R][U];
   load(0, even);
   load(1, odd);
+  // What the lane's result is made with, on its way as early: of row lane / N (kGateUp: lane).
+  const int at = lane < R * N ? lane / N : 0;
+  const int64_t my_row = w_row0 + row_of(at);
+  const float my_sw = p.sw[my_row];
+  const int my_shift = p.zeros ? p.zeros[my_row] - 128 : 0;
+  const float my_bias = FORM == kPlain && p.bias ? p.bias[my_row] : 0.f;
   stage_rows<QT, VEC>(p, FORM == kGateUp ? pair / p.k : 0, N, s, tops);
   for (int b = 0; b < blocks; b += 2) {
     use(b, even);
@@ -206,16 +212,14 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
       a = lane == i * N + t ? total : a;
     }
   if constexpr (FORM == kGateUp) {
-    const int64_t r = w_row0 + row_of(lane < R ? lane : 0);
-    float v = 0.f;
-    if (lane < R) v = scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[0], xscale[0], p.sw[r], 0.f);
+    const float v = scaled(a, my_shift, xsums[0], xscale[0], my_sw, 0.f);
     const float up = __shfl(v, lane + kOut);
     if (lane < kOut && r0 + lane < p.d_o) static_cast<float*>(p.Y)[pair * p.ldy + r0 + lane] = silu(v) * up;
   } else {
     const int t = lane % N;
     const int64_t r = r0 + lane / N;
     if (lane < R * N && r < p.d_o) {
-      const float v = scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[t], xscale[t], p.sw[r], p.bias ? p.bias[r] : 0.f);
+      const float v = scaled(a, my_shift, xsums[t], xscale[t], my_sw, my_bias);
       if (p.yt == QZ_BF16)
         static_cast<uint16_t*>(p.Y)[t * p.ldy + r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
       else
@@ -231,7 +235,8 @@ template <bool VEC, int SPLIT, int R>
 __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Product p) {
   constexpr int kOut = R * (4 / SPLIT);
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float xscale[QZ_ROUTE_MAX_TOP_K], part[QZ_ROUTE_MAX_TOP_K][kOut];
+  __shared__ float xscale[QZ_ROUTE_MAX_TOP_K];
+  __shared__ int part[QZ_ROUTE_MAX_TOP_K][kOut];   // sums, and then the weighted results' bits
   __shared__ int xsums[QZ_ROUTE_MAX_TOP_K];
   __shared__ uint32_t tops[4];
   const int lane = threadIdx.x & 63;
@@ -269,20 +274,33 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
     if ((b + 1) % per) return;
     int a = 0;
 #pragma unroll
-    for (int i = 0; i < R; ++i) {   // a pair's product, weighted
+    for (int i = 0; i < R; ++i) {   // a pair's sums
       const int total = lanes_sum(acc[i]);
       a = lane == i ? total : a;
       acc[i] = 0;
     }
-    const int e = expert_of(at);
-    if (lane < R && e >= 0) {
-      const int64_t r = e * p.d_o + (r0 + lane < p.d_o ? r0 + lane : p.d_o - 1);
-      part[at][r0 - wg0 + lane] = p.pair_weight[pair0 + at] * scaled(a, p.zeros ? p.zeros[r] - 128 : 0, xsums[at], xscale[at], p.sw[r], 0.f);
-    }
+    if (lane < R) part[at][r0 - wg0 + lane] = a;
   };
   i32x4 even[R], odd[R];
   load(0, even);
   load(1, odd);
+  // What a pair's result of a row is made with, on its way as early: a thread has up to kEach of them.
+  constexpr int kEach = QZ_ROUTE_MAX_TOP_K * kOut / kRowsThreads;
+  float my_sw[kEach], my_weight[kEach];
+  int my_shift[kEach];
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int i = (j * kRowsThreads + threadIdx.x) / kOut, o = threadIdx.x % kOut;
+    const int e = i < p.k ? expert_of(i) : -1;
+    my_sw[j] = my_weight[j] = 0.f;
+    my_shift[j] = 0;
+    if (e >= 0) {
+      const int64_t r = e * p.d_o + (wg0 + o < p.d_o ? wg0 + o : p.d_o - 1);
+      my_sw[j] = p.sw[r];
+      my_weight[j] = p.pair_weight[pair0 + i];
+      if (p.zeros) my_shift[j] = p.zeros[r] - 128;
+    }
+  }
   if constexpr (SPLIT == 4) {   // each wavefront its own: its LDS accesses stay in order, the compiler's too
     for (int i = wave; i < p.k; i += 4) stage_row<QZ_F32, VEC, 64>(p, pair0 + i, i, lane, s, nullptr);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -299,11 +317,18 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
     load(b + 3, odd);
   }
   __syncthreads();
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int i = (j * kRowsThreads + threadIdx.x) / kOut, o = threadIdx.x % kOut;
+    if (i < p.k)
+      part[i][o] = __float_as_int(my_weight[j] * scaled(part[i][o], my_shift[j], xsums[i], xscale[i], my_sw[j], 0.f));
+  }
+  __syncthreads();
   const int64_t r = wg0 + threadIdx.x;
   if (threadIdx.x < kOut && r < p.d_o) {
     float y = 0.f;
     for (int i = 0; i < p.k; ++i)
-      if (expert_of(i) >= 0) y += part[i][threadIdx.x];
+      if (expert_of(i) >= 0) y += __int_as_float(part[i][threadIdx.x]);
     static_cast<uint16_t*>(p.Y)[blockIdx.y * p.ldy + r] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(y));
   }
 }
