@@ -5,8 +5,8 @@
 // Bound by the reading of W and, on small layers, by the launch and one chain: load a token, its maximum,
 // codes, products, sums.  Every workgroup quantizes the tokens again (from L2; a second launch would cost
 // 3 us more), while its first two blocks of W are on their way.  W goes straight to registers: no
-// wavefront shares a row.  One token: 4096 -> 1024 4.4 us; 8 of 128 experts of 1024, d 4096, gate and up (67 MB)
-// 17.3 us (3.9 TB/s with the launch), down (34 MB) 12.4.
+// wavefront shares a row.  One token: 4096 -> 1024 4.1 us; 8 of 128 experts of 1024, d 4096, gate and up (67 MB)
+// 16.3 us (4.1 TB/s with the launch), down (34 MB) 11.3.
 #include <type_traits>
 
 #include "i8_gemm.h"
@@ -50,22 +50,51 @@ struct Staged {
   int pitch;
 };
 
-// A row by the T threads t = 0 .. T - 1 of a wavefront or (T = kRowsThreads) of the workgroup.
-template <int QT, bool VEC, int T>
+// The first two chunks of eight elements that a thread has of a row (and their factors).  A wavefront's loads
+// come back in the order of their issue, so these go out before the first blocks of W.
+template <int QT>
+struct RowStart {
+  Raw8<QT> x[2];
+  Raw8<QZ_F32> f[2];
+};
+// Of a row by the T threads t = 0 .. T - 1 of a wavefront or (T = kRowsThreads) of the workgroup.
+template <int QT, bool VEC, bool FACTORS, int T>
+__device__ __forceinline__ void fetch_row(const I8Product& p, int64_t row, int t, RowStart<QT>& r) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t c = 8 * (i * T + t);
+    r.x[i] = load8<QT, VEC>(p.raw, row * p.ldraw + c, p.cols - c);
+    if (FACTORS && p.colf) r.f[i] = load8<QZ_F32, VEC>(p.colf, c, p.cols - c);
+  }
+}
+// start: null where it costs more registers than it gives (the row is loaded twice then, the second time from
+// the caches).
+template <int QT, bool VEC, bool FACTORS, int T>
 __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i, int t, const Staged& s,
-                                          uint32_t* tops) {
+                                          uint32_t* tops, const RowStart<QT>* start) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   uint32_t top = 0;
+  auto with_factors = [&](const Raw8<QZ_F32>& raw, float (&v)[8]) {
+    float f[8];
+    numbers8(raw, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f[j];
+  };
   auto elements = [&](int c, float (&v)[8]) {
     numbers8(load8<QT, VEC>(p.raw, row * p.ldraw + c, p.cols - c), v);
-    if (p.colf) {
-      float f[8];
-      numbers8(load8<QZ_F32, VEC>(p.colf, c, p.cols - c), f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= f[j];
-    }
+    if (FACTORS && p.colf) with_factors(load8<QZ_F32, VEC>(p.colf, c, p.cols - c), v);
   };
-  for (int c = 8 * t; c < p.cols; c += 8 * T) {
+  const int from = start ? 2 * T + t : t;
+  float first[2][8];
+  if (start) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      numbers8(start->x[j], first[j]);
+      if (FACTORS && p.colf) with_factors(start->f[j], first[j]);
+      top = top8(first[j], top);
+    }
+  }
+  for (int c = 8 * from; c < p.cols; c += 8 * T) {
     float v[8];
     elements(c, v);
     top = top8(v, top);
@@ -79,15 +108,24 @@ __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i
   }
   const RowScale sc = row_scale(top);
   int sum = 0;
-  for (int c = 8 * t; c < s.pitch; c += 8 * T) {
+  auto write = [&](int c, const float (&v)[8]) {
     uint2 w = make_uint2(0, 0);
     if (c < p.cols) {
-      float v[8], q[8];
-      elements(c, v);
+      float q[8];
       w = codes8(v, sc, q);
       sum = add_codes(w.x, add_codes(w.y, sum));
     }
     *reinterpret_cast<uint2*>(s.codes + i * s.pitch + c) = w;
+  };
+  if (start) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (8 * (j * T + t) < s.pitch) write(8 * (j * T + t), first[j]);
+  }
+  for (int c = 8 * from; c < s.pitch; c += 8 * T) {
+    float v[8];
+    elements(c, v);
+    write(c, v);
   }
   if (p.zeros) {
     sum = lanes_sum(sum);
@@ -104,25 +142,42 @@ __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i
   }
 }
 
-// Rows first .. first + n - 1 of the tokens; all threads of the workgroup call it.
-template <int QT, bool VEC>
-__device__ __forceinline__ void stage_rows(const I8Product& p, int64_t first, int n, const Staged& s, uint32_t* tops) {
+// Rows first .. first + n - 1 of the tokens; all threads of the workgroup call it.  Up to three rows by the whole
+// workgroup, with a few barriers each; more, a wavefront a row.
+constexpr int kTogether = 3;
+template <int QT, bool VEC, bool FACTORS>
+__device__ __forceinline__ void fetch_rows(const I8Product& p, int64_t first, int n, RowStart<QT>& start) {
   const int tid = threadIdx.x;
-  if constexpr (QT == kCodes) {
-    for (int c = 16 * tid; c < n * s.pitch; c += 16 * kRowsThreads) {
-      const int i = c / s.pitch, at = c % s.pitch;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (at < p.P) v = *reinterpret_cast<const uint4*>(p.X + (first + i) * p.P + at);
-      *reinterpret_cast<uint4*>(s.codes + c) = v;
-    }
-    if (tid < n) {
-      s.scale[tid] = p.sx[first + tid];
-      s.sum[tid] = p.zeros ? p.xsum[first + tid] : 0;
-    }
-  } else if (n < 4) {   // a few barriers a row; otherwise a wavefront a row
-    for (int i = 0; i < n; ++i) stage_row<QT, VEC, kRowsThreads>(p, first + i, i, tid, s, tops);
+  if (n <= kTogether)
+    fetch_row<QT, VEC, FACTORS, kRowsThreads>(p, first, tid, start);
+  else
+    fetch_row<QT, VEC, FACTORS, 64>(p, first + (tid / 64 < n ? tid / 64 : 0), tid & 63, start);
+}
+template <int QT, bool VEC, bool FACTORS>
+__device__ __forceinline__ void stage_rows(const I8Product& p, int64_t first, int n, const Staged& s, uint32_t* tops,
+                                           const RowStart<QT>* start) {
+  const int tid = threadIdx.x;
+  if (n <= kTogether) {
+    for (int i = 0; i < n; ++i)
+      stage_row<QT, VEC, FACTORS, kRowsThreads>(p, first + i, i, tid, s, tops, i ? nullptr : start);
   } else {
-    for (int i = tid / 64; i < n; i += kRowsThreads / 64) stage_row<QT, VEC, 64>(p, first + i, i, tid & 63, s, tops);
+    for (int i = tid / 64; i < n; i += kRowsThreads / 64)
+      stage_row<QT, VEC, FACTORS, 64>(p, first + i, i, tid & 63, s, tops, i < kRowsThreads / 64 ? start : nullptr);
+  }
+  __syncthreads();
+}
+// Rows that come as codes: 16 bytes a thread at a time, the first of them fetched before.
+__device__ __forceinline__ uint4 code_piece(const I8Product& p, int64_t first, int n, const Staged& s, int c) {
+  const int i = c / s.pitch, at = c % s.pitch;
+  return c < n * s.pitch && at < p.P ? *reinterpret_cast<const uint4*>(p.X + (first + i) * p.P + at) : make_uint4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void stage_codes(const I8Product& p, int64_t first, int n, const Staged& s, const uint4& start) {
+  const int tid = threadIdx.x;
+  for (int c = 16 * tid; c < n * s.pitch; c += 16 * kRowsThreads)
+    *reinterpret_cast<uint4*>(s.codes + c) = c == 16 * tid ? start : code_piece(p, first, n, s, c);
+  if (tid < n) {
+    s.scale[tid] = p.sx[first + tid];
+    s.sum[tid] = p.zeros ? p.xsum[first + tid] : 0;
   }
   __syncthreads();
 }
@@ -186,6 +241,13 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
     }
   };
   i32x4 even[R][U], odd[R][U];
+  const int64_t first = FORM == kGateUp ? pair / p.k : 0;
+  std::conditional_t<QT == kCodes, uint4, RowStart<QT == kCodes ? QZ_F32 : QT>> start;
+  if constexpr (QT == kCodes)
+    start = code_piece(p, first, N, s, 16 * threadIdx.x);
+  else
+    fetch_rows<QT, VEC, FORM == kPlain>(p, first, N, start);
+  __builtin_amdgcn_sched_barrier(0);
   load(0, even);
   load(1, odd);
   // What the lane's result is made with, on its way as early: of row lane / N (kGateUp: lane).
@@ -194,7 +256,10 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
   const float my_sw = p.sw[my_row];
   const int my_shift = p.zeros ? p.zeros[my_row] - 128 : 0;
   const float my_bias = FORM == kPlain && p.bias ? p.bias[my_row] : 0.f;
-  stage_rows<QT, VEC>(p, FORM == kGateUp ? pair / p.k : 0, N, s, tops);
+  if constexpr (QT == kCodes)
+    stage_codes(p, first, N, s, start);
+  else
+    stage_rows<QT, VEC, FORM == kPlain>(p, first, N, s, tops, &start);
   for (int b = 0; b < blocks; b += 2) {
     use(b, even);
     load(b + 2, even);
@@ -282,6 +347,11 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
     if (lane < R) part[at][r0 - wg0 + lane] = a;
   };
   i32x4 even[R], odd[R];
+  RowStart<QZ_F32> start;
+  if constexpr (SPLIT == 4) {   // of the wavefront's first pair (with more workgroups a compute unit, the registers cost more)
+    fetch_row<QZ_F32, VEC, false, 64>(p, pair0 + (wave < p.k ? wave : 0), lane, start);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   load(0, even);
   load(1, odd);
   // What a pair's result of a row is made with, on its way as early: a thread has up to kEach of them.
@@ -302,12 +372,15 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
     }
   }
   if constexpr (SPLIT == 4) {   // each wavefront its own: its LDS accesses stay in order, the compiler's too
-    for (int i = wave; i < p.k; i += 4) stage_row<QZ_F32, VEC, 64>(p, pair0 + i, i, lane, s, nullptr);
+    for (int i = wave; i < p.k; i += 4) {
+      if (i >= 4) fetch_row<QZ_F32, VEC, false, 64>(p, pair0 + i, lane, start);
+      stage_row<QZ_F32, VEC, false, 64>(p, pair0 + i, i, lane, s, nullptr, &start);
+    }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   } else {
-    stage_rows<QZ_F32, VEC>(p, pair0, p.k, s, tops);
+    stage_rows<QZ_F32, VEC, false>(p, pair0, p.k, s, tops, nullptr);
   }
   for (int b = 0; b < blocks; b += 2) {
     use(b, even);
@@ -390,8 +463,8 @@ int launch_i8_rows_down(const I8Product& p, int64_t tokens, hipStream_t s) {
     return check_launch("i8_rows_down");
   };
   // Few workgroups: as many wavefronts on a token's pairs as there are pairs for, so that there are more of
-  // them (1 token 8 of 128 x 1024, d 4096: 12.3 us, half as many 18.8); else more rows for each staging
-  // (4 tokens there: 28.8 us against 32.8; 7 tokens 2 of 8 x 2048: 17.2 against 20.9).
+  // them (1 token 8 of 128 x 1024, d 4096: 12.3 us, half as many 18.8; now 11.3); else more rows for each staging
+  // (4 tokens there: 28.8 us against 32.8, now 28.0; 7 tokens 2 of 8 x 2048: 17.2 against 20.9).
   const bool many = tokens * ceil_div(p.d_o, 16) >= 512;
   auto by_pairs = [&](auto vec) {
     constexpr bool VEC = decltype(vec)::value;
