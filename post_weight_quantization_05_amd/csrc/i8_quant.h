@@ -141,16 +141,28 @@ __device__ __forceinline__ int add_codes(uint32_t w, int sum) {
   return __builtin_amdgcn_sdot4(static_cast<int>(w), 0x01010101, sum, false);
 }
 
-__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
-  for (int o = 32; o; o >>= 1) {
-    const uint32_t u = static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), o));
-    v = u > v ? u : v;
-  }
-  return v;
-}
+// Sum over the wavefront, in every lane; the largest below.  By moves inside the vector unit: through LDS each
+// of the six steps would wait a hundred cycles.
 __device__ __forceinline__ int wave_sum(int v) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+  v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true);    // lane ^ 1
+  v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true);    // lane ^ 2
+  v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);   // mirrored in eight
+  v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);   // mirrored in sixteen
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = static_cast<int>(a[0]) + static_cast<int>(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return static_cast<int>(b[0]) + static_cast<int>(b[1]);
+}
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+  const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true));
+  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true));
+  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true));
+  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = up(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return up(b[0], b[1]);
 }
 
 }  // namespace qz

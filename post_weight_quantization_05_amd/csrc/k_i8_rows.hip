@@ -18,29 +18,6 @@ namespace {
 constexpr int kCodes = -1;   // tokens that come as codes
 constexpr int kRowsThreads = 256;
 
-// Sum over the wavefront, in every lane.
-__device__ __forceinline__ int lanes_sum(int v) {
-  v += __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true);    // lane ^ 1
-  v += __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true);    // lane ^ 2
-  v += __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);   // mirrored in eight
-  v += __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);   // mirrored in sixteen
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = static_cast<int>(a[0]) + static_cast<int>(a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return static_cast<int>(b[0]) + static_cast<int>(b[1]);
-}
-__device__ __forceinline__ uint32_t lanes_top(uint32_t v) {
-  const auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  v = up(v, __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true));
-  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true));
-  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true));
-  v = up(v, __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true));
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = up(a[0], a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return up(b[0], b[1]);
-}
-
 // What the tokens of a workgroup become in LDS: codes [rows][P rounded up to 1024], zero behind the
 // columns, and each row's scale and sum of codes.
 struct Staged {
@@ -99,7 +76,7 @@ __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i
     elements(c, v);
     top = top8(v, top);
   }
-  top = lanes_top(top);
+  top = wave_top(top);
   if constexpr (T > 64) {
     if (lane == 0) tops[wave] = top;
     __syncthreads();
@@ -128,7 +105,7 @@ __device__ __forceinline__ void stage_row(const I8Product& p, int64_t row, int i
     write(c, v);
   }
   if (p.zeros) {
-    sum = lanes_sum(sum);
+    sum = wave_sum(sum);
     if constexpr (T > 64) {
       if (lane == 0) tops[wave] = static_cast<uint32_t>(sum);
       __syncthreads();
@@ -273,7 +250,7 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_kernel(const I8Product p
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int t = 0; t < N; ++t) {
-      const int total = lanes_sum(acc[i][t]);
+      const int total = wave_sum(acc[i][t]);
       a = lane == i * N + t ? total : a;
     }
   if constexpr (FORM == kGateUp) {
@@ -340,7 +317,7 @@ __global__ __launch_bounds__(kRowsThreads) void i8_rows_down_kernel(const I8Prod
     int a = 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {   // a pair's sums
-      const int total = lanes_sum(acc[i]);
+      const int total = wave_sum(acc[i]);
       a = lane == i ? total : a;
       acc[i] = 0;
     }
