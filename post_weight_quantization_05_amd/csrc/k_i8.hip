@@ -12,14 +12,15 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // TPR threads a row, CH chunks of eight elements each, which stay in registers between the row's
-// maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier.
+// maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier, where there
+// are enough of them.
 // A workgroup goes through several rows: the next one is on its way while one is worked on, and the
 // column factors are loaded once.
 //
 // Bound by HBM: 8192 x 5120 bf16 with factors and values, 84 MB read and 126 written, 37 us a call in a
 // warm loop (5.6 TB/s; torch's copy of 1 GiB reaches 5.1); 25600 x 5120 fp32 with values, 1.18 GB, 206 us
-// (5.7 TB/s).  Few rows are bound by one row's chain, load, maximum, codes: 70 x 200 fp32 3.2 us, 13 x 12288
-// bf16 4.8, most of it the launch.  Values leave past the caches in whole lines (42 -> 40 us in the former),
+// (5.7 TB/s).  Few rows are bound by one row's chain, load, maximum, codes: 70 x 200 fp32 2.8 us, 13 x 12288
+// bf16 4.0, most of it the launch.  Values leave past the caches in whole lines (42 -> 40 us in the former),
 // and the quotients of a code take one multiplication unless they lie next to a half (i8_quant.h).
 //
 // GROUP: the first g.E workgroups sort an expert layer's pairs beside it.
@@ -193,6 +194,8 @@ int quantize(const void* X, int xt, int64_t rows, int64_t cols, int64_t ldx, con
     constexpr int WT = decltype(type)::value;
     constexpr bool VEC = decltype(vec)::value, F = decltype(factors)::value;
     if (cols <= 512) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 1>, 64);
+    // few rows: a row's latency counts (300 rows of 2048 bf16, with the pairs sorted, 3.8 us against 6.6)
+    if (cols <= 2048 && rows <= 1024) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 256, 1>, 256);
     if (cols <= 1024) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 2>, 64);
     if (cols <= 2048) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 64, 4>, 64);
     if (cols <= 4096) return go(i8_quantize_kernel<WT, VEC, F, GROUP, 256, 2>, 256);
