@@ -71,6 +71,15 @@ def test_quantize_exact(rows, cols, dtype, factors):
     _check_quantize(x, xd, colf, cols)
 
 
+# Rows by wavefronts and by workgroups, one and several each; every number of chunks a thread.
+@pytest.mark.parametrize("rows,cols", [(1024, 1000), (1025, 1000), (1100, 2047), (1030, 1304), (1500, 520), (6, 5120), (5, 6001),
+                                       (2500, 2056), (8300, 296), (530, 8200), (515, 16400)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("factors", [False, True])
+def test_quantize_exact_many_rows(rows, cols, dtype, factors):
+    test_quantize_exact(rows, cols, dtype, factors)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_quantize_special_rows(dtype):
     top = float(_t().finfo(_dtype(dtype)).max)
@@ -413,6 +422,24 @@ def test_moe_by_every_kernel(n, E, k, d, f, zeroed):
     ids = np.argsort(rng.random((n, E)), axis=1)[:, :k].astype(np.int32)
     ids[rng.random((n, k)) < 0.05] = -1
     _check_layer(x, xd, ids, rng.random((n, k)).astype(np.float32), gu, dn, f)
+
+
+@pytest.mark.parametrize("n,E,k,d,f", [(2100, 8, 4, 64, 32), (1100, 70, 16, 1100, 32), (2500, 512, 8, 520, 8), (5000, 2, 2, 300, 16)])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_moe_of_many_pairs(n, E, k, d, f, aligned):
+    """Runs of ids that are loaded in batches, with their ends, from 16-byte boundaries and beside them."""
+    rng = np.random.default_rng([n, E, k])
+    x, xd = _rounded(rng.standard_normal((n, d)), "bf16")
+    gu, dn = _layer(rng, E, d, f, False)
+    ids = np.argsort(rng.random((n, E)), axis=1)[:, :k].astype(np.int32)
+    ids[rng.random((n, k)) < 0.02] = E
+    ids[n // 3:n // 2] = ids[0]
+    w = rng.random((n, k)).astype(np.float32)
+    y = _check_layer(x, xd, ids, w, gu, dn, f)
+    if not aligned:
+        hold = _t().zeros(n * k + 1, dtype=_t().int32, device="cuda")
+        hold[1:] = to_dev(ids).reshape(-1)
+        assert _t().equal(y, _run_layer(xd, hold[1:].view(n, k), to_dev(w), gu, dn))
 
 
 @pytest.mark.parametrize("n", [1, 6, 90, 400])
