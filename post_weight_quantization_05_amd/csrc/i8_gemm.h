@@ -23,11 +23,40 @@ __device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, fl
   return fmaf(static_cast<float>(a - __mul24(shift, xsum)) * sx, sw, bias);
 }
 
-// g / (1 + e^-g) by the hardware's power of two and reciprocal, a last bit off each: g log2 e is off by half
-// of one, so the whole by less than (4 + |g|) 2^-23 of itself.  (By the library's exponential and an exact
-// quotient an expert layer's gate and up products spent a sixth of their time here.)
+// silu: g / (1 + e^-g), off by less than 8 2^-24 of itself, and half of 2^-149 where it is below 2^-126.
+//
+// Up to |g| = 80, where neither the power nor its sum with 1 leaves the normal numbers: e^-g = 2^h e^(-g - h ln 2)
+// with h = -g log2 e rounded.  The hardware's power of two and reciprocal are a last bit off (2 2^-24 each), the second
+// factor is 1 + its exponent, below 2^-17, with ln 2 in two parts; its step, the sum and the product round once each.
+__device__ __forceinline__ float silu_near(float g) {
+  const float h = -0x1.715476p+0f * g, e = __builtin_amdgcn_exp2f(h);
+  const float rest = fmaf(h, 0x1.05c61p-29f, fmaf(h, -0x1.62e43p-1f, -g));
+  return g * __builtin_amdgcn_rcpf(1.f + fmaf(e, rest, e));
+}
+// Beyond: g itself, or g e^g = g p 2^n with n whole and p the power of two of a fraction within +-1/2, 2^n put on
+// at the end.  (Below -256 it is zero.)
+__device__ __forceinline__ float silu_far(float g) {
+  const float a = fminf(fabsf(g), 256.f), n = __builtin_rintf(-0x1.715476p+0f * a);
+  const float p = __builtin_amdgcn_exp2f(fmaf(-0x1.4ae0cp-26f, a, fmaf(-0x1.715476p+0f, a, -n)));
+  return g < 0.f ? __builtin_ldexpf(g * p, static_cast<int>(n)) : g;
+}
 __device__ __forceinline__ float silu(float g) {
-  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * g));
+  const float v = silu_near(g);
+  return fabsf(g) > 80.f ? silu_far(g) : v;
+}
+// Of four, with one look at whether any of the wavefront's is far.  (A large tile ends with 64 of them a thread: 4096
+// tokens 6 of 64, 2048 -> 2 x 1408, gate and up 209 us in a warm loop, 207 by the plain form, which overflows and loses
+// |g| last bits; 221 with a power split for every g.)
+__device__ __forceinline__ f32x4 silu(const f32x4& g) {
+  f32x4 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = silu_near(g[i]);
+  const float most = fmaxf(fmaxf(fabsf(g[0]), fabsf(g[1])), fmaxf(fabsf(g[2]), fabsf(g[3])));
+  if (__ballot(most > 80.f)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fabsf(g[i]) > 80.f ? silu_far(g[i]) : v[i];
+  }
+  return v;
 }
 
 // The token tiles of `bn` slots of an expert layer, the experts' tiles in their order.  Every lane of a

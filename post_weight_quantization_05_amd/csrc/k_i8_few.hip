@@ -142,16 +142,17 @@ __global__ __launch_bounds__(64 * T::kWaves) void i8_few_kernel(const I8Product 
     const int64_t xr = FORM == kGateUp ? pair / p.k : slot_at;
     const float sx = p.sx[xr];
     const int xsum = p.zeros ? p.xsum[xr] : 0;
-    f32x4 v;
+    f32x4 v, u;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int64_t c = w_row0 + (r + j < p.d_o ? r + j : p.d_o - 1);
       v[j] = scaled(sum[j], p.zeros ? p.zeros[c] - 128 : 0, xsum, sx, p.sw[c], FORM == kPlain && p.bias ? p.bias[c] : 0.f);
       if constexpr (FORM == kGateUp) {
         const int64_t cu = c + p.d_o;
-        v[j] = silu(v[j]) * scaled(up[j], p.zeros ? p.zeros[cu] - 128 : 0, xsum, sx, p.sw[cu], 0.f);
+        u[j] = scaled(up[j], p.zeros ? p.zeros[cu] - 128 : 0, xsum, sx, p.sw[cu], 0.f);
       }
     }
+    if constexpr (FORM == kGateUp) v = silu(v) * u;
     if constexpr (FORM == kDown) v *= p.pair_weight[pair];
     const int64_t at = (FORM == kDown ? pair : slot_at) * p.ldy + r;
     const bool whole = vec && r + 4 <= p.d_o;

@@ -390,9 +390,7 @@ void i8_tile_kernel(const I8Product p, int tiles_w, int tiles_x) {
           const int rr = (FORM == kGateUp ? a / 2 : a) * 32 + 8 * r4 + 4 * half;
           f32x4 v = results(a, b, r4, shifted);
           if constexpr (FORM == kGateUp) {
-            const f32x4 u = results(a + 1, b, r4, shifted);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * u[i];
+            v = silu(v) * results(a + 1, b, r4, shifted);
           } else if constexpr (FORM == kDown) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] *= pw[b];
