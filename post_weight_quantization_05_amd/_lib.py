@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libqz.so")
@@ -139,6 +140,21 @@ _BINDING_ORDER = ("qz_i8_quantize", "qz_i8_matmul_workspace", "qz_i8_matmul", "q
                   "qz_i8_linear", "qz_route", "qz_i8_moe_workspace", "qz_i8_moe")
 
 
+def _native_calls(lib):
+    """The binding module bound to `lib`; None where it is not built, or (with a warning) cannot be loaded here: one
+    of another Python, PyTorch or ABI version must not take the library with it."""
+    if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+        return None
+    try:
+        from . import _binding
+        _binding.init(lib.qz_abi_version(), *(C.cast(getattr(lib, name), C.c_void_p).value for name in _BINDING_ORDER))
+        return _binding
+    except Exception as e:
+        warnings.warn(f"_binding.so is not usable ({e}): calls go through ctypes; rebuild the package", RuntimeWarning,
+                      stacklevel=3)
+        return None
+
+
 def load(path: str = LIB_PATH):
     """Load libqz.so and declare its signatures.  Raises if it is not built."""
     global _lib, binding
@@ -157,9 +173,6 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    if os.path.exists(os.path.join(_HERE, "_binding.so")):
-        from . import _binding
-        _binding.init(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _BINDING_ORDER))
-        binding = _binding
+    binding = _native_calls(lib)
     _lib = lib
     return lib

@@ -301,10 +301,13 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// The addresses of the library's functions, in the order of `lib`.
+// The library's ABI version and the addresses of its functions, in the order of `lib`.
 PyObject* init(PyObject*, PyObject* args) {
+  int abi;
   unsigned long long p[8];
-  if (!PyArg_ParseTuple(args, "KKKKKKKK", p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, p + 7)) return nullptr;
+  if (!PyArg_ParseTuple(args, "iKKKKKKKK", &abi, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6, p + 7)) return nullptr;
+  if (abi != QZ_ABI_VERSION)
+    return PyErr_Format(PyExc_ImportError, "built for ABI version %d, and the library has %d", QZ_ABI_VERSION, abi);
   static_assert(sizeof lib == sizeof p);
   __builtin_memcpy(&lib, p, sizeof p);
   Py_RETURN_NONE;
