@@ -94,14 +94,20 @@ enum class I8Kind { kFew11, kFew21, kFew22, kFew24, k256x256, k256x128, k128x128
 
 // Times in microseconds from the sizes: `fixed`, then for every round of resident workgroups of a
 // compute unit `each` and a time for each stage of 128 columns of a wavefront: `alone`, or for r
-// together at least r times `share`.  Fitted to 1100 measurements (5 to 4000 tokens, seven layers of
-// 512 to 12288 columns; 7 to 15% root mean square); the kernel chosen is 1.5% slower than the best
-// one measured there on average, 25% at most.  Both sides, measured, us: 13 tokens 4096 -> 12288, few
-// 2 x 1 9.6, 1 x 1 10.2; 64 tokens 4096 -> 4096, few 2 x 2 6.3, 2 x 1 7.0, 64 x 64 9.2; 256 tokens
-// 4096 -> 12288, 64 x 64 by four 20.7, 128 x 128 22.1; 1000 tokens 4096 -> 4096, 128 x 128 22.2,
-// 128 x 64 23.9; 1600 tokens there, 256 x 128 31.2, 128 x 128 32.2; 4000 tokens 4096 -> 12288,
-// 256 x 256 178, 256 x 128 199.  Sums split along the contraction and joined in a second launch lost
+// together at least r times `share`.  Fitted to 1100 measurements of seven layers.  On 274 sizes measured since (5 to 5000
+// tokens, 128 to 12288 columns, half of the sizes drawn at random; the estimates 9 to 18% root mean square off) the
+// kernel chosen is 1.6% slower than the best one on average, 21% at most.  Both sides, measured, us: 13 tokens
+// 4096 -> 12288, few 2 x 1 9.6, 1 x 1 10.2; 64 tokens 4096 -> 4096, few 2 x 2 6.3, 2 x 1 7.0, 64 x 64 9.2; 1000 tokens
+// 4096 -> 4096, 128 x 128 22.5, 128 x 64 24.1; 1600 tokens there, 256 x 128 31.2, 128 x 128 32.2; 4000 tokens
+// 4096 -> 12288, 256 x 256 178, 256 x 128 199.  Sums split along the contraction and joined in a second launch lost
 // against the best of these at every size measured.
+//
+// Where it errs: 128 x 128 is estimated 15 to 20% too fast where there is most of a tile a compute unit, but no more
+// (256 tokens 4096 -> 12288, taken 22.0, 64 x 64 by four 20.5; 160 tokens there 20.9, 18.2), and tiles of 256 rows of W
+// as much over several rounds (1600 tokens 2048 -> 10240, taken 256 x 128 55.5, 128 x 128 47.9).  Of the 272 products of
+// 136 drawn and ordinary expert layers (2 to 4096 tokens, 2 to 128 experts, skewed) the one chosen is 3.6% slower than
+// the best on average; the worst are narrow layers of many experts with 90 tokens each, whose tiles of 256 are two
+// thirds empty (2910 tokens 2 of 64, 640 -> 2 x 416: 28.0, 128 x 64 16.8).
 struct I8Time {
   I8Kind kind;
   int bm, bn, resident, waves;   // waves that share the contraction
@@ -142,8 +148,9 @@ inline I8Kind i8_choose(int64_t n, int64_t d_o, int64_t stages, int experts, boo
     };
     double t = c.fixed + (groups / c.resident) * together(c.resident) +
                (groups % c.resident ? together(groups % c.resident) : 0.);
-    // Of several rounds of experts' tiles, full ones and short ones, half a round is left over on average
-    // (4096 tokens, 6 of 64 experts, 2048 -> 2 x 1408: 256 x 256 208 us, 256 x 128 227).
+    // Of several rounds of experts' tiles, full ones and short ones, half a round is left over on average: without this,
+    // 4096 tokens 6 of 64 experts, 2048 -> 2 x 1408, take 256 x 128, 227 us, and not 256 x 256, 208.  Over those 272 products
+    // it makes no difference (3.6 and 3.4%), and on the tiles of which several are resident it costs (4.0%).
     if (experts && c.resident == 1 && groups > 1) t = c.fixed + (all / 256. + 0.5) * together(1);
     if (t < best_t) {
       best_t = t;

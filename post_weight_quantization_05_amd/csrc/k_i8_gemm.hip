@@ -18,9 +18,10 @@
 //    library's product of the same codes, without scales: 1025 to 1044 us.
 //  - 2048 x 4096 -> 4096, 256 x 128: 36.5 us, busy for 40%: one tile a compute unit, so the first stages
 //    and the results are not covered by another's products; the library's 40 us.
-//  - 256 x 4096 -> 12288, 128 x 128: 22.7 us, 75 MB read (3.3 TB/s): 192 tiles on 256 compute units, each
-//    bound by its own stream from memory into LDS; the library's 31 us.  Splitting the contraction, with the
-//    join in a second launch, lost at every size.
+//  - 256 x 4096 -> 12288, 128 x 128: 22.9 us, 75 MB read (3.3 TB/s): 192 tiles on 256 compute units, each
+//    bound by its own stream from memory into LDS; the library's 31 us.  64 x 64, four resident, would take 20.5 (the
+//    choice's times err there, i8_plan.h).  Splitting the contraction, with the join in a second launch, lost at
+//    every size.
 //  - Expert layer, 4096 tokens 6 of 64, 2048 -> 2 x 1408: 200 us for 559 MB read and 138 written, busy for 34%:
 //    384 tokens an expert use its weights for 1.5 tiles, so it reads nearly as long as it multiplies,
 //    and a tile's ends (its slots, its results) are alone on their compute unit.  Down: 141 us for 286 MB read
