@@ -491,7 +491,8 @@ int qz_i8_unpack(const int8_t* codes, int64_t rows, int64_t cols, uint8_t* out, 
  *   left alone).  Must not overlap the inputs.
  *   n <= 2^20, d_o <= 2^24, d_i <= 65536; n = 0 or d_o = 0 does nothing.
  *   ws: as many bytes as the query says for the same sizes, 256-byte aligned; 0 bytes: may be null (0
- *   for bad sizes too); calls that may overlap need different workspaces.  Asynchronous.        */
+ *   for bad sizes too, and for every qz_i8_matmul); calls that may overlap need different workspaces.
+ *   Asynchronous.                                                                              */
 size_t qz_i8_matmul_workspace(int64_t n, int64_t d_o, int64_t d_i);
 int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsums, int64_t n,
                  const int8_t* codes, const float* scales, const uint8_t* zeros, int64_t d_o,

@@ -56,23 +56,20 @@ int check_product(const char* who, int64_t n, int64_t d_o, int64_t d_i, const in
   return QZ_OK;
 }
 
-// X quantized, and the product's own workspace.
+// X quantized.
 struct LinearWs {
   int8_t* codes;
   float* scales;
   int32_t* sums;
-  char* product;
-  size_t product_bytes, bytes;
+  size_t bytes;
 };
-LinearWs linear_ws(void* base, int64_t n, int64_t d_o, int64_t d_i) {
+LinearWs linear_ws(void* base, int64_t n, int64_t d_i) {
   Carver c(base);
   LinearWs w{};
   if (i8_by_rows(n, i8_pitch(d_i))) return w;
   w.codes = c.take<int8_t>(static_cast<size_t>(n) * i8_pitch(d_i));
   w.scales = c.take<float>(n);
   w.sums = c.take<int32_t>(n);
-  w.product_bytes = i8_product_ws(n, d_o, i8_pitch(d_i));
-  w.product = c.take<char>(w.product_bytes);
   w.bytes = c.used;
   return w;
 }
@@ -161,20 +158,17 @@ int qz_i8_unpack(const int8_t* codes, int64_t rows, int64_t cols, uint8_t* out, 
   return launch_i8_unpack(codes, rows, cols, out, stream);
 }
 
-size_t qz_i8_matmul_workspace(int64_t n, int64_t d_o, int64_t d_i) {
-  return product_sizes(n, d_o, d_i) ? i8_product_ws(n, d_o, i8_pitch(d_i)) : 0;
-}
+size_t qz_i8_matmul_workspace(int64_t, int64_t, int64_t) { return 0; }   // no kernel of the products has one
 
 int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsums, int64_t n,
                  const int8_t* codes, const float* scales, const uint8_t* zeros, int64_t d_o,
-                 int64_t d_i, const float* bias, void* Y, int32_t yt, int64_t ldy, void* ws,
-                 size_t ws_bytes, hipStream_t stream) {
+                 int64_t d_i, const float* bias, void* Y, int32_t yt, int64_t ldy, void*, size_t,
+                 hipStream_t stream) {
   QZ_TRY(check_product("i8_matmul", n, d_o, d_i, codes, scales, bias, Y, yt, ldy));
   if (n == 0 || d_o == 0) return QZ_OK;
   QZ_TRY(check_codes("i8_matmul", xcodes, xscales));
   if (zeros && !xsums) return fail(QZ_EINVAL, "i8_matmul: zeros need the row sums of X");
   if (!aligned(xsums, 4)) return fail(QZ_EINVAL, "i8_matmul: arrays must be aligned to their elements");
-  QZ_TRY(check_ws("i8_matmul", ws, ws_bytes, i8_product_ws(n, d_o, i8_pitch(d_i))));
   set_error("");
   ScopedTimer tm(K_I8_PRODUCT, stream);
   I8Product p{};
@@ -195,7 +189,7 @@ int qz_i8_matmul(const int8_t* xcodes, const float* xscales, const int32_t* xsum
 }
 
 size_t qz_i8_linear_workspace(int64_t n, int64_t d_o, int64_t d_i) {
-  return product_sizes(n, d_o, d_i) ? linear_ws(nullptr, n, d_o, d_i).bytes : 0;
+  return product_sizes(n, d_o, d_i) ? linear_ws(nullptr, n, d_i).bytes : 0;
 }
 
 int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float* colf,
@@ -209,7 +203,7 @@ int qz_i8_linear(const void* X, int32_t xt, int64_t n, int64_t ldx, const float*
   if (!X) return fail(QZ_EINVAL, "i8_linear: null pointer");
   if (!aligned(X, type_size(xt)) || !aligned(colf, 4))
     return fail(QZ_EINVAL, "i8_linear: arrays must be aligned to their elements");
-  const LinearWs w = linear_ws(ws, n, d_o, d_i);
+  const LinearWs w = linear_ws(ws, n, d_i);
   QZ_TRY(check_ws("i8_linear", ws, ws_bytes, w.bytes));
   set_error("");
   ScopedTimer tm(K_I8_PRODUCT, stream);

@@ -193,7 +193,6 @@ static int launch_few(const I8Product& p, hipStream_t s) {
   return check_launch("i8_few");
 }
 
-#ifndef QZ_NO_ENTRY
 template <Form FORM>
 static int by_kind(I8Kind kind, const I8Product& p, hipStream_t s) {
   switch (kind) {
@@ -209,6 +208,5 @@ static int by_kind(I8Kind kind, const I8Product& p, hipStream_t s) {
 int launch_i8_few(I8Kind kind, int form, const I8Product& p, hipStream_t s) {
   return form == kPlain ? by_kind<kPlain>(kind, p, s) : form == kGateUp ? by_kind<kGateUp>(kind, p, s) : by_kind<kDown>(kind, p, s);
 }
-#endif
 
 }  // namespace qz

@@ -474,11 +474,8 @@ int launch(const I8Product& p, hipStream_t s) {
 
 }  // namespace
 
-#ifndef QZ_NO_ENTRY
-size_t i8_product_ws(int64_t, int64_t, int64_t) { return 0; }
 int launch_i8_product(const I8Product& p, hipStream_t s) { return launch<kPlain>(p, s); }
 int launch_i8_gate_up(const I8Product& p, hipStream_t s) { return launch<kGateUp>(p, s); }
 int launch_i8_down(const I8Product& p, hipStream_t s) { return launch<kDown>(p, s); }
-#endif
 
 }  // namespace qz

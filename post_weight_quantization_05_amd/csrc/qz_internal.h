@@ -328,7 +328,6 @@ struct I8Product {
   const void* raw; int rt; int64_t ldraw, cols; const float* colf;
   const int32_t* ids;
 };
-size_t i8_product_ws(int64_t n, int64_t d_o, int64_t P);
 int launch_i8_product(const I8Product& p, hipStream_t s);
 // h[slot] = silu(gate) up, fp32 [slots x ldy]; rows d_o of W are gate rows, the next d_o up rows
 int launch_i8_gate_up(const I8Product& p, hipStream_t s);
