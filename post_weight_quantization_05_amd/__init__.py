@@ -690,7 +690,7 @@ def qz_i8_matmul(xcodes, xscales, codes, scales, d_i, zeros=None, xsums=None, bi
             raise TypeError("xsums must be int32")
         if xsums.get_device() != index or xsums.shape != (n,) or not xsums.is_contiguous():
             raise ValueError(f"xsums must be {n} contiguous values on GPU {index}")
-    elif zp is not None:
+    elif zp is not None and n and d_o:
         raise ValueError("zeros need xsums, the row sums of X")
     out, ldy, yt = _product_out(out, codes, n, d_o, out_dtype, dev)
     wp, wn, ws = _scratch(ws, L.qz_i8_matmul_workspace(n, d_o, d_i), dev)
