@@ -458,9 +458,9 @@ int qz_mx4_moe(const void* X, int32_t xt, int64_t n, int64_t ldx, int64_t d, int
  *
  * qz_i8_quantize: rows onto this format, symmetric: activations per token, weights per channel.
  *   v = x, or fl32(x colf) with colf [cols] fp32 (nullable; smoothing factors: quantise the weights
- *   with their reciprocals); s = fl32(max |v| fl32(1 / 127));
- *   code = the whole number nearest to v / s, ties
- *   to the even one, within -127 .. 127 (the quotient itself, not its rounding to 32 bits, decides).
+ *   with their reciprocals); s = fl32(max |v| fl32(1 / 127)), as PyTorch divides by 127 on this GPU;
+ *   code = the whole number nearest to v / s, ties to the even one, within -127 .. 127 (the quotient
+ *   itself by the s that is stored, not its rounding to 32 bits, decides).
  *   s = 0 (zero rows) gives zero codes; a row with a NaN or an infinity gets s = NaN and zero codes.
  *   X       [rows x cols], dtype xt, row stride ldx >= cols elements.
  *   sums    nullable: [rows] int32, each row's sum of codes (what zero points are multiplied by).
