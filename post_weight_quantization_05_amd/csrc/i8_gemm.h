@@ -17,8 +17,8 @@ enum Form { kPlain, kGateUp, kDown };
 enum class I8Kind;
 int launch_i8_few(I8Kind kind, int form, const I8Product& p, hipStream_t s);
 
-// An integer sum with its zero point, scales and bias.  shift: the zero point less 128; |xsum| < 2^23, so
-// the product takes the 24-bit multiplier.
+// An integer sum with its zero point, scales and bias.  shift: the zero point less 128; -2^23 <= xsum < 2^23
+// (65536 codes), so the product takes the 24-bit multiplier.
 __device__ __forceinline__ float scaled(int a, int shift, int xsum, float sx, float sw, float bias) {
   return fmaf(static_cast<float>(a - __mul24(shift, xsum)) * sx, sw, bias);
 }

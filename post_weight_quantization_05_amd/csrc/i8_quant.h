@@ -16,8 +16,8 @@ struct RowScale {
 // top: the largest magnitude's bits (magnitudes compare as integers, and a NaN is above every number).
 //
 // s is a product with the rounded 1 / 127, not a quotient: that is what PyTorch makes of max / 127 on this GPU, so
-// whoever quantizes there gets the same scales and codes, bit for bit.  The factor is 2^-28 of itself off, so in
-// 4.5% of the rows s is a last bit off the quotient's rounding; the largest value's quotient stays within 127 (1 +- 2^-23),
+// whoever quantizes there gets the same scales and codes, bit for bit.  The factor is 2^-28 of itself off, and
+// in 4.5% of the rows s is a last bit off the quotient's rounding; the largest value's quotient stays within 127 (1 +- 2^-23),
 // and codes are those of s as it is stored.
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   RowScale c;

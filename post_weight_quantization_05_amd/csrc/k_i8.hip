@@ -13,13 +13,16 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // TPR threads a row, CH chunks of eight elements each, which stay in registers between the row's
 // maximum and its codes: one pass over X.  Rows up to 2048 columns take a wavefront and no barrier, where there
-// are enough of them.
+// are enough of them.  Past 32768 columns (eight chunks of 1024 threads) 128 registers a thread do not hold the row, the
+// next one and the factors: the compiler keeps part of them in scratch, 20 to 152 bytes a thread and with factors 280 to
+// 416 (16 to 20 bytes in fp32 with factors from 16385 columns on), and 2048 x 65536 bf16 takes 125 us (3.2 TB/s),
+// with factors 248, fp32 241 and 361.
 // A workgroup goes through several rows: the next one is on its way while one is worked on, and the
 // column factors are loaded once.
 //
-// Bound by HBM: 8192 x 5120 bf16 with factors and values, 84 MB read and 126 written, 37 us a call in a
+// Bound by HBM: 8192 x 5120 bf16 with factors and values, 84 MB read and 126 written, 38 us a call in a
 // warm loop (5.6 TB/s; torch's copy of 1 GiB reaches 5.1); 25600 x 5120 fp32 with values, 1.18 GB, 206 us
-// (5.7 TB/s).  Few rows are bound by one row's chain, load, maximum, codes: 70 x 200 fp32 2.8 us, 13 x 12288
+// (5.7 TB/s).  Few rows are bound by one row's chain, load, maximum, codes: 70 x 200 fp32 3.0 us, 13 x 12288
 // bf16 4.0, most of it the launch.  Values leave past the caches in whole lines (42 -> 40 us in the former),
 // and the quotients of a code take one multiplication unless they lie next to a half (i8_quant.h).
 //
@@ -149,6 +152,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void i8_quantize_kernel(
   }
 }
 
+// A byte a thread at a time, with its place's division: 4096 x 12288 59 us either way (1.7 TB/s of 101 MB).  They stand
+// between a solver and its product, once a layer.
 __global__ __launch_bounds__(256) void i8_pack_kernel(const uint8_t* __restrict__ in, int64_t rows,
                                                       int64_t cols, int8_t* __restrict__ out) {
   const int64_t P = i8_pitch(cols);

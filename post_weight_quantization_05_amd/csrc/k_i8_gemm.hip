@@ -13,7 +13,7 @@
 // stage are read ahead.
 //
 // What bounds it, measured:
-//  - 8192 x 5120 -> 25600, 256 x 256: 905 to 960 us, 2.24 to 2.37 POP/s, matrix cores busy for 64% of the
+//  - 8192 x 5120 -> 25600, 256 x 256: 905 to 950 us, 2.26 to 2.37 POP/s, matrix cores busy for 64% of the
 //    cycles at 1.74 GHz of 2.4: the power limit (on zeros, which draw less, 729 us at 2.4 GHz).  The
 //    library's product of the same codes, without scales: 1025 to 1044 us.
 //  - 2048 x 4096 -> 4096, 256 x 128: 36.5 us, busy for 40%: one tile a compute unit, so the first stages
@@ -22,7 +22,7 @@
 //    bound by its own stream from memory into LDS; the library's 31 us.  64 x 64, four resident, would take 20.5 (the
 //    choice's times err there, i8_plan.h).  Splitting the contraction, with the join in a second launch, lost at
 //    every size.
-//  - Expert layer, 4096 tokens 6 of 64, 2048 -> 2 x 1408: 200 us for 559 MB read and 138 written, busy for 34%:
+//  - Expert layer, 4096 tokens 6 of 64, 2048 -> 2 x 1408: 206 us for 557 MB read and 138 written, busy for 33%:
 //    384 tokens an expert use its weights for 1.5 tiles, so it reads nearly as long as it multiplies,
 //    and a tile's ends (its slots, its results) are alone on their compute unit.  Down: 141 us for 286 MB read
 //    and 201 written, busy for 23%.

@@ -84,9 +84,9 @@ __device__ __forceinline__ double softmax64(double x, double top) {   // before 
 //
 // Scores and choices are held in 64 bits, so that two experts change places only where their choices
 // differ by less than a score's last bits.  Bound by that arithmetic (an exponential and a quotient an
-// expert) and by the chain of top_k maxima, whose latency other wavefronts of the SIMD cover: 8192 tokens,
-// 256 experts in 8 groups, fp32, 14 us, where the logits' 8.4 MB alone would take 1.7; one token of 128, 5.3
-// us, nearly all launch and latency.
+// expert) and by the chain of top_k maxima with a lane's choices looked through after each, of which two wavefronts a
+// SIMD (8192 tokens) cover little: 8192 tokens, 256 experts in 8 groups, fp32, 14 us, where the logits' 8.4 MB alone
+// would take 1.7; one token of 128, 5.1 us: the launch, and one wavefront's chain of that arithmetic.
 template <int LT, int PER>
 __global__ __launch_bounds__(kRouteTokens<PER> * kLanes) void route_kernel(const void* __restrict__ logits, int64_t n,
                                                     int64_t ldl, qz_router p, int vec,
