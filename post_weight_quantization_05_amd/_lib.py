@@ -173,6 +173,6 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
-    binding = _native_calls(lib)
     _lib = lib
+    binding = _native_calls(lib)
     return lib

@@ -70,6 +70,29 @@ else:
         (package / "_binding.so").write_bytes(held)
 
 
+def test_warnings_as_errors(package):
+    """The one warning is raised; the library is there all the same."""
+    held = (package / "_binding.so").read_bytes()
+    (package / "_binding.so").write_bytes(b"not a library")
+    try:
+        r = subprocess.run([sys.executable, "-c", f"""
+import warnings
+import torch
+import {NAME} as q
+warnings.simplefilter("error")
+try:
+    q.lib()
+except RuntimeWarning as e:
+    assert "_binding.so" in str(e)
+else:
+    raise AssertionError
+assert q.qz_i8_pitch(129) == 256
+"""], cwd=package.parent, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr
+    finally:
+        (package / "_binding.so").write_bytes(held)
+
+
 def test_native_calls_of_another_abi_version(package):
     _run(package, f"""
 from {NAME} import _binding
